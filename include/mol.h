@@ -75,7 +75,8 @@ MOL_API const char *mol_status_string(mol_status status);
 
 /* (host) ABI version of this header, 7 (2 added the per-slot ranks, 3 the combine, 4 the
  * base grouped GEMM with the fused delta, 5 the allocation-free stage delta, 6 the work
- * plan, 7 the plan as runs of blocks only, read by the expand). */
+ * plan, 7 the plan as runs of blocks only, read by the expand). Entry points that leave the
+ * earlier ones as they are (mol_router_topk) come within a version. */
 MOL_API int32_t mol_abi_version(void);
 
 /* ---------------------------------------------------------------------------------
@@ -341,6 +342,37 @@ MOL_API mol_status mol_lora_expand_combine(int32_t dtype, const float *s, int32_
                                            int32_t num_experts, int32_t num_slots,
                                            const void *base, int64_t ld_base, void *y,
                                            int64_t ld_y, void *stream);
+
+/* ---------------------------------------------------------------------------------
+ * mol_router_topk - from router logits to the top-k experts of each token and their weights:
+ * the topk_ids and topk_weights that the calls above take.
+ *   logits        [M, ld_logits] (dtype), one row of num_experts logits per token
+ *   Candidates of a row are its logits that are neither NaN nor -infinity (an expert is
+ *   masked by either). Slot j gets the candidate with the j-th largest logit, equal logits in
+ *   ascending expert order; slots past the last candidate get id -1 and weight 0.
+ *   scoring       MOL_SCORE_SOFTMAX: score = exp(l - max) / sum over the candidates of exp(l - max)
+ *                 (rows that hold +infinity share 1 among those entries);
+ *                 MOL_SCORE_SIGMOID: score = 1 / (1 + exp(-l))
+ *   renormalize   nonzero: each score is divided by the sum of the row's selected scores
+ *   scale         finite factor on the weights, applied last
+ *   first_expert, num_local
+ *                 the experts this GPU holds: a selected expert e gets id e - first_expert
+ *                 inside [first_expert, first_expert + num_local), else id -1 and weight 0 (the
+ *                 expert-parallel sentinel of the calls above). 0 and num_experts for all.
+ *                 Selection, scores and renormalization are over all num_experts.
+ *   topk_ids      int32 [M, topk] out;  topk_weights  float32 [M, topk] out
+ * Scores and sums are fp32. logits is aligned to its element, at any row stride >= num_experts.
+ * Errors: MOL_E_ARG, MOL_E_DTYPE, MOL_E_ALIGN, MOL_E_LIMIT (num_experts + 1 > MOL_MAX_BUCKETS,
+ * topk > MOL_MAX_ROUTER_TOPK, M * topk past 32 bits). M = 0 is a no-op.
+ * ------------------------------------------------------------------------------- */
+enum { MOL_SCORE_SOFTMAX = 0, MOL_SCORE_SIGMOID = 1 };
+#define MOL_MAX_ROUTER_TOPK 64
+
+MOL_API mol_status mol_router_topk(int32_t dtype, const void *logits, int64_t ld_logits,
+                                   int32_t M, int32_t num_experts, int32_t topk,
+                                   int32_t scoring, int32_t renormalize, float scale,
+                                   int32_t first_expert, int32_t num_local, int32_t *topk_ids,
+                                   float *topk_weights, void *stream);
 
 #ifdef __cplusplus
 }

@@ -20,9 +20,12 @@ LIB_PATH = os.environ.get("MOL_LIBRARY") or os.path.join(_PKG, "libmol.so")
 MOL_OK, MOL_E_ARG, MOL_E_LIMIT, MOL_E_DTYPE, MOL_E_ALIGN, MOL_E_WORKSPACE, MOL_E_HIP = range(7)
 MOL_F32, MOL_BF16 = 0, 1
 MOL_MAX_BUCKETS = 8192
+MOL_SCORE_SOFTMAX, MOL_SCORE_SIGMOID = 0, 1
+MOL_MAX_ROUTER_TOPK = 64
 
 # every symbol include/mol.h declares, with (restype, argtypes)
 _P, _I32, _I64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+_F32 = ctypes.c_float
 SIGNATURES = {
     "mol_status_string": (ctypes.c_char_p, [_I32]),
     "mol_abi_version": (_I32, []),
@@ -47,6 +50,8 @@ SIGNATURES = {
     "mol_moe_combine": (_I32, [_I32, _P, _I64, _P, _P, _I32, _I32, _I32, _I32, _P, _I64, _P]),
     "mol_lora_expand_combine": (_I32, [_I32, _P, _I32, _P, _I32, _P, _P, _P, _P, _P, _I32,
                                        _I32, _I32, _I32, _P, _I64, _P, _I64, _P]),
+    "mol_router_topk": (_I32, [_I32, _P, _I64, _I32, _I32, _I32, _I32, _I32, _F32, _I32, _I32,
+                               _P, _P, _P]),
 }
 
 
@@ -356,3 +361,44 @@ def mol_moe_gemm(xin, row_div: int, W, sorted_ids, expert_ids, num_post_padded, 
         _ptr(s), R, slices, _ptr(B), _ptr(slot_scale), _ranks(slot_ranks), _ptr(lora_ids), topk,
         num_slots, _stream(W)))
     return out
+
+
+def _on(dev, name: str, t: torch.Tensor, dtype, shape):
+    """t is on dev, contiguous, of this dtype and shape."""
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    _need(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _call(dev, fn: str, *args) -> None:
+    """The entry point on dev's current stream, with dev current for the launch."""
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        _check(fn, getattr(lib(), fn)(*args, torch.cuda.current_stream(dev).cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn, getattr(lib(), fn)(*args, torch.cuda.current_stream(dev).cuda_stream))
+
+
+def mol_router_topk(logits, topk: int, scoring: int = MOL_SCORE_SOFTMAX,
+                    renormalize: bool = True, scale: float = 1.0, first_expert: int = 0,
+                    num_local: int = None, topk_ids=None, topk_weights=None):
+    """The top-k experts of each token from router logits [M, E] (rows may be strided):
+    (topk_ids int32 [M, topk], topk_weights float32 [M, topk])."""
+    _need(logits, "logits", contiguous=False)
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be 2-d with contiguous rows")
+    M, E = logits.shape
+    dev = logits.device
+    if topk_ids is None:
+        topk_ids = torch.empty((M, topk), dtype=torch.int32, device=dev)
+    if topk_weights is None:
+        topk_weights = torch.empty((M, topk), dtype=torch.float32, device=dev)
+    _on(dev, "topk_ids", topk_ids, torch.int32, (M, topk))
+    _on(dev, "topk_weights", topk_weights, torch.float32, (M, topk))
+    _call(dev, "mol_router_topk", _dtype_code(logits), logits.data_ptr(),
+          max(logits.stride(0), E) if M <= 1 else logits.stride(0), M, E, topk, scoring,
+          1 if renormalize else 0, scale, first_expert, E if num_local is None else num_local,
+          topk_ids.data_ptr(), topk_weights.data_ptr())
+    return topk_ids, topk_weights

@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <limits>
 #include <mutex>
 
@@ -657,6 +658,46 @@ MOL_API mol_status mol_lora_expand_combine(int32_t dtype, const float* s, int32_
   a.y = y;
   a.ld_y = ld_y;
   return hip_status(mol::launch_expand_combine(a, bf16, (hipStream_t)stream));
+}
+
+// ---- router ------------------------------------------------------------------------
+
+MOL_API mol_status mol_router_topk(int32_t dtype, const void* logits, int64_t ld_logits,
+                                   int32_t M, int32_t num_experts, int32_t topk,
+                                   int32_t scoring, int32_t renormalize, float scale,
+                                   int32_t first_expert, int32_t num_local, int32_t* topk_ids,
+                                   float* topk_weights, void* stream) {
+  if (dtype != MOL_F32 && dtype != MOL_BF16) return MOL_E_DTYPE;
+  if (M < 0 || num_experts < 1 || topk < 1 || ld_logits < num_experts) return MOL_E_ARG;
+  if (scoring != MOL_SCORE_SOFTMAX && scoring != MOL_SCORE_SIGMOID) return MOL_E_ARG;
+  if (!std::isfinite(scale) || first_expert < 0 || num_local < 1 ||
+      (int64_t)first_expert + num_local > num_experts)
+    return MOL_E_ARG;
+  if ((int64_t)num_experts + 1 > MOL_MAX_BUCKETS || topk > MOL_MAX_ROUTER_TOPK ||
+      (int64_t)M * topk > kI32Max)
+    return MOL_E_LIMIT;
+  if (M == 0) return MOL_OK;
+  if (!logits || !topk_ids || !topk_weights) return MOL_E_ARG;
+  const bool bf16 = dtype == MOL_BF16;
+  const int esz = bf16 ? 2 : 4;
+  if (reinterpret_cast<uintptr_t>(logits) % esz || reinterpret_cast<uintptr_t>(topk_ids) % 4 ||
+      reinterpret_cast<uintptr_t>(topk_weights) % 4)
+    return MOL_E_ALIGN;
+  mol::RouterArgs a{};
+  a.logits = logits;
+  a.ld = ld_logits;
+  a.M = M;
+  a.E = num_experts;
+  a.topk = topk;
+  a.sigmoid = scoring == MOL_SCORE_SIGMOID;
+  a.renorm = renormalize != 0;
+  a.vec = aligned16(logits) && (ld_logits * esz) % 16 == 0;
+  a.scale = scale;
+  a.first = first_expert;
+  a.local = num_local;
+  a.ids = topk_ids;
+  a.weights = topk_weights;
+  return hip_status(mol::launch_router(a, bf16, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -182,6 +182,23 @@ struct GemmArgs {
   int32_t S;
 };
 
+// The router: top-k experts of each token from its logits.
+struct RouterArgs {
+  const void* logits;      // [M, E], ld apart
+  int64_t ld;
+  int32_t M;
+  int32_t E;
+  int32_t topk;
+  bool sigmoid;            // scores: sigmoid instead of softmax
+  bool renorm;
+  bool vec;                // rows start on 16-byte boundaries: vector loads
+  float scale;
+  int32_t first;           // local experts: [first, first + local)
+  int32_t local;
+  int32_t* ids;            // [M, topk]
+  float* weights;          // [M, topk]
+};
+
 // host-side launchers (return the launch status)
 hipError_t launch_virtual_topk(const int32_t* topk_ids, const int32_t* lora_ids, int32_t M,
                                int32_t topk, int32_t E, int32_t S, int32_t* out,
@@ -215,5 +232,6 @@ hipError_t launch_combine(const CombineArgs& a, bool bf16, hipStream_t stream);
 // fused expand + combine: ranks it is built for (R/8 or R/4 a power of two up to 16)
 bool fused_rank_supported(int32_t R, bool bf16);
 hipError_t launch_expand_combine(const CombineArgs& a, bool bf16, hipStream_t stream);
+hipError_t launch_router(const RouterArgs& a, bool bf16, hipStream_t stream);
 
 }  // namespace mol

@@ -76,7 +76,7 @@ MOL_API const char *mol_status_string(mol_status status);
 /* (host) ABI version of this header, 7 (2 added the per-slot ranks, 3 the combine, 4 the
  * base grouped GEMM with the fused delta, 5 the allocation-free stage delta, 6 the work
  * plan, 7 the plan as runs of blocks only, read by the expand). Entry points that leave the
- * earlier ones as they are (mol_router_topk) come within a version. */
+ * earlier ones as they are (mol_router_topk, mol_moe_gemm_q4, mol_moe_layer) come within a version. */
 MOL_API int32_t mol_abi_version(void);
 
 /* ---------------------------------------------------------------------------------
@@ -373,6 +373,108 @@ MOL_API mol_status mol_router_topk(int32_t dtype, const void *logits, int64_t ld
                                    int32_t scoring, int32_t renormalize, float scale,
                                    int32_t first_expert, int32_t num_local, int32_t *topk_ids,
                                    float *topk_weights, void *stream);
+
+/* ---------------------------------------------------------------------------------
+ * 4-bit weights. A matrix of N rows of K weights is stored as uint8 [N, K / 2], two per byte:
+ * byte b of a row holds k = 2b in its low half and k = 2b + 1 in its high half, each an
+ * unsigned q in 0..15. Every group of G (32, 64 or 128) consecutive k's of a row has a scale and
+ * optionally a zero point: weight = (q - z) * scale. scales [N, K / G] has the dtype of the
+ * input rows; zeros uint8 [N, K / G] holds any value 0..255, NULL means 8 throughout.
+ * K is a multiple of G, of at most 256 groups.
+ *
+ * mol_moe_gemm_q4 - mol_moe_gemm's base product over such weights:
+ *   out[p, n] = round( sum_k (q[t,n,k] - z[t,n,k/G]) * scale[t,n,k/G] * xin[p / row_div, k] )
+ * for every pair p with a local base expert t in [0, E); other rows are untouched. Summed in
+ * fp32, the scale applied to a group's sum, rounded once. num_experts = 1 and ids of zero give the
+ * product with a single matrix.
+ *   dtype         MOL_F32 or MOL_BF16: xin, scales and out
+ *   W             uint8 [E, N, K / 2], 16-byte aligned;  scales [E, N, K / group], aligned to
+ *                 its element;  zeros uint8 [E, N, K / group] or NULL
+ *   others        as for mol_moe_gemm (rows of xin on 16-byte boundaries)
+ * Built for decode-sized batches; blocks of any block_m are taken.
+ * Errors: MOL_E_ARG (a group that is not 32, 64 or 128, K not a multiple of it), MOL_E_LIMIT
+ * (more than 256 groups a row, one expert's weights 2 GiB or more), others as for mol_moe_gemm.
+ * ------------------------------------------------------------------------------- */
+MOL_API mol_status mol_moe_gemm_q4(int32_t dtype, const void *xin, int64_t ld_x, int32_t row_div,
+                                   const uint8_t *W, const void *scales, const uint8_t *zeros,
+                                   int32_t group, int32_t K, int32_t N, int32_t num_experts,
+                                   const int32_t *sorted_ids, const int32_t *expert_ids,
+                                   const int32_t *num_post_padded, int32_t numel,
+                                   int32_t block_m, void *out, int64_t ld_out, void *stream);
+
+/* ---------------------------------------------------------------------------------
+ * mol_moe_layer - a whole layer for a few tokens, from the routed ids to the combined rows, with
+ * no aligned routing: two launches up to 32 tokens (gate/up with the activation, down with
+ * the combine), the combine as a third beyond; with adapters, a rank product more before each
+ * of the two. For pair p = m * topk + k with a local base expert t = topk_ids[m, k] in [0, E),
+ * and l = lora_ids[m] (the adapter terms only for l in [0, S) and slot rank rl > 0, v = t + l * E):
+ *   g    = gate_up[t, 0:I] x_m + slot_scale[l] * gate_up_B[v, 0:I, :rl] (gate_up_A[v, 0:rl] x_m)
+ *   u    = gate_up[t, I:2I] x_m + slot_scale[l] * gate_up_B[v, I:2I, :rl] (gate_up_A[v, r:r+rl] x_m)
+ *   h_p  = round( g / (1 + exp(-g)) * u )
+ *   y_m  = round( sum_k topk_weights[m, k] * (down[t] h_p
+ *                  + slot_scale[l] * down_B[v, :, :rl] (down_A[v, 0:rl] h_p)) )
+ * Pairs without a local expert contribute nothing; a token that has none gets a row of
+ * zeros. Sums are fp32; h and y alone are rounded (bf16: to nearest even).
+ *   w             (host) the weights; read during the call only. dtype: MOL_F32 or MOL_BF16 of x,
+ *                 y, the scales, the adapters, and of the weights themselves when group is 0.
+ *                 gate_up [E, 2 * inter, hidden] (gate rows first), down [E, hidden, inter],
+ *                 16-byte aligned. group 32, 64 or 128: 4-bit weights (above) with their
+ *                 scales and zero points (zeros may be NULL); group 0: no scales, no zeros.
+ *   adapters      (host) the adapters of S = num_slots slots, or NULL for none (lora_ids is
+ *                 then NULL): gate_up_A [E*S, 2 rank, hidden], gate_up_B [E*S, 2 inter, rank],
+ *                 down_A [E*S, rank, inter], down_B [E*S, hidden, rank], 16-byte aligned;
+ *                 slot_scale float32 [S]; slot_ranks int32 [S] or NULL (clamped to [0, rank]; the
+ *                 weights past a slot's rank are never read)
+ *   x             [M, ld_x], 16-byte aligned rows;  y [M, ld_y] out, aligned to its element.
+ *                 y may not overlap x.
+ *   topk_ids int32 [M, topk], topk_weights float32 [M, topk], lora_ids int32 [M] or NULL
+ *   workspace     device scratch of mol_moe_layer_workspace_bytes(), 16-byte aligned; needs no
+ *                 initial contents. Calls that may overlap must not share a workspace.
+ * Requires hidden, inter, ld_x and rank to be multiples of 16 bytes' worth of elements (8
+ * bf16, 4 fp32), with 4-bit weights hidden and inter multiples of group.
+ * Errors: MOL_E_ARG, MOL_E_DTYPE, MOL_E_ALIGN, MOL_E_WORKSPACE, MOL_E_LIMIT (M * topk >
+ * MOL_LAYER_MAX_PAIRS, topk > MOL_LAYER_MAX_TOPK, E * S + 1 > MOL_MAX_BUCKETS, rank over
+ * MOL_MAX_RANK_BYTES, one expert's matrix 2 GiB or more). M = 0 is a no-op.
+ * For more tokens: mol_align_block_size, mol_moe_gemm or mol_moe_gemm_q4, mol_lora_delta and
+ * mol_moe_combine.
+ * ------------------------------------------------------------------------------- */
+#define MOL_LAYER_MAX_PAIRS 4096
+#define MOL_LAYER_MAX_TOPK 64
+
+typedef struct mol_moe_weights {
+    int32_t dtype;
+    int32_t group; /* 0: dense; 32, 64 or 128: 4-bit weights with group scales */
+    int32_t num_experts;
+    int32_t hidden;
+    int32_t inter;
+    int32_t reserved;
+    const void *gate_up;
+    const void *down;
+    const void *gate_up_scales;
+    const void *down_scales;
+    const uint8_t *gate_up_zeros;
+    const uint8_t *down_zeros;
+} mol_moe_weights;
+
+typedef struct mol_moe_adapters {
+    int32_t num_slots;
+    int32_t rank;
+    const void *gate_up_A;
+    const void *gate_up_B;
+    const void *down_A;
+    const void *down_B;
+    const float *slot_scale;
+    const int32_t *slot_ranks;
+} mol_moe_adapters;
+
+/* bytes of a layer's workspace (rank 0: no adapters), or -mol_status */
+MOL_API int64_t mol_moe_layer_workspace_bytes(int32_t dtype, int32_t M, int32_t topk,
+                                              int32_t hidden, int32_t inter, int32_t rank);
+MOL_API mol_status mol_moe_layer(const mol_moe_weights *w, const mol_moe_adapters *adapters,
+                                 const void *x, int64_t ld_x, const int32_t *topk_ids,
+                                 const float *topk_weights, const int32_t *lora_ids, int32_t M,
+                                 int32_t topk, void *y, int64_t ld_y, void *workspace,
+                                 size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -52,6 +52,10 @@ SIGNATURES = {
                                        _I32, _I32, _I32, _P, _I64, _P, _I64, _P]),
     "mol_router_topk": (_I32, [_I32, _P, _I64, _I32, _I32, _I32, _I32, _I32, _F32, _I32, _I32,
                                _P, _P, _P]),
+    "mol_moe_gemm_q4": (_I32, [_I32, _P, _I64, _I32, _P, _P, _P, _I32, _I32, _I32, _I32, _P, _P,
+                               _P, _I32, _I32, _P, _I64, _P]),
+    "mol_moe_layer_workspace_bytes": (_I64, [_I32, _I32, _I32, _I32, _I32, _I32]),
+    "mol_moe_layer": (_I32, [_P, _P, _P, _I64, _P, _P, _P, _I32, _I32, _P, _I64, _P, _SZ, _P]),
 }
 
 
@@ -402,3 +406,179 @@ def mol_router_topk(logits, topk: int, scoring: int = MOL_SCORE_SOFTMAX,
           1 if renormalize else 0, scale, first_expert, E if num_local is None else num_local,
           topk_ids.data_ptr(), topk_weights.data_ptr())
     return topk_ids, topk_weights
+
+
+def _rows(t: torch.Tensor, name: str, dev, dtype, shape) -> int:
+    """t is on dev, 2-d with contiguous rows, of this dtype and shape; its row stride."""
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    _need(t, name, dtype, contiguous=False)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+
+
+def _q4(W, scales, zeros, name: str, dev):
+    """(N, K, group) of packed 4-bit weights [E, N, K/2] with scales (and zeros) [E, N, K/G]."""
+    if W.dim() != 3 or scales.dim() != 3 or scales.shape[2] < 1:
+        raise ValueError(f"{name} must be [E, N, K/2] with scales [E, N, K/group]")
+    E, N, half = W.shape
+    _on(dev, name, W, torch.uint8, (E, N, half))
+    _on(dev, name + " scales", scales, scales.dtype, (E, N, scales.shape[2]))
+    if zeros is not None:
+        _on(dev, name + " zeros", zeros, torch.uint8, scales.shape)
+    if 2 * half % scales.shape[2]:
+        raise ValueError(f"{name}: {2 * half} columns are not whole groups of {scales.shape[2]}")
+    return N, 2 * half, 2 * half // scales.shape[2]
+
+
+def mol_moe_gemm_q4(xin, row_div: int, W, scales, sorted_ids, expert_ids, num_post_padded,
+                    numel: int, block_m: int, out, zeros=None):
+    """The base grouped GEMM of a stage into out [numel, N] over 4-bit weights W uint8
+    [E, N, K/2] with scales [E, N, K/group] (routing by base expert)."""
+    dev = W.device
+    N, K, group = _q4(W, scales, zeros, "W", dev)
+    E = W.shape[0]
+    dtype = scales.dtype
+    ld_x = _rows(xin, "xin", dev, dtype, (xin.shape[0], K))
+    if xin.shape[0] * row_div < numel:
+        raise ValueError(f"xin has {xin.shape[0]} rows: {numel} pairs need "
+                         f"{-(-numel // row_div)}")
+    ld_out = _rows(out, "out", dev, dtype, (numel, N))
+    blocks = mol_align_max_blocks(numel, E, block_m)
+    for t, name, least in ((sorted_ids, "sorted_ids", blocks * block_m),
+                           (expert_ids, "expert_ids", blocks),
+                           (num_post_padded, "num_post_padded", 1)):
+        _on(dev, name, t, torch.int32, t.shape)
+        if t.numel() < least:
+            raise ValueError(f"{name} has {t.numel()} entries, fewer than the routing's {least}")
+    _call(dev, "mol_moe_gemm_q4", _dtype_code(scales), xin.data_ptr(), ld_x, row_div,
+          W.data_ptr(), scales.data_ptr(), _ptr(zeros), group, K, N, E, sorted_ids.data_ptr(),
+          expert_ids.data_ptr(), num_post_padded.data_ptr(), numel, block_m, out.data_ptr(),
+          ld_out)
+    return out
+
+
+class _MoeWeightsC(ctypes.Structure):
+    _fields_ = ([(n, _I32) for n in ("dtype", "group", "num_experts", "hidden", "inter",
+                                     "reserved")] +
+                [(n, _P) for n in ("gate_up", "down", "gate_up_scales", "down_scales",
+                                   "gate_up_zeros", "down_zeros")])
+
+
+class _MoeAdaptersC(ctypes.Structure):
+    _fields_ = ([(n, _I32) for n in ("num_slots", "rank")] +
+                [(n, _P) for n in ("gate_up_A", "gate_up_B", "down_A", "down_B", "slot_scale",
+                                   "slot_ranks")])
+
+
+class MoeWeights:
+    """The base weights of a layer as mol_moe_layer takes them, described once: gate_up [E,
+    2*inter, hidden] and down [E, hidden, inter] (bf16 or fp32), or packed 4-bit (uint8, last
+    dimension halved) with scales and, optionally, zeros. Keeps the tensors alive."""
+
+    def __init__(self, gate_up, down, gate_up_scales=None, down_scales=None,
+                 gate_up_zeros=None, down_zeros=None):
+        dev = gate_up.device
+        q4 = gate_up_scales is not None or down_scales is not None
+        if gate_up.dim() != 3 or down.dim() != 3:
+            raise ValueError("gate_up and down must be 3-d")
+        E, N1, _ = gate_up.shape
+        if q4:
+            if gate_up_scales is None or down_scales is None:
+                raise ValueError("4-bit weights need both scales")
+            N1, H, group = _q4(gate_up, gate_up_scales, gate_up_zeros, "gate_up", dev)
+            N2, inter, g2 = _q4(down, down_scales, down_zeros, "down", dev)
+            if g2 != group or down_scales.dtype != gate_up_scales.dtype:
+                raise ValueError("gate_up and down must have one group size and scale dtype")
+            self.dtype = gate_up_scales.dtype
+        else:
+            if gate_up_zeros is not None or down_zeros is not None:
+                raise ValueError("zeros without scales")
+            H, group = gate_up.shape[2], 0
+            N2, inter = down.shape[1], down.shape[2]
+            self.dtype = gate_up.dtype
+            _on(dev, "gate_up", gate_up, self.dtype, (E, N1, H))
+            _on(dev, "down", down, self.dtype, (E, N2, inter))
+        if N1 != 2 * inter or N2 != H or down.shape[0] != E:
+            raise ValueError(f"gate_up {tuple(gate_up.shape)} and down {tuple(down.shape)} are "
+                             "not one layer's")
+        self.device, self.num_experts, self.hidden, self.inter = dev, E, H, inter
+        self.tensors = (gate_up, down, gate_up_scales, down_scales, gate_up_zeros, down_zeros)
+        self.c = _MoeWeightsC(_dtype_code(gate_up_scales if q4 else gate_up), group, E, H, inter,
+                              0, *(None if t is None else t.data_ptr() for t in self.tensors))
+
+
+class MoeAdapters:
+    """The adapters of a layer as mol_moe_layer takes them: gate_up_A [E*S, 2r, hidden],
+    gate_up_B [E*S, 2*inter, r], down_A [E*S, r, inter], down_B [E*S, hidden, r], slot_scale
+    [S], slot_ranks [S] or None. Keeps the tensors alive."""
+
+    def __init__(self, gate_up_A, gate_up_B, down_A, down_B, slot_scale, slot_ranks=None):
+        dev, dt = gate_up_A.device, gate_up_A.dtype
+        _dtype_code(gate_up_A)
+        S = slot_scale.shape[0]
+        V, r2, H = gate_up_A.shape
+        r, inter = r2 // 2, down_A.shape[2]
+        if S < 1 or V % S:
+            raise ValueError(f"{V} virtual experts are not a multiple of {S} slots")
+        for t, name, shape in ((gate_up_A, "gate_up_A", (V, 2 * r, H)),
+                               (gate_up_B, "gate_up_B", (V, 2 * inter, r)),
+                               (down_A, "down_A", (V, r, inter)), (down_B, "down_B", (V, H, r))):
+            _on(dev, name, t, dt, shape)
+        _on(dev, "slot_scale", slot_scale, torch.float32, (S,))
+        if slot_ranks is not None:
+            _on(dev, "slot_ranks", slot_ranks, torch.int32, (S,))
+        self.device, self.dtype, self.num_slots, self.rank = dev, dt, S, r
+        self.num_virtual, self.hidden, self.inter = V, H, inter
+        self.tensors = (gate_up_A, gate_up_B, down_A, down_B, slot_scale, slot_ranks)
+        self.c = _MoeAdaptersC(S, r, *(None if t is None else t.data_ptr()
+                                       for t in self.tensors))
+
+
+def mol_moe_layer_workspace_bytes(w: MoeWeights, M: int, topk: int, adapters=None) -> int:
+    v = lib().mol_moe_layer_workspace_bytes(w.c.dtype, M, topk, w.hidden, w.inter,
+                                            0 if adapters is None else adapters.rank)
+    if v < 0:
+        raise MolError("mol_moe_layer_workspace_bytes", -v)
+    return int(v)
+
+
+def new_moe_layer_workspace(w: MoeWeights, M: int, topk: int, adapters=None):
+    """A workspace for mol_moe_layer at up to M tokens (its contents need no initialisation)."""
+    n = mol_moe_layer_workspace_bytes(w, M, topk, adapters)
+    return torch.empty(max(256, n), dtype=torch.uint8, device=w.device)
+
+
+def mol_moe_layer(w: MoeWeights, x, topk_ids, topk_weights, adapters=None, lora_ids=None,
+                  y=None, workspace=None):
+    """A whole layer for a few tokens: y [M, hidden] from x [M, hidden] and its routing."""
+    dev = w.device
+    M, topk = topk_ids.shape
+    ld_x = _rows(x, "x", dev, w.dtype, (M, w.hidden))
+    _on(dev, "topk_ids", topk_ids, torch.int32, (M, topk))
+    _on(dev, "topk_weights", topk_weights, torch.float32, (M, topk))
+    if adapters is not None:
+        if (adapters.dtype != w.dtype or adapters.device != dev or adapters.hidden != w.hidden or
+                adapters.inter != w.inter or
+                adapters.num_virtual != w.num_experts * adapters.num_slots):
+            raise ValueError("the adapters are not for these weights")
+        if lora_ids is None:
+            raise ValueError("adapters need lora_ids")
+        _on(dev, "lora_ids", lora_ids, torch.int32, (M,))
+    elif lora_ids is not None:
+        raise ValueError("lora_ids without adapters")
+    if y is None:
+        y = torch.empty((M, w.hidden), dtype=w.dtype, device=dev)
+    ld_y = _rows(y, "y", dev, w.dtype, (M, w.hidden))
+    if workspace is None:
+        workspace = new_moe_layer_workspace(w, M, topk, adapters)
+    _on(dev, "workspace", workspace, torch.uint8, workspace.shape)
+    _call(dev, "mol_moe_layer", ctypes.addressof(w.c),
+          None if adapters is None else ctypes.addressof(adapters.c), x.data_ptr(), ld_x,
+          topk_ids.data_ptr(), topk_weights.data_ptr(),
+          None if lora_ids is None else lora_ids.data_ptr(), M, topk, y.data_ptr(), ld_y,
+          workspace.data_ptr(), workspace.numel())
+    return y

@@ -130,6 +130,36 @@ mol::DeltaArgs make_delta_args(const void* xin, int64_t ld_x, int32_t row_div, c
   return a;
 }
 
+bool aligned_to(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+// A row of 4-bit weights: K elements in groups, N such rows in one expert's matrix.
+mol_status q4_check(int32_t K, int32_t group, int64_t N) {
+  if (group != 32 && group != 64 && group != 128) return MOL_E_ARG;
+  if (K < 1 || K % group) return MOL_E_ARG;
+  if (K / group > mol::kMaxQ4Groups) return MOL_E_LIMIT;
+  if (N * (K / 2) >= (int64_t(1) << 31)) return MOL_E_LIMIT;  // one expert's weights
+  return MOL_OK;
+}
+
+static_assert(MOL_LAYER_MAX_PAIRS == mol::kLayerMaxPairs && MOL_LAYER_MAX_TOPK == mol::kLayerMaxTopk,
+              "the layer's limits");
+
+// Whether the layer's down stage runs per token, with the combine in it.
+bool layer_direct(int32_t M) { return M <= 32; }
+
+// The layer's scratch: byte offsets of z, s1 and s2 (h is first) and the total.
+struct LayerWorkspace {
+  int64_t z, s1, s2, bytes;
+};
+LayerWorkspace layer_workspace(int64_t numel, int32_t M, int32_t H, int32_t I, int32_t r, int esz) {
+  LayerWorkspace w;
+  w.z = round256(numel * I * esz);
+  w.s1 = w.z + (layer_direct(M) ? 0 : round256(numel * H * 4));
+  w.s2 = w.s1 + round256(numel * 2 * r * 4);
+  w.bytes = w.s2 + round256(numel * r * 4);
+  return w;
+}
+
 }  // namespace
 
 extern "C" {
@@ -698,6 +728,193 @@ MOL_API mol_status mol_router_topk(int32_t dtype, const void* logits, int64_t ld
   a.ids = topk_ids;
   a.weights = topk_weights;
   return hip_status(mol::launch_router(a, bf16, (hipStream_t)stream));
+}
+
+// ---- 4-bit weights -------------------------------------------------------------------
+
+MOL_API mol_status mol_moe_gemm_q4(int32_t dtype, const void* xin, int64_t ld_x, int32_t row_div,
+                                   const uint8_t* W, const void* scales, const uint8_t* zeros,
+                                   int32_t group, int32_t K, int32_t N, int32_t num_experts,
+                                   const int32_t* sorted_ids, const int32_t* expert_ids,
+                                   const int32_t* num_post_padded, int32_t numel,
+                                   int32_t block_m, void* out, int64_t ld_out, void* stream) {
+  const StageCheck rc =
+      routing_check(sorted_ids, expert_ids, num_post_padded, numel, num_experts, block_m);
+  if (rc.st != MOL_OK) return rc.st;
+  if (dtype != MOL_F32 && dtype != MOL_BF16) return MOL_E_DTYPE;
+  if (N < 1 || row_div < 1 || ld_x < K || ld_out < N) return MOL_E_ARG;
+  const mol_status qc = q4_check(K, group, N);
+  if (qc != MOL_OK) return qc;
+  if (numel == 0) return MOL_OK;
+  if (!xin || !W || !scales || !out) return MOL_E_ARG;
+  const bool bf16 = dtype == MOL_BF16;
+  const int esz = bf16 ? 2 : 4;
+  if ((ld_x * esz) % 16 || !aligned16(xin) || !aligned16(W) || !aligned_to(scales, esz) ||
+      !aligned_to(out, esz))
+    return MOL_E_ALIGN;
+  mol::Q4GemmArgs a{};
+  a.x = xin;
+  a.ld_x = ld_x;
+  a.W = W;
+  a.scales = scales;
+  a.zeros = zeros;
+  a.group = group;
+  a.K = K;
+  a.N = N;
+  a.E = num_experts;
+  a.sorted = sorted_ids;
+  a.expert_ids = expert_ids;
+  a.npp = num_post_padded;
+  a.numel = numel;
+  a.BM = block_m;
+  a.max_blocks = (int32_t)rc.max_blocks;
+  a.tiles = (int32_t)cdiv64(N, 16);
+  if (rc.max_blocks * a.tiles > kI32Max) return MOL_E_LIMIT;
+  a.out = out;
+  a.ld_out = ld_out;
+  a.f_rd = mol::make_fastdiv((uint32_t)row_div);
+  a.f_bm = mol::make_fastdiv((uint32_t)block_m);
+  a.f_tiles = mol::make_fastdiv((uint32_t)a.tiles);
+  return hip_status(mol::launch_q4_gemm(a, bf16, (hipStream_t)stream));
+}
+
+// ---- whole layer ---------------------------------------------------------------------
+
+MOL_API int64_t mol_moe_layer_workspace_bytes(int32_t dtype, int32_t M, int32_t topk,
+                                              int32_t hidden, int32_t inter, int32_t rank) {
+  if (dtype != MOL_F32 && dtype != MOL_BF16) return -MOL_E_DTYPE;
+  if (M < 0 || topk < 1 || hidden < 1 || inter < 1 || rank < 0) return -MOL_E_ARG;
+  const int esz = dtype == MOL_BF16 ? 2 : 4;
+  if (topk > MOL_LAYER_MAX_TOPK || (int64_t)M * topk > MOL_LAYER_MAX_PAIRS ||
+      (int64_t)rank * esz > MOL_MAX_RANK_BYTES)
+    return -MOL_E_LIMIT;
+  return layer_workspace((int64_t)M * topk, M, hidden, inter, rank, esz).bytes;
+}
+
+MOL_API mol_status mol_moe_layer(const mol_moe_weights* w, const mol_moe_adapters* adapters,
+                                 const void* x, int64_t ld_x, const int32_t* topk_ids,
+                                 const float* topk_weights, const int32_t* lora_ids, int32_t M,
+                                 int32_t topk, void* y, int64_t ld_y, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  if (!w) return MOL_E_ARG;
+  if (w->dtype != MOL_F32 && w->dtype != MOL_BF16) return MOL_E_DTYPE;
+  const int32_t E = w->num_experts, H = w->hidden, I = w->inter, G = w->group;
+  if (M < 0 || topk < 1 || E < 1 || H < 1 || I < 1 || ld_x < H || ld_y < H) return MOL_E_ARG;
+  const bool bf16 = w->dtype == MOL_BF16;
+  const int esz = bf16 ? 2 : 4;
+  if ((int64_t)E + 1 > MOL_MAX_BUCKETS || topk > MOL_LAYER_MAX_TOPK ||
+      (int64_t)M * topk > MOL_LAYER_MAX_PAIRS)
+    return MOL_E_LIMIT;
+  if (!w->gate_up || !w->down) return MOL_E_ARG;
+  if (G) {
+    mol_status qc = q4_check(H, G, 2 * (int64_t)I);
+    if (qc == MOL_OK) qc = q4_check(I, G, H);
+    if (qc != MOL_OK) return qc;
+    if (!w->gate_up_scales || !w->down_scales) return MOL_E_ARG;
+    if (!aligned_to(w->gate_up_scales, esz) || !aligned_to(w->down_scales, esz))
+      return MOL_E_ALIGN;
+  } else {
+    if (w->gate_up_scales || w->down_scales || w->gate_up_zeros || w->down_zeros)
+      return MOL_E_ARG;  // dense weights have neither
+    if (((int64_t)H * esz) % 16 || ((int64_t)I * esz) % 16) return MOL_E_ALIGN;
+    if (2 * (int64_t)I * H * esz >= (int64_t(1) << 31)) return MOL_E_LIMIT;  // one expert
+  }
+  if (!aligned16(w->gate_up) || !aligned16(w->down) || (ld_x * esz) % 16) return MOL_E_ALIGN;
+  const int32_t r = adapters ? adapters->rank : 0;
+  if (adapters) {
+    const mol_moe_adapters& d = *adapters;
+    if (d.num_slots < 1 || r < 1) return MOL_E_ARG;
+    if ((int64_t)E * d.num_slots + 1 > MOL_MAX_BUCKETS || (int64_t)r * esz > MOL_MAX_RANK_BYTES)
+      return MOL_E_LIMIT;
+    if (((int64_t)r * esz) % 16 || ((int64_t)H * esz) % 16 || ((int64_t)I * esz) % 16)
+      return MOL_E_ALIGN;
+    if (2 * (int64_t)r * H * esz >= (int64_t(1) << 31) || (int64_t)r * I * esz >= (int64_t(1) << 31))
+      return MOL_E_LIMIT;  // one virtual expert's A
+    if (!d.gate_up_A || !d.gate_up_B || !d.down_A || !d.down_B || !d.slot_scale)
+      return MOL_E_ARG;
+    if (!aligned16(d.gate_up_A) || !aligned16(d.gate_up_B) || !aligned16(d.down_A) ||
+        !aligned16(d.down_B) || !aligned_to(d.slot_scale, 4) || !aligned_to(d.slot_ranks, 4))
+      return MOL_E_ALIGN;
+  } else if (lora_ids) {
+    return MOL_E_ARG;  // slots without adapters
+  }
+  if (M == 0) return MOL_OK;
+  if (!x || !topk_ids || !topk_weights || !y || (adapters && !lora_ids)) return MOL_E_ARG;
+  if (!aligned16(x) || !aligned_to(y, esz) || !aligned_to(topk_ids, 4) ||
+      !aligned_to(topk_weights, 4) || !aligned_to(lora_ids, 4))
+    return MOL_E_ALIGN;
+  const LayerWorkspace ws = layer_workspace((int64_t)M * topk, M, H, I, r, esz);
+  if (!workspace || workspace_bytes < (size_t)ws.bytes) return MOL_E_WORKSPACE;
+  if (!aligned16(workspace)) return MOL_E_ALIGN;
+
+  char* base = static_cast<char*>(workspace);
+  mol::LayerArgs a{};
+  a.x = x;
+  a.ld_x = ld_x;
+  a.ids = topk_ids;
+  a.weights = topk_weights;
+  a.lora = lora_ids;
+  a.W_gu = w->gate_up;
+  a.W_dn = w->down;
+  a.sc_gu = w->gate_up_scales;
+  a.sc_dn = w->down_scales;
+  a.z_gu = w->gate_up_zeros;
+  a.z_dn = w->down_zeros;
+  if (adapters) {
+    a.B_gu = adapters->gate_up_B;
+    a.B_dn = adapters->down_B;
+    a.scale = adapters->slot_scale;
+    a.ranks = adapters->slot_ranks;
+    a.S = adapters->num_slots;
+    a.r = r;
+  }
+  a.h = base;
+  a.z = reinterpret_cast<float*>(base + ws.z);
+  a.s1 = reinterpret_cast<float*>(base + ws.s1);
+  a.s2 = reinterpret_cast<float*>(base + ws.s2);
+  a.y = y;
+  a.ld_y = ld_y;
+  a.M = M;
+  a.topk = topk;
+  a.E = E;
+  a.H = H;
+  a.I = I;
+  a.group = G;
+  a.numel = M * topk;
+  a.by_pair = a.numel <= E;
+  a.slots = a.by_pair ? a.numel : E;
+  a.direct = layer_direct(M);
+  const int64_t gu_tiles = cdiv64(I, 8), dn_tiles = cdiv64(H, 16);
+  // every grid of the call: matrices x tiles, and direct down's columns x tokens
+  if (a.slots * gu_tiles > kI32Max || a.slots * dn_tiles > kI32Max ||
+      ((int64_t)H + 32) * M > kI32Max)
+    return MOL_E_LIMIT;
+  a.gu_tiles = (int32_t)gu_tiles;
+  a.dn_tiles = (int32_t)dn_tiles;
+  a.f_topk = mol::make_fastdiv((uint32_t)topk);
+  a.f_gu_tiles = mol::make_fastdiv((uint32_t)gu_tiles);
+  a.f_dn_tiles = mol::make_fastdiv((uint32_t)dn_tiles);
+  a.f_m = mol::make_fastdiv((uint32_t)M);
+  a.f_one = mol::make_fastdiv(1u);
+  mol::ShrinkPart sp[2] = {};
+  if (adapters) {
+    for (int i = 0; i < 2; ++i) {
+      mol::ShrinkPart& s = sp[i];
+      s.x = i ? a.h : x;
+      s.ld_x = i ? I : ld_x;
+      s.A = i ? adapters->down_A : adapters->gate_up_A;
+      s.s = i ? a.s2 : a.s1;
+      s.rows = i ? r : 2 * r;
+      s.K = i ? I : H;
+      const int32_t V = E * adapters->num_slots;
+      s.by_pair = a.numel <= V;
+      s.slots = s.by_pair ? a.numel : V;
+      s.tiles = (int32_t)cdiv64(s.rows, 16);
+      s.f_rd = i ? a.f_one : a.f_topk;
+      s.f_tiles = mol::make_fastdiv((uint32_t)s.tiles);
+    }
+  }
+  return hip_status(mol::launch_moe_layer(a, sp[0], sp[1], bf16, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -199,6 +199,83 @@ struct RouterArgs {
   float* weights;          // [M, topk]
 };
 
+// The base grouped GEMM over 4-bit weights (group scales along K).
+struct Q4GemmArgs {
+  const void* x;           // rows of ld_x elements; pair p reads row p / row_div (f_rd)
+  int64_t ld_x;
+  const void* W;           // [E, N, K / 2] bytes
+  const void* scales;      // [E, N, K / group] (dtype of x)
+  const uint8_t* zeros;    // [E, N, K / group] or nullptr (8)
+  int32_t group;
+  int32_t K;
+  int32_t N;
+  int32_t E;
+  const int32_t* sorted;
+  const int32_t* expert_ids;
+  const int32_t* npp;
+  int32_t numel;
+  int32_t BM;
+  int32_t max_blocks;
+  int32_t tiles;           // 16-column tiles of N
+  void* out;               // [numel, ld_out]
+  int64_t ld_out;
+  FastDiv f_rd;
+  FastDiv f_bm;
+  FastDiv f_tiles;
+};
+
+// A whole layer for a few tokens.
+constexpr int kLayerMaxPairs = 4096;
+constexpr int kLayerMaxTopk = 64;
+constexpr int kMaxQ4Groups = 256;  // groups of one row (their scales are staged in LDS)
+
+struct LayerArgs {
+  const void* x;           // [M, H], ld_x apart
+  int64_t ld_x;
+  const int32_t* ids;      // [M, topk]
+  const float* weights;    // [M, topk]
+  const int32_t* lora;     // [M] or nullptr: no adapters
+  const void* W_gu;        // [E, 2 I, H] dense, or packed 4-bit
+  const void* W_dn;        // [E, H, I]
+  const void* sc_gu;
+  const void* sc_dn;
+  const uint8_t* z_gu;
+  const uint8_t* z_dn;
+  const void* B_gu;        // [E S, 2 I, r]
+  const void* B_dn;        // [E S, H, r]
+  const float* scale;      // [S]
+  const int32_t* ranks;    // [S] or nullptr
+  void* h;                 // [M topk, I] (dtype)
+  float* z;                // [M topk, H], grouped down only
+  float* s1;               // [M topk, 2 r]
+  float* s2;               // [M topk, r]
+  void* y;                 // [M, H], ld_y apart
+  int64_t ld_y;
+  int32_t M, topk, E, H, I, S, r, group;
+  int32_t numel;           // M * topk
+  int32_t slots;           // work items per tile: pairs (by_pair) or experts
+  bool by_pair;
+  bool direct;             // down: per token, with the combine
+  int32_t gu_tiles;        // tiles of 8 gate and 8 up columns
+  int32_t dn_tiles;        // tiles of 16 down columns
+  FastDiv f_topk, f_gu_tiles, f_dn_tiles, f_m, f_one;
+};
+
+// One rank product of a layer: s = x A_v^T.
+struct ShrinkPart {
+  const void* x;           // input rows: pair p reads row p / row_div
+  int64_t ld_x;
+  const void* A;           // [E S, rows, K]
+  float* s;                // [M topk, rows]
+  int32_t rows;
+  int32_t K;
+  int32_t slots;
+  int32_t tiles;
+  bool by_pair;
+  FastDiv f_rd;
+  FastDiv f_tiles;
+};
+
 // host-side launchers (return the launch status)
 hipError_t launch_virtual_topk(const int32_t* topk_ids, const int32_t* lora_ids, int32_t M,
                                int32_t topk, int32_t E, int32_t S, int32_t* out,
@@ -232,6 +309,9 @@ hipError_t launch_combine(const CombineArgs& a, bool bf16, hipStream_t stream);
 // fused expand + combine: ranks it is built for (R/8 or R/4 a power of two up to 16)
 bool fused_rank_supported(int32_t R, bool bf16);
 hipError_t launch_expand_combine(const CombineArgs& a, bool bf16, hipStream_t stream);
+hipError_t launch_q4_gemm(const Q4GemmArgs& a, bool bf16, hipStream_t stream);
+hipError_t launch_moe_layer(const LayerArgs& a, const ShrinkPart& gate_up_rank,
+                            const ShrinkPart& down_rank, bool bf16, hipStream_t stream);
 hipError_t launch_router(const RouterArgs& a, bool bf16, hipStream_t stream);
 
 }  // namespace mol

@@ -144,19 +144,23 @@ mol_status q4_check(int32_t K, int32_t group, int64_t N) {
 static_assert(MOL_LAYER_MAX_PAIRS == mol::kLayerMaxPairs && MOL_LAYER_MAX_TOPK == mol::kLayerMaxTopk,
               "the layer's limits");
 
-// Whether the layer's down stage runs per token, with the combine in it.
-bool layer_direct(int32_t M) { return M <= 32; }
+// Whether the layer's down stage runs per token, with the combine.
+bool layer_direct(int32_t M, int32_t r) { return r == 0 && M <= 4; }
 
-// The layer's scratch: byte offsets of z, s1 and s2 (h is first) and the total.
+// The layer's scratch: byte offsets and the total. Without adapters h, then z; with them gu (at
+// 0), the adapters' part of it, z and the adapters' part of that. All of it is fp32 (h in bf16
+// is two planes), so the type does not matter.
 struct LayerWorkspace {
-  int64_t z, s1, s2, bytes;
+  int64_t d1, z, d2, bytes;
 };
-LayerWorkspace layer_workspace(int64_t numel, int32_t M, int32_t H, int32_t I, int32_t r, int esz) {
+LayerWorkspace layer_workspace(int64_t numel, int32_t M, int32_t H, int32_t I, int32_t r) {
   LayerWorkspace w;
-  w.z = round256(numel * I * esz);
-  w.s1 = w.z + (layer_direct(M) ? 0 : round256(numel * H * 4));
-  w.s2 = w.s1 + round256(numel * 2 * r * 4);
-  w.bytes = w.s2 + round256(numel * r * 4);
+  const int64_t rows = round256(numel * I * 4), wide = round256(numel * 2 * I * 4);
+  const int64_t out = round256(numel * H * 4);
+  w.d1 = r ? wide : rows;
+  w.z = w.d1 + (r ? wide : 0);
+  w.d2 = w.z + (layer_direct(M, r) ? 0 : out);
+  w.bytes = w.d2 + (r ? out : 0);
   return w;
 }
 
@@ -768,13 +772,16 @@ MOL_API mol_status mol_moe_gemm_q4(int32_t dtype, const void* xin, int64_t ld_x,
   a.numel = numel;
   a.BM = block_m;
   a.max_blocks = (int32_t)rc.max_blocks;
-  a.tiles = (int32_t)cdiv64(N, 16);
-  if (rc.max_blocks * a.tiles > kI32Max) return MOL_E_LIMIT;
+  // blocks that hold pairs: at most one partly filled per expert, beside the full ones
+  const int64_t filled = std::min<int64_t>(numel, (int64_t)num_experts + numel / block_m);
+  a.split_k = filled * cdiv64(N, mol::q4_gemm_item_cols(false)) < mol::kSplitItems;
+  a.items = (int32_t)cdiv64(N, mol::q4_gemm_item_cols(a.split_k));
+  if (rc.max_blocks * a.items > kI32Max) return MOL_E_LIMIT;
   a.out = out;
   a.ld_out = ld_out;
   a.f_rd = mol::make_fastdiv((uint32_t)row_div);
   a.f_bm = mol::make_fastdiv((uint32_t)block_m);
-  a.f_tiles = mol::make_fastdiv((uint32_t)a.tiles);
+  a.f_items = mol::make_fastdiv((uint32_t)a.items);
   return hip_status(mol::launch_q4_gemm(a, bf16, (hipStream_t)stream));
 }
 
@@ -788,7 +795,7 @@ MOL_API int64_t mol_moe_layer_workspace_bytes(int32_t dtype, int32_t M, int32_t 
   if (topk > MOL_LAYER_MAX_TOPK || (int64_t)M * topk > MOL_LAYER_MAX_PAIRS ||
       (int64_t)rank * esz > MOL_MAX_RANK_BYTES)
     return -MOL_E_LIMIT;
-  return layer_workspace((int64_t)M * topk, M, hidden, inter, rank, esz).bytes;
+  return layer_workspace((int64_t)M * topk, M, hidden, inter, rank).bytes;
 }
 
 MOL_API mol_status mol_moe_layer(const mol_moe_weights* w, const mol_moe_adapters* adapters,
@@ -828,8 +835,8 @@ MOL_API mol_status mol_moe_layer(const mol_moe_weights* w, const mol_moe_adapter
       return MOL_E_LIMIT;
     if (((int64_t)r * esz) % 16 || ((int64_t)H * esz) % 16 || ((int64_t)I * esz) % 16)
       return MOL_E_ALIGN;
-    if (2 * (int64_t)r * H * esz >= (int64_t(1) << 31) || (int64_t)r * I * esz >= (int64_t(1) << 31))
-      return MOL_E_LIMIT;  // one virtual expert's A
+    if (2 * (int64_t)r * std::max(H, I) * esz >= (int64_t(1) << 31))
+      return MOL_E_LIMIT;  // one virtual expert's A or B
     if (!d.gate_up_A || !d.gate_up_B || !d.down_A || !d.down_B || !d.slot_scale)
       return MOL_E_ARG;
     if (!aligned16(d.gate_up_A) || !aligned16(d.gate_up_B) || !aligned16(d.down_A) ||
@@ -843,7 +850,7 @@ MOL_API mol_status mol_moe_layer(const mol_moe_weights* w, const mol_moe_adapter
   if (!aligned16(x) || !aligned_to(y, esz) || !aligned_to(topk_ids, 4) ||
       !aligned_to(topk_weights, 4) || !aligned_to(lora_ids, 4))
     return MOL_E_ALIGN;
-  const LayerWorkspace ws = layer_workspace((int64_t)M * topk, M, H, I, r, esz);
+  const LayerWorkspace ws = layer_workspace((int64_t)M * topk, M, H, I, r);
   if (!workspace || workspace_bytes < (size_t)ws.bytes) return MOL_E_WORKSPACE;
   if (!aligned16(workspace)) return MOL_E_ALIGN;
 
@@ -860,18 +867,19 @@ MOL_API mol_status mol_moe_layer(const mol_moe_weights* w, const mol_moe_adapter
   a.sc_dn = w->down_scales;
   a.z_gu = w->gate_up_zeros;
   a.z_dn = w->down_zeros;
+  a.h = base;
+  a.gu = reinterpret_cast<float*>(base);
+  a.z = reinterpret_cast<float*>(base + ws.z);
   if (adapters) {
-    a.B_gu = adapters->gate_up_B;
-    a.B_dn = adapters->down_B;
-    a.scale = adapters->slot_scale;
-    a.ranks = adapters->slot_ranks;
-    a.S = adapters->num_slots;
+    const mol_moe_adapters& d = *adapters;
+    a.rank_gu = {d.gate_up_A, d.gate_up_B, reinterpret_cast<float*>(base + ws.d1), H, 2 * I, 2};
+    a.rank_dn = {d.down_A, d.down_B, reinterpret_cast<float*>(base + ws.d2), I, H, 1};
+    a.d1 = a.rank_gu.d;
+    a.scale = d.slot_scale;
+    a.ranks = d.slot_ranks;
+    a.S = d.num_slots;
     a.r = r;
   }
-  a.h = base;
-  a.z = reinterpret_cast<float*>(base + ws.z);
-  a.s1 = reinterpret_cast<float*>(base + ws.s1);
-  a.s2 = reinterpret_cast<float*>(base + ws.s2);
   a.y = y;
   a.ld_y = ld_y;
   a.M = M;
@@ -883,38 +891,26 @@ MOL_API mol_status mol_moe_layer(const mol_moe_weights* w, const mol_moe_adapter
   a.numel = M * topk;
   a.by_pair = a.numel <= E;
   a.slots = a.by_pair ? a.numel : E;
-  a.direct = layer_direct(M);
-  const int64_t gu_tiles = cdiv64(I, 8), dn_tiles = cdiv64(H, 16);
-  // every grid of the call: matrices x tiles, and direct down's columns x tokens
-  if (a.slots * gu_tiles > kI32Max || a.slots * dn_tiles > kI32Max ||
-      ((int64_t)H + 32) * M > kI32Max)
+  const int64_t V = (int64_t)E * (adapters ? adapters->num_slots : 0);
+  a.rank_by_pair = a.numel <= V;
+  a.rank_slots = adapters ? (int32_t)std::min<int64_t>(a.numel, V) : 0;
+  a.direct = layer_direct(M, r);
+  auto items = [&](int64_t rows, bool& split) {
+    split = a.slots * cdiv64(rows, mol::moe_layer_item_rows(false)) < mol::kSplitItems;
+    return cdiv64(rows, mol::moe_layer_item_rows(split));
+  };
+  const int64_t gu_items = items(2 * (int64_t)I, a.gu_split), dn_items = items(H, a.dn_split);
+  // every grid of the call: matrices x row groups, and direct down's columns x tokens
+  if (a.slots * gu_items + a.rank_slots > kI32Max || a.slots * dn_items + a.rank_slots > kI32Max ||
+      ((int64_t)H + 128) * M > kI32Max)
     return MOL_E_LIMIT;
-  a.gu_tiles = (int32_t)gu_tiles;
-  a.dn_tiles = (int32_t)dn_tiles;
+  a.gu_items = (int32_t)gu_items;
+  a.dn_items = (int32_t)dn_items;
   a.f_topk = mol::make_fastdiv((uint32_t)topk);
-  a.f_gu_tiles = mol::make_fastdiv((uint32_t)gu_tiles);
-  a.f_dn_tiles = mol::make_fastdiv((uint32_t)dn_tiles);
+  a.f_gu_items = mol::make_fastdiv((uint32_t)gu_items);
+  a.f_dn_items = mol::make_fastdiv((uint32_t)dn_items);
   a.f_m = mol::make_fastdiv((uint32_t)M);
-  a.f_one = mol::make_fastdiv(1u);
-  mol::ShrinkPart sp[2] = {};
-  if (adapters) {
-    for (int i = 0; i < 2; ++i) {
-      mol::ShrinkPart& s = sp[i];
-      s.x = i ? a.h : x;
-      s.ld_x = i ? I : ld_x;
-      s.A = i ? adapters->down_A : adapters->gate_up_A;
-      s.s = i ? a.s2 : a.s1;
-      s.rows = i ? r : 2 * r;
-      s.K = i ? I : H;
-      const int32_t V = E * adapters->num_slots;
-      s.by_pair = a.numel <= V;
-      s.slots = s.by_pair ? a.numel : V;
-      s.tiles = (int32_t)cdiv64(s.rows, 16);
-      s.f_rd = i ? a.f_one : a.f_topk;
-      s.f_tiles = mol::make_fastdiv((uint32_t)s.tiles);
-    }
-  }
-  return hip_status(mol::launch_moe_layer(a, sp[0], sp[1], bf16, (hipStream_t)stream));
+  return hip_status(mol::launch_moe_layer(a, bf16, (hipStream_t)stream));
 }
 
 }  // extern "C"

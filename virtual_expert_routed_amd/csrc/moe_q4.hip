@@ -4,59 +4,72 @@
 // dense grouped GEMM (the aligned blocks of one base expert each).
 //
 // At decode it reads half a byte of each touched weight once and little else, so a work item is
-// (block, 16 output columns): 16 rows of W_t, read once for up to 64 pairs of the block.
+// (block, 64 output columns): 64 rows of W_t, read once for up to 64 pairs of the block. Where
+// that makes too few items to fill the chip (split_k), an item is 16 rows whose k's the four waves
+// split.
 #include "skinny.h"
 
 namespace mol {
 namespace {
 
-template <int G, bool BF16>
-__global__ void __launch_bounds__(kThreads) q4_gemm_kernel(Q4GemmArgs a) {
-  __shared__ float red[kWaves * kTiles * 256];
-  extern __shared__ __attribute__((aligned(16))) float2 sc[];
-  const int blk = fdiv((int)blockIdx.x, a.f_tiles);
-  const int n0 = ((int)blockIdx.x - blk * a.tiles) * kTileRows;
+template <int G, bool BF16, int KS>
+__global__ void __launch_bounds__(kThreads, 3) q4_gemm_kernel(Q4GemmArgs a) {
+  constexpr int kCols = kPassCols<1, KS>;
+  __shared__ int pair[kCols];
+  __shared__ __attribute__((aligned(16))) char lds[StreamLds<G>::kBytes];
+  const int blk = fdiv((int)blockIdx.x, a.f_items);
+  const int n0 = ((int)blockIdx.x - blk * a.items) * kItemRowsOf<KS>;
   const int npp = *a.npp;
   const int er = a.expert_ids[blk];
+  const int32_t* sorted = a.sorted + (int64_t)blk * a.BM;
+  // the first entries with the routing reads (their index stays inside the block)
+  int p = threadIdx.x < kCols && (int)threadIdx.x < a.BM ? sorted[threadIdx.x] : a.numel;
   const int nb = npp < 0 ? 0 : fdiv(npp, a.f_bm);
   if (blk >= nb || (unsigned)er >= (unsigned)a.E) return;
   const int e = __builtin_amdgcn_readfirstlane(er);
-  const int32_t* sorted = a.sorted + (int64_t)blk * a.BM;
-  auto entry = [&](int j) {  // the pair of entry j of the block, or -1
-    const int p = j < a.BM ? sorted[j] : a.numel;
-    return real_pair(p, a.numel) ? p : -1;
+  const int64_t rb = a.K / 2, wbytes = (int64_t)a.N * rb;
+  const int wn0 = wave_row0<KS>(n0);
+  const int n = wn0 + (int)(threadIdx.x & 15);
+  const WeightRows w{expert_rsrc((const char*)a.W + (int64_t)e * wbytes, wbytes),
+                     n < a.N ? (uint32_t)(n * rb) : kOutOfRange};
+  const Q4Tables q{a.scales, a.zeros, a.K / G};
+  auto row_at = [&](int r) {
+    return wn0 + r < a.N ? (int64_t)e * a.N + wn0 + r : (int64_t)-1;
   };
-  if (entry(0) < 0) return;
-  const int ng = a.K / G;
-  stage_scales<BF16>(sc, a.scales, a.zeros, ng, [&](int r) {
-    return n0 + r < a.N ? (int64_t)e * a.N + n0 + r : (int64_t)-1;
-  });
-  __syncthreads();
-  const int64_t wbytes = (int64_t)a.N * a.K / 2;
-  const int n = n0 + (int)(threadIdx.x & 15);
-  const BufRow w{expert_rsrc((const char*)a.W + (int64_t)e * wbytes, wbytes),
-                 n < a.N ? (uint32_t)n * (uint32_t)(a.K / 2) : kOutOfRange};
-  for (int j0 = 0; j0 < a.BM; j0 += 16 * kTiles) {
-    int nt = 0;  // tiles that hold a real pair (the real pairs are a prefix of the block)
+  const RowSrc src{(const char*)a.x, a.ld_x * (BF16 ? 2 : 4), pair, a.f_rd};
+  const int quad = (threadIdx.x & 63) >> 4;
+  for (int j0 = 0; j0 < a.BM; j0 += kCols) {
+    if (j0 > 0) {
+      const int j = j0 + (int)threadIdx.x;
+      p = threadIdx.x < kCols && j < a.BM ? sorted[j] : a.numel;
+      __syncthreads();  // pair is no longer read
+    }
+    if (threadIdx.x < kCols) pair[threadIdx.x] = p;
+    __syncthreads();
+    // the real pairs are a prefix of the block
+    const int j = threadIdx.x & 63;
+    const int ncol = __popcll(
+        __builtin_amdgcn_ballot_w64(j < kCols && real_pair(pair[j < kCols ? j : 0], a.numel)));
+    if (ncol == 0) return;
+    stream_cols<G, BF16, 1, KS>(lds, w, q, row_at, wn0 < a.N, src, ncol, a.K,
+                            [&](int c, const f32x4_t& acc) {
+      if (c >= ncol) return;
+      const int64_t at = (int64_t)pair[c] * a.ld_out + wn0 + quad * 4;
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) nt += entry(j0 + 16 * t) >= 0 ? 1 : 0;
-    if (nt == 0) return;
-    auto store = [&](int j, int r, float v) {
-      const int p = entry(j);
-      if (p >= 0 && n0 + r < a.N) store_elem<BF16>(a.out, (int64_t)p * a.ld_out + n0 + r, v);
-    };
-    if (nt == 1)
-      tile_pass<G, BF16, 1>(w, a.x, a.ld_x, a.f_rd, a.K, sc, entry, j0, 1, red, store);
-    else
-      tile_pass<G, BF16, kTiles>(w, a.x, a.ld_x, a.f_rd, a.K, sc, entry, j0, nt, red, store);
+      for (int i = 0; i < 4; ++i)
+        if (wn0 + quad * 4 + i < a.N) store_elem<BF16>(a.out, at + i, acc[i]);
+    });
+    if (ncol < kCols) return;
   }
 }
 
 template <int G, bool BF16>
 hipError_t launch(const Q4GemmArgs& a, hipStream_t st) {
-  const size_t lds = (size_t)(a.K / G) * kTileRows * sizeof(float2);
-  hipLaunchKernelGGL((q4_gemm_kernel<G, BF16>), dim3(a.max_blocks * a.tiles), dim3(kThreads), lds,
-                     st, a);
+  const dim3 grid(a.max_blocks * a.items);
+  if (a.split_k)
+    hipLaunchKernelGGL((q4_gemm_kernel<G, BF16, kWaves>), grid, dim3(kThreads), 0, st, a);
+  else
+    hipLaunchKernelGGL((q4_gemm_kernel<G, BF16, 1>), grid, dim3(kThreads), 0, st, a);
   return hipGetLastError();
 }
 
@@ -70,5 +83,7 @@ hipError_t launch_q4_gemm(const Q4GemmArgs& a, bool bf16, hipStream_t st) {
     default: return hipErrorInvalidValue;
   }
 }
+
+int q4_gemm_item_cols(bool split_k) { return split_k ? kTileRows : kItemRows; }
 
 }  // namespace mol

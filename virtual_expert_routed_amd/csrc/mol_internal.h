@@ -200,6 +200,11 @@ struct RouterArgs {
 };
 
 // The base grouped GEMM over 4-bit weights (group scales along K).
+// Items of 64 weight rows and of 16 (their k's split between four waves) read the same bytes; the
+// smaller ones are for launches whose larger ones would leave the chip's 256 CUs with fewer than
+// kSplitItems between them.
+constexpr int64_t kSplitItems = 1024;
+
 struct Q4GemmArgs {
   const void* x;           // rows of ld_x elements; pair p reads row p / row_div (f_rd)
   int64_t ld_x;
@@ -216,18 +221,29 @@ struct Q4GemmArgs {
   int32_t numel;
   int32_t BM;
   int32_t max_blocks;
-  int32_t tiles;           // 16-column tiles of N
+  bool split_k;            // items of 16 columns, k's split between the waves (else 64)
+  int32_t items;           // work items of q4_gemm_item_cols() columns per block
   void* out;               // [numel, ld_out]
   int64_t ld_out;
   FastDiv f_rd;
   FastDiv f_bm;
-  FastDiv f_tiles;
+  FastDiv f_items;
 };
 
 // A whole layer for a few tokens.
 constexpr int kLayerMaxPairs = 4096;
 constexpr int kLayerMaxTopk = 64;
-constexpr int kMaxQ4Groups = 256;  // groups of one row (their scales are staged in LDS)
+constexpr int kMaxQ4Groups = 256;  // groups of one row
+
+// The adapters of one of its stages: d = c B (A x) per pair.
+struct RankPart {
+  const void* A;           // [E S, slices r, K]
+  const void* B;           // [E S, N, r]
+  float* d;                // [M topk, N] fp32
+  int32_t K;
+  int32_t N;
+  int32_t slices;
+};
 
 struct LayerArgs {
   const void* x;           // [M, H], ld_x apart
@@ -241,39 +257,27 @@ struct LayerArgs {
   const void* sc_dn;
   const uint8_t* z_gu;
   const uint8_t* z_dn;
-  const void* B_gu;        // [E S, 2 I, r]
-  const void* B_dn;        // [E S, H, r]
+  RankPart rank_gu;
+  RankPart rank_dn;
   const float* scale;      // [S]
   const int32_t* ranks;    // [S] or nullptr
-  void* h;                 // [M topk, I] (dtype)
-  float* z;                // [M topk, H], grouped down only
-  float* s1;               // [M topk, 2 r]
-  float* s2;               // [M topk, r]
+  void* h;                 // without adapters: [M topk, I] as bf16 hi, lo planes or fp32
+  float* gu;               // with adapters: [M topk, 2 I]
+  const float* d1;         // rank_gu.d
+  float* z;                // [M topk, H]
   void* y;                 // [M, H], ld_y apart
   int64_t ld_y;
   int32_t M, topk, E, H, I, S, r, group;
   int32_t numel;           // M * topk
-  int32_t slots;           // work items per tile: pairs (by_pair) or experts
+  int32_t slots;           // work items per row group: pairs (by_pair) or experts
   bool by_pair;
-  bool direct;             // down: per token, with the combine
-  int32_t gu_tiles;        // tiles of 8 gate and 8 up columns
-  int32_t dn_tiles;        // tiles of 16 down columns
-  FastDiv f_topk, f_gu_tiles, f_dn_tiles, f_m, f_one;
-};
-
-// One rank product of a layer: s = x A_v^T.
-struct ShrinkPart {
-  const void* x;           // input rows: pair p reads row p / row_div
-  int64_t ld_x;
-  const void* A;           // [E S, rows, K]
-  float* s;                // [M topk, rows]
-  int32_t rows;
-  int32_t K;
-  int32_t slots;
-  int32_t tiles;
-  bool by_pair;
-  FastDiv f_rd;
-  FastDiv f_tiles;
+  int32_t rank_slots;      // adapter items: pairs (rank_by_pair) or virtual experts
+  bool rank_by_pair;
+  bool direct;             // down per token, with the combine
+  bool gu_split, dn_split; // items of 16 rows, k's split between the waves (else 64 rows)
+  int32_t gu_items;        // row groups of gate/up and of down
+  int32_t dn_items;
+  FastDiv f_topk, f_gu_items, f_dn_items, f_m;
 };
 
 // host-side launchers (return the launch status)
@@ -309,9 +313,12 @@ hipError_t launch_combine(const CombineArgs& a, bool bf16, hipStream_t stream);
 // fused expand + combine: ranks it is built for (R/8 or R/4 a power of two up to 16)
 bool fused_rank_supported(int32_t R, bool bf16);
 hipError_t launch_expand_combine(const CombineArgs& a, bool bf16, hipStream_t stream);
+int q4_gemm_item_cols(bool split_k);
 hipError_t launch_q4_gemm(const Q4GemmArgs& a, bool bf16, hipStream_t stream);
-hipError_t launch_moe_layer(const LayerArgs& a, const ShrinkPart& gate_up_rank,
-                            const ShrinkPart& down_rank, bool bf16, hipStream_t stream);
+// rows of a layer's work items
+int moe_layer_item_rows(bool split);
+hipError_t launch_moe_layer(const LayerArgs& a, bool bf16, hipStream_t stream);
+hipError_t launch_moe_layer_direct(const LayerArgs& a, bool bf16, hipStream_t stream);
 hipError_t launch_router(const RouterArgs& a, bool bf16, hipStream_t stream);
 
 }  // namespace mol

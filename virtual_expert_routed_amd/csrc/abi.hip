@@ -147,19 +147,19 @@ static_assert(MOL_LAYER_MAX_PAIRS == mol::kLayerMaxPairs && MOL_LAYER_MAX_TOPK =
 // Whether the layer's down stage runs per token, with the combine.
 bool layer_direct(int32_t M, int32_t r) { return r == 0 && M <= 4; }
 
-// The layer's scratch: byte offsets and the total. Without adapters h, then z; with them gu (at
-// 0), the adapters' part of it, z and the adapters' part of that. All of it is fp32 (h in bf16
-// is two planes), so the type does not matter.
+// The layer's scratch: byte offsets and the total. h is first, then z (not for a direct down), and
+// with adapters gu and both of their parts. All of it is four bytes an element (h in bf16 is two
+// planes), so the type does not matter.
 struct LayerWorkspace {
-  int64_t d1, z, d2, bytes;
+  int64_t z, gu, d1, d2, bytes;
 };
 LayerWorkspace layer_workspace(int64_t numel, int32_t M, int32_t H, int32_t I, int32_t r) {
   LayerWorkspace w;
-  const int64_t rows = round256(numel * I * 4), wide = round256(numel * 2 * I * 4);
-  const int64_t out = round256(numel * H * 4);
-  w.d1 = r ? wide : rows;
-  w.z = w.d1 + (r ? wide : 0);
-  w.d2 = w.z + (layer_direct(M, r) ? 0 : out);
+  const int64_t wide = r ? round256(numel * 2 * I * 4) : 0, out = round256(numel * H * 4);
+  w.z = round256(numel * I * 4);
+  w.gu = w.z + (layer_direct(M, r) ? 0 : out);
+  w.d1 = w.gu + wide;
+  w.d2 = w.d1 + wide;
   w.bytes = w.d2 + (r ? out : 0);
   return w;
 }
@@ -774,8 +774,10 @@ MOL_API mol_status mol_moe_gemm_q4(int32_t dtype, const void* xin, int64_t ld_x,
   a.max_blocks = (int32_t)rc.max_blocks;
   // blocks that hold pairs: at most one partly filled per expert, beside the full ones
   const int64_t filled = std::min<int64_t>(numel, (int64_t)num_experts + numel / block_m);
-  a.split_k = filled * cdiv64(N, mol::q4_gemm_item_cols(false)) < mol::kSplitItems;
-  a.items = (int32_t)cdiv64(N, mol::q4_gemm_item_cols(a.split_k));
+  const mol::ItemShape shape = mol::item_shape(filled, N);
+  a.split_k = shape.split;
+  a.item_tiles = shape.tiles;
+  a.items = (int32_t)shape.items;
   if (rc.max_blocks * a.items > kI32Max) return MOL_E_LIMIT;
   a.out = out;
   a.ld_out = ld_out;
@@ -868,13 +870,12 @@ MOL_API mol_status mol_moe_layer(const mol_moe_weights* w, const mol_moe_adapter
   a.z_gu = w->gate_up_zeros;
   a.z_dn = w->down_zeros;
   a.h = base;
-  a.gu = reinterpret_cast<float*>(base);
+  a.gu = reinterpret_cast<float*>(base + ws.gu);
   a.z = reinterpret_cast<float*>(base + ws.z);
   if (adapters) {
     const mol_moe_adapters& d = *adapters;
     a.rank_gu = {d.gate_up_A, d.gate_up_B, reinterpret_cast<float*>(base + ws.d1), H, 2 * I, 2};
     a.rank_dn = {d.down_A, d.down_B, reinterpret_cast<float*>(base + ws.d2), I, H, 1};
-    a.d1 = a.rank_gu.d;
     a.scale = d.slot_scale;
     a.ranks = d.slot_ranks;
     a.S = d.num_slots;
@@ -895,20 +896,21 @@ MOL_API mol_status mol_moe_layer(const mol_moe_weights* w, const mol_moe_adapter
   a.rank_by_pair = a.numel <= V;
   a.rank_slots = adapters ? (int32_t)std::min<int64_t>(a.numel, V) : 0;
   a.direct = layer_direct(M, r);
-  auto items = [&](int64_t rows, bool& split) {
-    split = a.slots * cdiv64(rows, mol::moe_layer_item_rows(false)) < mol::kSplitItems;
-    return cdiv64(rows, mol::moe_layer_item_rows(split));
-  };
-  const int64_t gu_items = items(2 * (int64_t)I, a.gu_split), dn_items = items(H, a.dn_split);
+  const mol::ItemShape gu = mol::item_shape(a.slots, 2 * (int64_t)I);
+  const mol::ItemShape dn = mol::item_shape(a.slots, H);
   // every grid of the call: matrices x row groups, and direct down's columns x tokens
-  if (a.slots * gu_items + a.rank_slots > kI32Max || a.slots * dn_items + a.rank_slots > kI32Max ||
+  if (a.slots * gu.items + a.rank_slots > kI32Max || a.slots * dn.items + a.rank_slots > kI32Max ||
       ((int64_t)H + 128) * M > kI32Max)
     return MOL_E_LIMIT;
-  a.gu_items = (int32_t)gu_items;
-  a.dn_items = (int32_t)dn_items;
+  a.gu_split = gu.split;
+  a.gu_tiles = gu.tiles;
+  a.gu_items = (int32_t)gu.items;
+  a.dn_split = dn.split;
+  a.dn_tiles = dn.tiles;
+  a.dn_items = (int32_t)dn.items;
   a.f_topk = mol::make_fastdiv((uint32_t)topk);
-  a.f_gu_items = mol::make_fastdiv((uint32_t)gu_items);
-  a.f_dn_items = mol::make_fastdiv((uint32_t)dn_items);
+  a.f_gu_items = mol::make_fastdiv((uint32_t)gu.items);
+  a.f_dn_items = mol::make_fastdiv((uint32_t)dn.items);
   a.f_m = mol::make_fastdiv((uint32_t)M);
   return hip_status(mol::launch_moe_layer(a, bf16, (hipStream_t)stream));
 }

@@ -4,8 +4,8 @@
 // dense grouped GEMM (the aligned blocks of one base expert each).
 //
 // At decode it reads half a byte of each touched weight once and little else, so a work item is
-// (block, 64 output columns): 64 rows of W_t, read once for up to 64 pairs of the block. Where
-// that makes too few items to fill the chip (split_k), an item is 16 rows whose k's the four waves
+// (block, 64, 128 or 256 output columns): rows of W_t, read once for up to 64 pairs of the block.
+// Where 64 make too few items to fill the chip (split_k), an item is 16 rows whose k's the four waves
 // split.
 #include "skinny.h"
 
@@ -18,7 +18,7 @@ __global__ void __launch_bounds__(kThreads, 3) q4_gemm_kernel(Q4GemmArgs a) {
   __shared__ int pair[kCols];
   __shared__ __attribute__((aligned(16))) char lds[StreamLds<G>::kBytes];
   const int blk = fdiv((int)blockIdx.x, a.f_items);
-  const int n0 = ((int)blockIdx.x - blk * a.items) * kItemRowsOf<KS>;
+  const int n0 = ((int)blockIdx.x - blk * a.items) * (KS > 1 ? kTileRows : kItemRows * a.item_tiles);
   const int npp = *a.npp;
   const int er = a.expert_ids[blk];
   const int32_t* sorted = a.sorted + (int64_t)blk * a.BM;
@@ -28,16 +28,18 @@ __global__ void __launch_bounds__(kThreads, 3) q4_gemm_kernel(Q4GemmArgs a) {
   if (blk >= nb || (unsigned)er >= (unsigned)a.E) return;
   const int e = __builtin_amdgcn_readfirstlane(er);
   const int64_t rb = a.K / 2, wbytes = (int64_t)a.N * rb;
-  const int wn0 = wave_row0<KS>(n0);
-  const int n = wn0 + (int)(threadIdx.x & 15);
-  const WeightRows w{expert_rsrc((const char*)a.W + (int64_t)e * wbytes, wbytes),
-                     n < a.N ? (uint32_t)(n * rb) : kOutOfRange};
+  const __amdgpu_buffer_rsrc_t rsrc = expert_rsrc((const char*)a.W + (int64_t)e * wbytes, wbytes);
+  const int lane = threadIdx.x & 63, quad = lane >> 4;
   const Q4Tables q{a.scales, a.zeros, a.K / G};
-  auto row_at = [&](int r) {
-    return wn0 + r < a.N ? (int64_t)e * a.N + wn0 + r : (int64_t)-1;
+  auto row_at = [&](int t) {
+    const int n = tile_row0<KS>(n0, t) + (lane & 15);
+    return n < a.N ? (int64_t)e * a.N + n : (int64_t)-1;
+  };
+  auto off = [&](int t) {
+    const int n = tile_row0<KS>(n0, t) + (lane & 15);
+    return n < a.N ? (uint32_t)(n * rb) : kOutOfRange;
   };
   const RowSrc src{(const char*)a.x, a.ld_x * (BF16 ? 2 : 4), pair, a.f_rd};
-  const int quad = (threadIdx.x & 63) >> 4;
   for (int j0 = 0; j0 < a.BM; j0 += kCols) {
     if (j0 > 0) {
       const int j = j0 + (int)threadIdx.x;
@@ -51,13 +53,14 @@ __global__ void __launch_bounds__(kThreads, 3) q4_gemm_kernel(Q4GemmArgs a) {
     const int ncol = __popcll(
         __builtin_amdgcn_ballot_w64(j < kCols && real_pair(pair[j < kCols ? j : 0], a.numel)));
     if (ncol == 0) return;
-    stream_cols<G, BF16, 1, KS>(lds, w, q, row_at, wn0 < a.N, src, ncol, a.K,
-                            [&](int c, const f32x4_t& acc) {
+    stream_cols<G, BF16, 1, KS>(lds, rsrc, off, KS > 1 ? 1 : a.item_tiles, q, row_at, src, ncol, a.K,
+                                [&](int t, int c, const f32x4_t& acc) {
       if (c >= ncol) return;
-      const int64_t at = (int64_t)pair[c] * a.ld_out + wn0 + quad * 4;
+      const int n = tile_row0<KS>(n0, t) + quad * 4;
+      const int64_t at = (int64_t)pair[c] * a.ld_out + n;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (wn0 + quad * 4 + i < a.N) store_elem<BF16>(a.out, at + i, acc[i]);
+        if (n + i < a.N) store_elem<BF16>(a.out, at + i, acc[i]);
     });
     if (ncol < kCols) return;
   }
@@ -84,6 +87,6 @@ hipError_t launch_q4_gemm(const Q4GemmArgs& a, bool bf16, hipStream_t st) {
   }
 }
 
-int q4_gemm_item_cols(bool split_k) { return split_k ? kTileRows : kItemRows; }
+int stream_item_rows(bool split, int tiles) { return item_rows(split, tiles); }
 
 }  // namespace mol

@@ -199,12 +199,26 @@ struct RouterArgs {
   float* weights;          // [M, topk]
 };
 
-// The base grouped GEMM over 4-bit weights (group scales along K).
-// Items of 64 weight rows and of 16 (their k's split between four waves) read the same bytes; the
-// smaller ones are for launches whose larger ones would leave the chip's 256 CUs with fewer than
-// kSplitItems between them.
-constexpr int64_t kSplitItems = 1024;
+// Work items of a stream of weight rows: 64 rows times `tiles`, or 16 rows whose k's four waves
+// split. All read the same bytes. Larger ones stage x less often, and need enough of them to
+// fill the chip's 256 CUs evenly.
+struct ItemShape {
+  bool split;
+  int tiles;
+  int64_t items;  // per matrix
+};
+int stream_item_rows(bool split, int tiles);
+inline ItemShape item_shape(int64_t matrices, int64_t rows) {
+  auto items = [&](bool split, int tiles) {
+    const int64_t n = stream_item_rows(split, tiles);
+    return (rows + n - 1) / n;
+  };
+  for (int tiles = 1; tiles >= 1; tiles /= 2)
+    if (matrices * items(false, tiles) >= 1024) return {false, tiles, items(false, tiles)};
+  return {true, 1, items(true, 1)};
+}
 
+// The base grouped GEMM over 4-bit weights (group scales along K).
 struct Q4GemmArgs {
   const void* x;           // rows of ld_x elements; pair p reads row p / row_div (f_rd)
   int64_t ld_x;
@@ -221,8 +235,9 @@ struct Q4GemmArgs {
   int32_t numel;
   int32_t BM;
   int32_t max_blocks;
-  bool split_k;            // items of 16 columns, k's split between the waves (else 64)
-  int32_t items;           // work items of q4_gemm_item_cols() columns per block
+  bool split_k;            // item_shape()
+  int32_t item_tiles;
+  int32_t items;           // work items per block
   void* out;               // [numel, ld_out]
   int64_t ld_out;
   FastDiv f_rd;
@@ -261,9 +276,8 @@ struct LayerArgs {
   RankPart rank_dn;
   const float* scale;      // [S]
   const int32_t* ranks;    // [S] or nullptr
-  void* h;                 // without adapters: [M topk, I] as bf16 hi, lo planes or fp32
+  void* h;                 // [M topk, I] as bf16 hi, lo planes or fp32
   float* gu;               // with adapters: [M topk, 2 I]
-  const float* d1;         // rank_gu.d
   float* z;                // [M topk, H]
   void* y;                 // [M, H], ld_y apart
   int64_t ld_y;
@@ -274,7 +288,8 @@ struct LayerArgs {
   int32_t rank_slots;      // adapter items: pairs (rank_by_pair) or virtual experts
   bool rank_by_pair;
   bool direct;             // down per token, with the combine
-  bool gu_split, dn_split; // items of 16 rows, k's split between the waves (else 64 rows)
+  bool gu_split, dn_split; // item_shape() of gate/up and of down
+  int32_t gu_tiles, dn_tiles;
   int32_t gu_items;        // row groups of gate/up and of down
   int32_t dn_items;
   FastDiv f_topk, f_gu_items, f_dn_items, f_m;
@@ -313,10 +328,7 @@ hipError_t launch_combine(const CombineArgs& a, bool bf16, hipStream_t stream);
 // fused expand + combine: ranks it is built for (R/8 or R/4 a power of two up to 16)
 bool fused_rank_supported(int32_t R, bool bf16);
 hipError_t launch_expand_combine(const CombineArgs& a, bool bf16, hipStream_t stream);
-int q4_gemm_item_cols(bool split_k);
 hipError_t launch_q4_gemm(const Q4GemmArgs& a, bool bf16, hipStream_t stream);
-// rows of a layer's work items
-int moe_layer_item_rows(bool split);
 hipError_t launch_moe_layer(const LayerArgs& a, bool bf16, hipStream_t stream);
 hipError_t launch_moe_layer_direct(const LayerArgs& a, bool bf16, hipStream_t stream);
 hipError_t launch_router(const RouterArgs& a, bool bf16, hipStream_t stream);

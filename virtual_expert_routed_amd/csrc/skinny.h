@@ -39,7 +39,7 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kTileRows = 16;
 constexpr int kWaves = kThreads / 64;
-constexpr int kItemRows = kWaves * kTileRows;  // weight rows of a work item (KS = 1)
+constexpr int kItemRows = kWaves * kTileRows;  // weight rows of a tile of each wave
 constexpr int kMaxCols = 64;                   // columns of one pass, over the planes of x
 constexpr int kXBytes = 32768;                 // x staged at a time (four workgroups a CU)
 constexpr int kQ4Load = 128;                   // k's of one load of 4-bit weights
@@ -156,12 +156,11 @@ struct Stream {
   static constexpr int CLG = G ? kMaxGroups<G> * G / kQ4Load : CLX;  // and whose scales do
   static constexpr int CL = CLX < CLG ? CLX : CLG;
   static constexpr int Q = CL / KS;                       // of them, one wave's
-  static constexpr int UM = G ? (G == 32 ? 2 : 4) : 8;
+  static constexpr int UM = G == 0 || G == 128 ? 8 : G == 64 ? 4 : 2;
   static constexpr int U = Q < UM ? Q : UM;               // loads of W in flight: a round
-  static constexpr int R = G && U > 2 ? 2 : U;            // the shorter last round
   static constexpr int T = CW > 16 ? CW / 16 : 1;         // matrix-core tiles of columns
   static constexpr int PERIOD = LX % 4 ? 4 : 1;           // loads between equal x rotations
-  static_assert(Q >= 1 && Q % U == 0 && U % R == 0 && Q % PERIOD == 0 && R % PERIOD == 0,
+  static_assert(Q >= 1 && Q % U == 0 && Q % PERIOD == 0 && U % PERIOD == 0,
                 "a wave's part of a stage is whole rounds of loads");
   static_assert(KS == 1 || T == 1, "split k's: one tile of columns");
 };
@@ -282,13 +281,7 @@ struct StageX {
 
 // ---- the stream ----
 
-// A wave's 16 weight rows inside one expert's matrix: lane l's row at byte `off` (kOutOfRange:
-// none), bytes past the matrix read as zero. Scales and zero points, when 4-bit: row r of the
-// tile at index row_at(r) of the tables, negative for none.
-struct WeightRows {
-  __amdgpu_buffer_rsrc_t rsrc;
-  uint32_t off;
-};
+// Scales and zero points of 4-bit weights.
 struct Q4Tables {
   const void* scales;
   const uint8_t* zeros;
@@ -324,15 +317,18 @@ struct ScaleRegs {
   }
 };
 
-// Runs one item: this wave's 16 rows (live: it has any) against ncol staged columns; with KS =
-// kWaves the waves have the same rows and split their k's. epilogue(col, acc) gets, on every
-// lane (of wave 0 for KS = kWaves), column col's sums of tile rows 4 * quad + i; only columns
-// below ncol and rows that exist are meant. All four waves take part in the barriers; on return
-// LDS may still be read by slower waves.
-template <int G, bool BF16, int CW, int NP, int KS, class Src, class RowAt, class Epi>
-__device__ __forceinline__ void stream_rows(char* lds, const WeightRows& w, const Q4Tables& q,
-                                            RowAt row_at, bool live, const Src& src, int ncol,
-                                            int K, Epi epilogue) {
+// Runs one item against ncol staged columns: `tiles` tiles of this wave, one after another (KS = 1),
+// the same x serving all of them when a row's x fits one stage; with KS = kWaves the waves have
+// the same rows and split their k's. off(t): this lane's row of tile t (lane % 16) as a byte
+// offset into the matrix, kOutOfRange for none; row_at(t): its row in the scale tables, negative
+// for none. epilogue(t, col, acc) gets, on every lane (of wave 0 for KS = kWaves), column
+// col's sums of tile rows 4 * quad + i; only columns below ncol and rows that exist are
+// meant. All four waves take part in the barriers; on return LDS may still be read by slower
+// waves.
+template <int G, bool BF16, int CW, int NP, int KS, class Off, class Src, class RowAt, class Epi>
+__device__ __forceinline__ void stream_rows(char* lds, __amdgpu_buffer_rsrc_t rsrc, Off off,
+                                            int tiles, const Q4Tables& q, RowAt row_at,
+                                            const Src& src, int ncol, int K, Epi epilogue) {
   using S = Stream<G, BF16, CW, NP, KS>;
   // (opaque to the compiler, which would otherwise compute every variant's addresses ahead of the
   // loop over passes and spill them)
@@ -343,26 +339,24 @@ __device__ __forceinline__ void stream_rows(char* lds, const WeightRows& w, cons
   const int loads = (K + S::KL - 1) / S::KL;
   // loads per stage, and this wave's part of them: one stage is split evenly
   int cl = S::CL, part = S::Q, first = 0;
-  if constexpr (KS > 1) {
-    if (loads <= S::CL) {
-      part = ((loads + KS - 1) / KS + S::R - 1) / S::R * S::R;
-      cl = part * KS;
-    }
-    first = wv * part;
+  const bool one_stage = loads <= S::CL;
+  if (one_stage) {
+    part = ((loads + KS - 1) / KS + S::U - 1) / S::U * S::U;
+    cl = part * KS;
   }
+  if constexpr (KS > 1) first = wv * part;
   // every load is issued: past the row (and for rows that are not there) it reads zeros and
   // moves nothing
-  const uint32_t lane_off = w.off + (uint32_t)quad * 16u;
   const int k_left = K - quad * (S::KL / 4);  // k's from this lane's part of load 0 on
-  auto load = [&](int l) {
-    return buf16(w.rsrc, l * S::KL < k_left ? lane_off + (uint32_t)l * 64u : kOutOfRange);
+  auto load = [&](uint32_t row_off, int l) {
+    return buf16(rsrc, l * S::KL < k_left ? row_off + (uint32_t)quad * 16u + (uint32_t)l * 64u
+                                          : kOutOfRange);
   };
+  uint32_t here = off(0), next = tiles > 1 ? off(1) : kOutOfRange;
   uint4 wr[S::U];
 #pragma unroll
-  for (int u = 0; u < S::U; ++u) wr[u] = load(u < part ? first + u : loads);
+  for (int u = 0; u < S::U; ++u) wr[u] = load(here, first + u);
   f32x4_t acc[S::T];
-#pragma unroll
-  for (int t = 0; t < S::T; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   // this lane's slots of x steps 0-3 (the rotation's period) relative to the step's first slot
   int slot[4];
 #pragma unroll
@@ -371,120 +365,120 @@ __device__ __forceinline__ void stream_rows(char* lds, const WeightRows& w, cons
   const float* sums = reinterpret_cast<const float*>(lds + kXBytes) + (col & (CW - 1));
   float2* sc = reinterpret_cast<float2*>(lds + kXBytes + StreamLds<G>::kSums) +
                (KS > 1 ? 0 : wv) * (kMaxGroups<G> * kTileRows);
-  int64_t srow = -1;
-  if constexpr (G > 0) srow = row_at(col);
+  constexpr int GPL = G ? kQ4Load / (G ? G : 1) : 0;  // groups of a load
 
-  for (int l0 = 0; l0 < loads; l0 += cl) {
-    __syncthreads();
-    StageX<S, G, BF16, CW, NP, Src> stage(src, ncol, K, l0, cl, tid);
-    ScaleRegs<G ? G : 32, BF16> regs;
-    const int gn = G ? min(cl * kQ4Load / (G ? G : 1), q.ng - l0 * kQ4Load / (G ? G : 1)) : 0;
-    if constexpr (G > 0) regs.load(q, srow, l0 * kQ4Load / (G ? G : 1), gn, quad);
-    stage.load();
-    stage.arrived();
-    if constexpr (G > 0) regs.store(sc, gn, lane);  // (KS > 1: all waves the same values)
-    stage.store(lds);
-    __syncthreads();
-
-    // the products of load `l` of the stage (in register u of the round that starts at xb)
-    auto products = [&](int u, const uint4* xb, const float* sumb, const float2* scb) {
-      auto x_at = [&](int step, int t, int plane) {  // step within the round
-        return xb[slot[step & 3] + step * (4 * CW) + t * 16 + plane * (S::XS * 4 * CW)];
-      };
-      if constexpr (G == 0) {
+  // the products of register u, in a round that starts at xb, sumb and scb
+  auto products = [&](int u, const uint4* xb, const float* sumb, const float2* scb) {
+    auto x_at = [&](int step, int t, int plane) {  // step within the round
+      return xb[slot[step & 3] + step * (4 * CW) + t * 16 + plane * (S::XS * 4 * CW)];
+    };
+    if constexpr (G == 0) {
 #pragma unroll
-        for (int t = 0; t < S::T; ++t)
+      for (int t = 0; t < S::T; ++t)
 #pragma unroll
-          for (int pl = 0; pl < NP; ++pl) acc[t] = mma16<BF16>(wr[u], x_at(u, t, pl), acc[t]);
-      } else {
-        constexpr int SPG = G / 32;  // dwords (steps of 32 k's) of a group
-        uint32_t r[4] = {wr[u].x, wr[u].y, wr[u].z, wr[u].w};
-        if constexpr (G < 128) transpose_quads(r);
+        for (int pl = 0; pl < NP; ++pl) acc[t] = mma16<BF16>(wr[u], x_at(u, t, pl), acc[t]);
+    } else {
+      constexpr int SPG = G / 32;  // dwords (steps of 32 k's) of a group
+      uint32_t r[4] = {wr[u].x, wr[u].y, wr[u].z, wr[u].w};
+      if constexpr (G < 128) transpose_quads(r);
 #pragma unroll
-        for (int g = 0; g < 4 / SPG; ++g) {
-          f32x4_t prod[S::T];
+      for (int g = 0; g < GPL; ++g) {
+        f32x4_t prod[S::T];
 #pragma unroll
-          for (int t = 0; t < S::T; ++t) prod[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < S::T; ++t) prod[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int j = g * SPG; j < (g + 1) * SPG; ++j) {
-            if constexpr (BF16) {
-              const uint4 a = q4_bf16(r[j]);
+        for (int j = g * SPG; j < (g + 1) * SPG; ++j) {
+          if constexpr (BF16) {
+            const uint4 a = q4_bf16(r[j]);
 #pragma unroll
-              for (int t = 0; t < S::T; ++t)
+            for (int t = 0; t < S::T; ++t)
 #pragma unroll
-                for (int pl = 0; pl < NP; ++pl)
-                  prod[t] = mma_bf16(a, x_at(u * 4 + j, t, pl), prod[t]);
-            } else {
+              for (int pl = 0; pl < NP; ++pl)
+                prod[t] = mma_bf16(a, x_at(u * 4 + j, t, pl), prod[t]);
+          } else {
 #pragma unroll
-              for (int t = 0; t < S::T; ++t) {
+            for (int t = 0; t < S::T; ++t) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const uint4 x = x_at((u * 4 + j) * 2 + h, t, 0);
-                  const uint32_t xe[4] = {x.x, x.y, x.z, x.w};
+              for (int h = 0; h < 2; ++h) {
+                const uint4 x = x_at((u * 4 + j) * 2 + h, t, 0);
+                const uint32_t xe[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                  for (int i = 0; i < 4; ++i)
-                    prod[t] = mma_f32((float)((r[j] >> (16 * h + 4 * i)) & 15u),
-                                      __uint_as_float(xe[i]), prod[t]);
-                }
+                for (int i = 0; i < 4; ++i)
+                  prod[t] = mma_f32((float)((r[j] >> (16 * h + 4 * i)) & 15u),
+                                    __uint_as_float(xe[i]), prod[t]);
               }
             }
           }
-          constexpr int GPL = 4 / SPG;  // groups of a load
-          float2 f[4];
+        }
+        float2 f[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) f[i] = scb[(u * GPL + g) * kTileRows + i];
+        for (int i = 0; i < 4; ++i) f[i] = scb[(u * GPL + g) * kTileRows + i];
 #pragma unroll
-          for (int t = 0; t < S::T; ++t) {
-            const float sx = sumb[(u * GPL + g) * CW + t * 16];
+        for (int t = 0; t < S::T; ++t) {
+          const float sx = sumb[(u * GPL + g) * CW + t * 16];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              acc[t][i] = fmaf(-f[i].y, sx, fmaf(f[i].x, prod[t][i], acc[t][i]));
-          }
+          for (int i = 0; i < 4; ++i)
+            acc[t][i] = fmaf(-f[i].y, sx, fmaf(f[i].x, prod[t][i], acc[t][i]));
         }
       }
-    };
-    // this wave: loads first .. n - 1 of the stage (its part), in whole rounds and a shorter last
-    // one; there is no branch between the loads of a round
-    const int n = live ? min(first + part, loads - l0) : 0;
-    // a round's first slot, sum and scale (the offset is opaque to the compiler, which would
-    // otherwise keep an address register for every access of the round)
-    auto round = [&](int b, auto run) {
-      int o = b;
-      asm volatile("" : "+s"(o));
-      constexpr int GPR = G ? kQ4Load / (G ? G : 1) : 0;  // groups of a load
-      run(xs + o * (S::LX * 4 * CW), sums + o * (GPR * CW), sc + o * (GPR * kTileRows) + quad * 4);
-    };
-    int b = first;
-    for (; n - b > (S::R < S::U ? S::R : 0); b += S::U) {
-      round(b, [&](const uint4* xb, const float* sumb, const float2* scb) {
+    }
+  };
+
+  ScaleRegs<G ? G : 32, BF16> regs;
+  for (int tile = 0; tile < tiles; ++tile) {
+#pragma unroll
+    for (int t = 0; t < S::T; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int l0 = 0; l0 < loads; l0 += cl) {
+      const int g0 = l0 * GPL, gn = G ? min(cl * GPL, q.ng - g0) : 0;
+      if (!one_stage || tile == 0) {
+        __syncthreads();
+        StageX<S, G, BF16, CW, NP, Src> stage(src, ncol, K, l0, cl, tid);
+        if constexpr (G > 0) regs.load(q, row_at(tile), g0, gn, quad);
+        stage.load();
+        stage.arrived();
+        if constexpr (G > 0) regs.store(sc, gn, lane);  // (KS > 1: all waves the same values)
+        stage.store(lds);
+        __syncthreads();
+      } else if constexpr (G > 0) {
+        regs.store(sc, gn, lane);  // loaded while the last tile ran; this wave's own part of LDS
+      }
+      if constexpr (G > 0) {
+        if (one_stage && tile + 1 < tiles) regs.load(q, row_at(tile + 1), g0, gn, quad);
+      }
+      // this wave's loads of the stage, first .. n - 1, in whole rounds
+      const int n = min(first + part, loads - l0);
+      for (int b = first; b < n; b += S::U) {
+        // (the offset is opaque to the compiler, which would otherwise keep an address register
+        // for every access of the round)
+        int o = b;
+        asm volatile("" : "+s"(o));
+        const uint4* xb = xs + o * (S::LX * 4 * CW);
+        const float* sumb = sums + o * (GPL * CW);
+        const float2* scb = sc + o * (GPL * kTileRows) + quad * 4;
+        // the registers go on with the next round, the next stage or the next tile
+        const bool on = b + S::U < first + part, more = l0 + cl < loads;
+        const uint32_t ro = on || more ? here : next;
+        const int lo = on ? l0 + b + S::U : more ? l0 + cl + first : first;
 #pragma unroll
         for (int u = 0; u < S::U; ++u) {
           products(u, xb, sumb, scb);
-          // the next round's, or the next stage's first
-          const int nx = b + u + S::U;
-          wr[u] = load(nx < first + part ? l0 + nx : l0 + cl + nx - part);
+          wr[u] = load(ro, lo + u);
         }
-      });
+      }
     }
-    if (S::R < S::U && b < n) {  // (only in the row's last stage)
-      round(b, [&](const uint4* xb, const float* sumb, const float2* scb) {
+    here = next;
+    if (tile + 2 < tiles) next = off(tile + 2);
+    if constexpr (KS > 1) {
+      __syncthreads();
+      f32x4_t* red = reinterpret_cast<f32x4_t*>(lds);
+      red[wv * 64 + lane] = acc[0];
+      __syncthreads();
+      if (wv != 0) return;  // (one tile)
 #pragma unroll
-        for (int u = 0; u < S::R; ++u) products(u, xb, sumb, scb);
-      });
+      for (int i = 1; i < kWaves; ++i) acc[0] += red[i * 64 + lane];
     }
-  }
-  if constexpr (KS > 1) {
-    __syncthreads();
-    f32x4_t* red = reinterpret_cast<f32x4_t*>(lds);
-    red[wv * 64 + lane] = acc[0];
-    __syncthreads();
-    if (wv != 0) return;
 #pragma unroll
-    for (int i = 1; i < kWaves; ++i) acc[0] += red[i * 64 + lane];
-  }
-  if (live) {
-#pragma unroll
-    for (int t = 0; t < S::T; ++t) epilogue(t * 16 + col, acc[t]);
+    for (int t = 0; t < S::T; ++t) epilogue(tile, t * 16 + col, acc[t]);
   }
 }
 
@@ -493,29 +487,29 @@ template <int NP, int KS>
 constexpr int kPassCols = KS > 1 ? 16 : kMaxCols / NP;
 
 // As many columns as the pass has: 8 (twice the k's per stage), 16, 32 or 64.
-template <int G, bool BF16, int NP, int KS, class Src, class RowAt, class Epi>
-__device__ __forceinline__ void stream_cols(char* lds, const WeightRows& w, const Q4Tables& q,
-                                            RowAt row_at, bool live, const Src& src, int ncol,
-                                            int K, Epi epilogue) {
+template <int G, bool BF16, int NP, int KS, class Off, class Src, class RowAt, class Epi>
+__device__ __forceinline__ void stream_cols(char* lds, __amdgpu_buffer_rsrc_t rsrc, Off off,
+                                            int tiles, const Q4Tables& q, RowAt row_at,
+                                            const Src& src, int ncol, int K, Epi epi) {
   if (ncol <= 8) {
-    stream_rows<G, BF16, 8, NP, KS>(lds, w, q, row_at, live, src, ncol, K, epilogue);
+    stream_rows<G, BF16, 8, NP, KS>(lds, rsrc, off, tiles, q, row_at, src, ncol, K, epi);
   } else if (KS > 1 || ncol <= 16) {
-    stream_rows<G, BF16, 16, NP, KS>(lds, w, q, row_at, live, src, ncol, K, epilogue);
+    stream_rows<G, BF16, 16, NP, KS>(lds, rsrc, off, tiles, q, row_at, src, ncol, K, epi);
   } else if constexpr (KS == 1) {
     if (NP == 2 || ncol <= 32)
-      stream_rows<G, BF16, 32, NP, 1>(lds, w, q, row_at, live, src, ncol, K, epilogue);
+      stream_rows<G, BF16, 32, NP, 1>(lds, rsrc, off, tiles, q, row_at, src, ncol, K, epi);
     else if constexpr (NP == 1)
-      stream_rows<G, BF16, 64, NP, 1>(lds, w, q, row_at, live, src, ncol, K, epilogue);
+      stream_rows<G, BF16, 64, NP, 1>(lds, rsrc, off, tiles, q, row_at, src, ncol, K, epi);
   }
 }
 
-// The rows of this wave within a work item that begins at row n0: kItemRows rows, 16 a wave, or
-// (KS = kWaves) 16 rows for all.
+// Rows of a work item of `tiles` tiles a wave, and the first row of this wave's tile t in an item
+// that begins at row n0: a tile's rows are kItemRows apart, or (KS = kWaves) 16 rows for all.
+inline int item_rows(bool split, int tiles) { return split ? kTileRows : kItemRows * tiles; }
 template <int KS>
-constexpr int kItemRowsOf = KS > 1 ? kTileRows : kItemRows;
-template <int KS>
-__device__ __forceinline__ int wave_row0(int n0) {
-  return KS > 1 ? n0 : n0 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * kTileRows;
+__device__ __forceinline__ int tile_row0(int n0, int t) {
+  return KS > 1 ? n0
+                : n0 + t * kItemRows + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * kTileRows;
 }
 
 // bytes of one weight row of K elements
@@ -537,6 +531,17 @@ struct RowSrc {
     return {ld16(row + (uint32_t)v * 16u), make_uint4(0, 0, 0, 0)};
   }
 };
+
+// silu(g) = g / (1 + exp(-g)), to about 2^-22: the hardware's exp2 of -g log2(e), corrected by what
+// the product with log2(e) rounds away, and its reciprocal.
+__device__ __forceinline__ float silu(float g) {
+  constexpr float kL = 1.44269502f, kLlo = 1.92596303e-8f, kLn2 = 0.693147182f;
+  const float t = -g * kL;
+  const float lost = fmaf(-g, kLlo, fmaf(-g, kL, -t)) * kLn2;
+  const float e = __builtin_amdgcn_exp2f(t);
+  const float x = fabsf(t) < 126.f ? fmaf(e, lost, e) : e;  // (0 and infinity stay as they are)
+  return g * __builtin_amdgcn_rcpf(1.f + x);
+}
 
 template <bool BF16>
 __device__ __forceinline__ void store_elem(void* out, int64_t i, float v) {

@@ -774,10 +774,7 @@ MOL_API mol_status mol_moe_gemm_q4(int32_t dtype, const void* xin, int64_t ld_x,
   a.max_blocks = (int32_t)rc.max_blocks;
   // blocks that hold pairs: at most one partly filled per expert, beside the full ones
   const int64_t filled = std::min<int64_t>(numel, (int64_t)num_experts + numel / block_m);
-  const mol::ItemShape shape = mol::item_shape(filled, N);
-  a.split_k = shape.split;
-  a.item_tiles = shape.tiles;
-  a.items = (int32_t)shape.items;
+  a.items = (int32_t)mol::stream_items(filled, N, a.split_k);
   if (rc.max_blocks * a.items > kI32Max) return MOL_E_LIMIT;
   a.out = out;
   a.ld_out = ld_out;
@@ -896,21 +893,17 @@ MOL_API mol_status mol_moe_layer(const mol_moe_weights* w, const mol_moe_adapter
   a.rank_by_pair = a.numel <= V;
   a.rank_slots = adapters ? (int32_t)std::min<int64_t>(a.numel, V) : 0;
   a.direct = layer_direct(M, r);
-  const mol::ItemShape gu = mol::item_shape(a.slots, 2 * (int64_t)I);
-  const mol::ItemShape dn = mol::item_shape(a.slots, H);
+  const int64_t gu_items = mol::stream_items(a.slots, 2 * (int64_t)I, a.gu_split);
+  const int64_t dn_items = mol::stream_items(a.slots, H, a.dn_split);
   // every grid of the call: matrices x row groups, and direct down's columns x tokens
-  if (a.slots * gu.items + a.rank_slots > kI32Max || a.slots * dn.items + a.rank_slots > kI32Max ||
+  if (a.slots * gu_items + a.rank_slots > kI32Max || a.slots * dn_items + a.rank_slots > kI32Max ||
       ((int64_t)H + 128) * M > kI32Max)
     return MOL_E_LIMIT;
-  a.gu_split = gu.split;
-  a.gu_tiles = gu.tiles;
-  a.gu_items = (int32_t)gu.items;
-  a.dn_split = dn.split;
-  a.dn_tiles = dn.tiles;
-  a.dn_items = (int32_t)dn.items;
+  a.gu_items = (int32_t)gu_items;
+  a.dn_items = (int32_t)dn_items;
   a.f_topk = mol::make_fastdiv((uint32_t)topk);
-  a.f_gu_items = mol::make_fastdiv((uint32_t)gu.items);
-  a.f_dn_items = mol::make_fastdiv((uint32_t)dn.items);
+  a.f_gu_items = mol::make_fastdiv((uint32_t)gu_items);
+  a.f_dn_items = mol::make_fastdiv((uint32_t)dn_items);
   a.f_m = mol::make_fastdiv((uint32_t)M);
   return hip_status(mol::launch_moe_layer(a, bf16, (hipStream_t)stream));
 }

@@ -1,0 +1,10 @@
+// A whole mixture-of-experts layer for a few tokens: 4-bit weights in groups of 128.
+#include "moe_layer.h"
+
+namespace mol {
+
+hipError_t launch_moe_layer_q128(const LayerArgs& a, bool bf16, hipStream_t st) {
+  return launch_layer_group<128>(a, bf16, st);
+}
+
+}  // namespace mol

@@ -1,0 +1,84 @@
+// The base MoE grouped GEMM of a stage over 4-bit weights with group scales:
+//   out[p, n] = round( sum_k (q[t, n, k] - z[t, n, k / G]) s[t, n, k / G] x[p / row_div, k] )
+// for every pair p whose base expert t is local; other rows are untouched. Routed like the
+// dense grouped GEMM (the aligned blocks of one base expert each).
+//
+// At decode it reads half a byte of each touched weight once and little else, so a work item is
+// (block, 64 output columns): 64 rows of W_t, read once for up to 64 pairs of the block. Where that
+// makes too few items to fill the chip (split_k), an item is 16 rows whose k's the four waves
+// split.
+#pragma once
+
+#include "skinny.h"
+
+namespace mol {
+namespace {
+
+template <int G, bool BF16, int KS>
+__global__ void __launch_bounds__(kThreads, 3) q4_gemm_kernel(Q4GemmArgs a) {
+  constexpr int kCols = kPassCols<G, BF16, 1, KS>;
+  __shared__ int pair[kCols];
+  __shared__ __attribute__((aligned(16))) char lds[StreamLds<G, BF16>::kBytes];
+  const int blk = fdiv((int)blockIdx.x, a.f_items);
+  const int n0 = ((int)blockIdx.x - blk * a.items) * item_rows(KS > 1);
+  const int npp = *a.npp;
+  const int er = a.expert_ids[blk];
+  const int32_t* sorted = a.sorted + (int64_t)blk * a.BM;
+  // the first entries with the routing reads (their index stays inside the block)
+  int p = threadIdx.x < kCols && (int)threadIdx.x < a.BM ? sorted[threadIdx.x] : a.numel;
+  const int nb = npp < 0 ? 0 : fdiv(npp, a.f_bm);
+  if (blk >= nb || (unsigned)er >= (unsigned)a.E) return;
+  const int e = __builtin_amdgcn_readfirstlane(er);
+  const int64_t rb = a.K / 2, wbytes = (int64_t)a.N * rb;
+  const __amdgpu_buffer_rsrc_t rsrc = expert_rsrc((const char*)a.W + (int64_t)e * wbytes, wbytes);
+  const int lane = threadIdx.x & 63, quad = lane >> 4;
+  const Q4Tables q{a.scales, a.zeros, a.K / G};
+  const int r0 = wave_row0<KS>(n0), n = r0 + (lane & 15);
+  const uint32_t off = n < a.N ? (uint32_t)(n * rb) : kOutOfRange;
+  const int64_t srow = n < a.N ? (int64_t)e * a.N + n : (int64_t)-1;
+  const RowSrc src{(const char*)a.x, a.ld_x * (BF16 ? 2 : 4), pair, a.f_rd};
+  for (int j0 = 0; j0 < a.BM; j0 += kCols) {
+    if (j0 > 0) {
+      const int j = j0 + (int)threadIdx.x;
+      p = threadIdx.x < kCols && j < a.BM ? sorted[j] : a.numel;
+      __syncthreads();  // pair is no longer read
+    }
+    if (threadIdx.x < kCols) pair[threadIdx.x] = p;
+    __syncthreads();
+    // the real pairs are a prefix of the block
+    const int j = threadIdx.x & 63;
+    const int ncol = __popcll(
+        __builtin_amdgcn_ballot_w64(j < kCols && real_pair(pair[j < kCols ? j : 0], a.numel)));
+    if (ncol == 0) return;
+    stream_cols<G, BF16, 1, KS>(lds, rsrc, off, q, srow, src, ncol, a.K,
+                                [&](int c, const f32x4_t& acc) {
+      if (c >= ncol) return;
+      const int n = r0 + quad * 4;
+      const int64_t at = (int64_t)pair[c] * a.ld_out + n;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n + i < a.N) store_elem<BF16>(a.out, at + i, acc[i]);
+    });
+    if (ncol < kCols) return;
+  }
+}
+
+template <int G, bool BF16>
+hipError_t launch_gemm(const Q4GemmArgs& a, hipStream_t st) {
+  const dim3 grid(a.max_blocks * a.items);
+  if (a.split_k)
+    hipLaunchKernelGGL((q4_gemm_kernel<G, BF16, kWaves>), grid, dim3(kThreads), 0, st, a);
+  else
+    hipLaunchKernelGGL((q4_gemm_kernel<G, BF16, 1>), grid, dim3(kThreads), 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// The product over weights of group G: one translation unit each.
+template <int G>
+hipError_t launch_q4_group(const Q4GemmArgs& a, bool bf16, hipStream_t st) {
+  return bf16 ? launch_gemm<G, true>(a, st) : launch_gemm<G, false>(a, st);
+}
+
+}  // namespace mol

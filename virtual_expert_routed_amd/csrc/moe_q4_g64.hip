@@ -1,0 +1,10 @@
+// The base grouped GEMM over 4-bit weights: groups of 64.
+#include "moe_q4.h"
+
+namespace mol {
+
+hipError_t launch_q4_gemm_g64(const Q4GemmArgs& a, bool bf16, hipStream_t st) {
+  return launch_q4_group<64>(a, bf16, st);
+}
+
+}  // namespace mol

@@ -199,23 +199,15 @@ struct RouterArgs {
   float* weights;          // [M, topk]
 };
 
-// Work items of a stream of weight rows: 64 rows times `tiles`, or 16 rows whose k's four waves
-// split. All read the same bytes. Larger ones stage x less often, and need enough of them to
-// fill the chip's 256 CUs evenly.
-struct ItemShape {
-  bool split;
-  int tiles;
-  int64_t items;  // per matrix
-};
-int stream_item_rows(bool split, int tiles);
-inline ItemShape item_shape(int64_t matrices, int64_t rows) {
-  auto items = [&](bool split, int tiles) {
-    const int64_t n = stream_item_rows(split, tiles);
-    return (rows + n - 1) / n;
-  };
-  for (int tiles = 1; tiles >= 1; tiles /= 2)
-    if (matrices * items(false, tiles) >= 1024) return {false, tiles, items(false, tiles)};
-  return {true, 1, items(true, 1)};
+// Work items of a stream of weight rows: 64 rows, or 16 rows whose k's four waves split. Both
+// read the same bytes; the smaller ones are for launches whose larger ones would leave the chip's
+// 256 CUs with too few.
+int stream_item_rows(bool split);
+inline int64_t stream_items(int64_t matrices, int64_t rows, bool& split) {
+  auto items = [&] { return (rows + stream_item_rows(split) - 1) / stream_item_rows(split); };
+  split = false;
+  split = matrices * items() < 1024;
+  return items();
 }
 
 // The base grouped GEMM over 4-bit weights (group scales along K).
@@ -235,8 +227,7 @@ struct Q4GemmArgs {
   int32_t numel;
   int32_t BM;
   int32_t max_blocks;
-  bool split_k;            // item_shape()
-  int32_t item_tiles;
+  bool split_k;            // stream_items()
   int32_t items;           // work items per block
   void* out;               // [numel, ld_out]
   int64_t ld_out;
@@ -288,8 +279,7 @@ struct LayerArgs {
   int32_t rank_slots;      // adapter items: pairs (rank_by_pair) or virtual experts
   bool rank_by_pair;
   bool direct;             // down per token, with the combine
-  bool gu_split, dn_split; // item_shape() of gate/up and of down
-  int32_t gu_tiles, dn_tiles;
+  bool gu_split, dn_split; // stream_items() of gate/up and of down
   int32_t gu_items;        // row groups of gate/up and of down
   int32_t dn_items;
   FastDiv f_topk, f_gu_items, f_dn_items, f_m;
@@ -328,8 +318,13 @@ hipError_t launch_combine(const CombineArgs& a, bool bf16, hipStream_t stream);
 // fused expand + combine: ranks it is built for (R/8 or R/4 a power of two up to 16)
 bool fused_rank_supported(int32_t R, bool bf16);
 hipError_t launch_expand_combine(const CombineArgs& a, bool bf16, hipStream_t stream);
+hipError_t launch_q4_gemm_g32(const Q4GemmArgs& a, bool bf16, hipStream_t stream);
+hipError_t launch_q4_gemm_g64(const Q4GemmArgs& a, bool bf16, hipStream_t stream);
 hipError_t launch_q4_gemm(const Q4GemmArgs& a, bool bf16, hipStream_t stream);
 hipError_t launch_moe_layer(const LayerArgs& a, bool bf16, hipStream_t stream);
+hipError_t launch_moe_layer_q32(const LayerArgs& a, bool bf16, hipStream_t stream);
+hipError_t launch_moe_layer_q64(const LayerArgs& a, bool bf16, hipStream_t stream);
+hipError_t launch_moe_layer_q128(const LayerArgs& a, bool bf16, hipStream_t stream);
 hipError_t launch_moe_layer_direct(const LayerArgs& a, bool bf16, hipStream_t stream);
 hipError_t launch_router(const RouterArgs& a, bool bf16, hipStream_t stream);
 

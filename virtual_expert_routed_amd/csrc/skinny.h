@@ -41,7 +41,7 @@ constexpr int kTileRows = 16;
 constexpr int kWaves = kThreads / 64;
 constexpr int kItemRows = kWaves * kTileRows;  // weight rows of a tile of each wave
 constexpr int kMaxCols = 64;                   // columns of one pass, over the planes of x
-constexpr int kXBytes = 32768;                 // x staged at a time (four workgroups a CU)
+constexpr int kXHalf = 16384;                  // bytes of a stage of x, in one of two buffers
 constexpr int kQ4Load = 128;                   // k's of one load of 4-bit weights
 template <int G>
 constexpr int kMaxGroups = G == 128 ? 16 : 32;  // groups whose scales are staged at a time
@@ -145,32 +145,43 @@ __device__ __forceinline__ XVec split_vec(const float (&f)[BF16 ? 8 : 4]) {
 }
 
 // The shape of a stream: G the group of 4-bit weights (0: dense), CW columns, NP planes of x, KS
-// the waves that share 16 rows and split their k's (1 or kWaves).
-template <int G, bool BF16, int CW, int NP, int KS>
+// the waves that share 16 rows and split their k's (1 or kWaves), MULTI whether a row of x takes
+// several stages.
+template <int G, bool BF16, int CW, int NP, int KS, bool MULTI>
 struct Stream {
   static constexpr int VE = BF16 ? 8 : 4;                 // elements of a vector of x
   static constexpr int KL = G ? kQ4Load : 4 * VE;         // k's of a load of W
   static constexpr int LX = KL / (4 * VE);                // x steps (four vectors) of a load
-  static constexpr int XS = kXBytes / (64 * CW * NP);     // x steps staged at a time
+  static constexpr int XS = kXHalf / (64 * CW * NP);      // x steps of a stage
+  static constexpr int GPL = G ? kQ4Load / (G ? G : 1) : 0;  // groups of a load
   static constexpr int CLX = XS / LX;                     // loads of W whose x fits a stage
-  static constexpr int CLG = G ? kMaxGroups<G> * G / kQ4Load : CLX;  // and whose scales do
+  static constexpr int CLG = G ? kMaxGroups<G> / (G ? GPL : 1) : CLX;  // and whose scales do
   static constexpr int CL = CLX < CLG ? CLX : CLG;
   static constexpr int Q = CL / KS;                       // of them, one wave's
-  static constexpr int UM = G == 0 || G == 128 ? 8 : G == 64 ? 4 : 2;
-  static constexpr int U = Q < UM ? Q : UM;               // loads of W in flight: a round
+  // a row of up to this many loads is staged at once, through both buffers
+  static constexpr int ONE = G && 2 * CL > CLG ? CLG : 2 * CL;
+  // loads of W in flight, as many as the registers allow beside the next stage's x (4-bit: each
+  // load's products take many of them)
+  static constexpr int UM = G == 0 ? 8 : MULTI || G == 32 ? 2 : G == 64 ? 4 : 8;
+  static constexpr int U = Q < UM ? Q : UM;               // a round of loads
   static constexpr int T = CW > 16 ? CW / 16 : 1;         // matrix-core tiles of columns
   static constexpr int PERIOD = LX % 4 ? 4 : 1;           // loads between equal x rotations
+  static constexpr int PLANE = 2 * XS * 4 * CW;           // 16-byte slots of a plane (both buffers)
+  static constexpr int NV = CL * KL / VE;                 // vectors of a column in a stage
+  static constexpr int PER = (CW * NV + kThreads - 1) / kThreads;  // a thread's of a whole stage
   static_assert(Q >= 1 && Q % U == 0 && Q % PERIOD == 0 && U % PERIOD == 0,
                 "a wave's part of a stage is whole rounds of loads");
   static_assert(KS == 1 || T == 1, "split k's: one tile of columns");
+  static_assert((NV & (NV - 1)) == 0, "a stage's vectors are told apart by shifts");
 };
 
 // Bytes of LDS: x, then sums of x per group and column, then each wave's scales.
-template <int G>
+template <int G, bool BF16>
 struct StreamLds {
-  static constexpr int kSums = G ? kMaxGroups<G> * 16 * 4 : 0;
+  // (a stage of CW columns and NP planes has kXHalf / (64 CW NP) x steps)
+  static constexpr int kSums = G ? 2 * (kXHalf / 64 / (BF16 ? 4 : 8)) * (kQ4Load / (G ? G : 1)) * 4 : 0;
   static constexpr int kScales = G ? kWaves * kMaxGroups<G> * kTileRows * 8 : 0;
-  static constexpr int kBytes = kXBytes + kSums + kScales;
+  static constexpr int kBytes = 2 * kXHalf + kSums + kScales;
 };
 
 // 16-byte slot of x step `xs` (within the stage), quad, column: columns are rotated by the step
@@ -178,103 +189,116 @@ struct StreamLds {
 // step) spread over the banks.
 template <int CW>
 __device__ __forceinline__ int x_rot(int xs, int quad) {  // has period 4 in xs
-  return CW == 8 ? ((xs * 4 + quad) >> 1) & 7 : (xs * 4 + quad) & 15;
+  return CW == 4 ? xs & 3 : CW == 8 ? ((xs * 4 + quad) >> 1) & 7 : (xs * 4 + quad) & 15;
 }
 template <int CW>
 __device__ __forceinline__ int x_slot(int xs, int quad, int col) {
   return (xs * 4 + quad) * CW + (col ^ x_rot<CW>(xs, quad));
 }
 
-// Stages columns [0, ncol) (ncol >= 1) of x for loads [l0, l0 + cl): src.row(c) is column c's
-// row (uniform), src(row, v) its vector v (v < K / VE), an XVec whose lo counts for NP = 2. Units
-// of 64 vectors of one column go round the waves, NB of them in flight: load() takes the first
-// ones, store() puts them in LDS and goes on with the rest. Every load is issued, on clamped
-// indices, so that no branch stands between loads.
-template <class S, int G, bool BF16, int CW, int NP, class Src>
-struct StageX {
-  static constexpr int GV = G ? G / S::VE : 1;  // vectors of a group
-  static constexpr int NB = NP == 2 ? 2 : 4;
-  static constexpr int VL = S::KL / S::VE;      // vectors of a load
-  const Src& src;
-  int ncol, lane, v0, vend, nv, nb, inv, unit;
-  XVec x[NB];
+// Puts vector v of column c of a stage into LDS: planes at xs, sums of 4-bit groups at sums. The
+// lanes of a group are consecutive, all of them here.
+template <class S, int G, bool BF16, int CW, int NP>
+__device__ __forceinline__ void put_x(uint4* xs, float* sums, int c, int v, const XVec& x) {
+  constexpr int GV = G ? G / S::VE : 1;  // vectors of a group
+  int step, quad;
+  if constexpr (G == 0) {
+    step = v >> 2;
+    quad = v & 3;
+  } else {
+    constexpr int VD = 8 / S::VE;  // vectors of a dword of W (8 k's)
+    const int d = v / VD;          // dword of the row
+    const int j = G == 128 ? d & 3 : (d >> 2) & 3;
+    quad = G == 128 ? (d >> 2) & 3 : d & 3;
+    step = ((d >> 4) * 4 + j) * VD + v % VD;
+  }
+  const int at = x_slot<CW>(step, quad, c);
+  if constexpr (G > 0 && BF16) {
+    xs[at] = q4_order(x.hi);
+    if constexpr (NP == 2) xs[S::PLANE + at] = q4_order(x.lo);
+  } else {
+    xs[at] = x.hi;
+    if constexpr (NP == 2) xs[S::PLANE + at] = x.lo;
+  }
+  if constexpr (G > 0) {
+    float sum = vec_sum<BF16>(x.hi, 0.f);
+    if constexpr (NP == 2) sum = vec_sum<BF16>(x.lo, sum);
+    sum = group_sum<GV>(sum);
+    if ((v & (GV - 1)) == 0) sums[v / GV * CW + c] = sum;
+  }
+}
 
-  __device__ __forceinline__ StageX(const Src& src_, int ncol_, int K, int l0, int cl, int tid)
-      : src(src_), ncol(ncol_), lane(tid & 63) {
-    v0 = l0 * VL;
-    vend = K / S::VE;
-    // the row is filled up with zeros to whole rounds of loads (what a load past the row's end
-    // returns, times a stale infinity, would not be zero)
-    constexpr int VR = VL * S::U;
-    nv = min(cl * VL, (vend - v0 + VR - 1) / VR * VR);
-    nb = (nv + 63) >> 6;
-    inv = 65536 / nb + 1;  // u / nb = u * inv >> 16 for the units of a stage (below 2^12)
-    unit = __builtin_amdgcn_readfirstlane(tid >> 6);
+// The loads stay where they are issued: used here by all lanes, they cannot sink into the conditions
+// of the stores, where each would be waited for on its own.
+template <int NP, int N>
+__device__ __forceinline__ void arrived(const XVec (&x)[N]) {
+#pragma unroll
+  for (int b = 0; b < N; ++b) {
+    asm volatile("" ::"v"(x[b].hi.x), "v"(x[b].hi.y), "v"(x[b].hi.z), "v"(x[b].hi.w));
+    if constexpr (NP == 2)
+      asm volatile("" ::"v"(x[b].lo.x), "v"(x[b].lo.y), "v"(x[b].lo.z), "v"(x[b].lo.w));
   }
-  __device__ __forceinline__ int column(int u) const { return (u * inv) >> 16; }
-  __device__ __forceinline__ int vector(int u) const {
-    return (u - column(u) * nb) * 64 + lane;
-  }
-  __device__ __forceinline__ void load() {
+}
+
+__device__ __forceinline__ uint4 vec_if(const uint4& v, bool ok) {
+  return make_uint4(ok ? v.x : 0u, ok ? v.y : 0u, ok ? v.z : 0u, ok ? v.w : 0u);
+}
+template <int NP>
+__device__ __forceinline__ XVec xvec_if(const XVec& x, bool ok) {
+  return {vec_if(x.hi, ok), NP == 2 ? vec_if(x.lo, ok) : x.lo};
+}
+
+// A whole row of columns [0, ncol), ncol >= 1: src.row(c) is column c's row (c uniform), src(row,
+// v) its vector v, an XVec whose lo counts for NP = 2. Units of 64 vectors of one column go round the
+// waves, NB of them in flight; every load is issued, on clamped indices, so that no branch
+// stands between loads. The row is filled up with zeros to whole rounds of loads (what a load of W
+// past the row's end returns, times a stale infinity, would not be zero).
+template <class S, int G, bool BF16, int CW, int NP, class Src>
+__device__ __forceinline__ void stage_row(uint4* xs, float* sums, const Src& src, int ncol, int K,
+                                          int tid) {
+  constexpr int NB = NP == 2 ? 2 : 4;
+  constexpr int VR = S::KL / S::VE * S::U;  // vectors of a round of loads
+  const int vend = K / S::VE, nv = (vend + VR - 1) / VR * VR, nb = (nv + 63) >> 6;
+  const int inv = 65536 / nb + 1;  // u / nb = u * inv >> 16 for these units (below 2^12)
+  const int units = ncol * nb, lane = tid & 63;
+  for (int unit = __builtin_amdgcn_readfirstlane(tid >> 6); unit < units; unit += NB * kWaves) {
+    XVec x[NB];
+    int c[NB], v[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       const int u = unit + b * kWaves;
-      const int c = column(u), v = v0 + vector(u);
-      x[b] = src(src.row(min(c, ncol - 1)), min(v, vend - 1));
+      c[b] = (u * inv) >> 16;
+      v[b] = (u - c[b] * nb) * 64 + lane;
+      x[b] = src(src.row(min(c[b], ncol - 1)), min(v[b], vend - 1));
+    }
+    arrived<NP>(x);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      if (c[b] < ncol && v[b] < nv)
+        put_x<S, G, BF16, CW, NP>(xs, sums, c[b], v[b], xvec_if<NP>(x[b], v[b] < vend));
+  }
+}
+
+// One of several stages, on its way through registers while the one before it is at work: vectors
+// v0 .. v0 + S::NV - 1 of every column; src.lane_row(c) is column c's row, c of the lane's own.
+template <class S, int G, bool BF16, int CW, int NP, class Src>
+struct StageRegs {
+  XVec x[S::PER];
+  __device__ __forceinline__ void load(const Src& src, int ncol, int v0, int vend, int tid) {
+#pragma unroll
+    for (int b = 0; b < S::PER; ++b) {
+      const int i = b * kThreads + tid, c = i / S::NV, v = v0 + i % S::NV;
+      x[b] = src(src.lane_row(min(c, ncol - 1)), min(v, vend - 1));
     }
   }
-  // The loads stay where they are issued: used here by all lanes, they cannot sink into store()'s
-  // conditions, where each would be waited for on its own.
-  __device__ __forceinline__ void arrived() const {
+  __device__ __forceinline__ void store(uint4* xs, float* sums, int ncol, int v0, int vend,
+                                        int tid) {
+    arrived<NP>(x);
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      asm volatile("" ::"v"(x[b].hi.x), "v"(x[b].hi.y), "v"(x[b].hi.z), "v"(x[b].hi.w));
-      if constexpr (NP == 2)
-        asm volatile("" ::"v"(x[b].lo.x), "v"(x[b].lo.y), "v"(x[b].lo.z), "v"(x[b].lo.w));
-    }
-  }
-  __device__ __forceinline__ void store(char* lds) {
-    uint4* xs = reinterpret_cast<uint4*>(lds);
-    float* sums = reinterpret_cast<float*>(lds + kXBytes);
-    const int units = ncol * nb;
-    for (;;) {
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const int u = unit + b * kWaves;
-        const int c = column(u), v = vector(u);
-        if (c < ncol && v < nv) {
-          int step, quad;
-          if constexpr (G == 0) {
-            step = v >> 2;
-            quad = v & 3;
-          } else {
-            constexpr int VD = 8 / S::VE;  // vectors of a dword of W (8 k's)
-            const int d = v / VD;          // dword of the row
-            const int j = G == 128 ? d & 3 : (d >> 2) & 3;
-            quad = G == 128 ? (d >> 2) & 3 : d & 3;
-            step = ((d >> 4) * 4 + j) * VD + v % VD;
-          }
-          const int at = x_slot<CW>(step, quad, c);
-          if (v0 + v >= vend) x[b] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-          if constexpr (G > 0 && BF16) {
-            xs[at] = q4_order(x[b].hi);
-            if constexpr (NP == 2) xs[S::XS * 4 * CW + at] = q4_order(x[b].lo);
-          } else {
-            xs[at] = x[b].hi;
-            if constexpr (NP == 2) xs[S::XS * 4 * CW + at] = x[b].lo;
-          }
-          if constexpr (G > 0) {  // the lanes of a group are consecutive, all of them here
-            float sum = vec_sum<BF16>(x[b].hi, 0.f);
-            if constexpr (NP == 2) sum = vec_sum<BF16>(x[b].lo, sum);
-            sum = group_sum<GV>(sum);
-            if ((v & (GV - 1)) == 0) sums[v / GV * CW + c] = sum;
-          }
-        }
-      }
-      unit += NB * kWaves;
-      if (unit >= units) break;
-      load();
-      arrived();
+    for (int b = 0; b < S::PER; ++b) {
+      const int i = b * kThreads + tid, c = i / S::NV, v = i % S::NV;
+      if (c < ncol)
+        put_x<S, G, BF16, CW, NP>(xs, sums, c, v, xvec_if<NP>(x[b], v0 + v < vend));
     }
   }
 };
@@ -317,30 +341,27 @@ struct ScaleRegs {
   }
 };
 
-// Runs one item against ncol staged columns: `tiles` tiles of this wave, one after another (KS = 1),
-// the same x serving all of them when a row's x fits one stage; with KS = kWaves the waves have
-// the same rows and split their k's. off(t): this lane's row of tile t (lane % 16) as a byte
-// offset into the matrix, kOutOfRange for none; row_at(t): its row in the scale tables, negative
-// for none. epilogue(t, col, acc) gets, on every lane (of wave 0 for KS = kWaves), column
-// col's sums of tile rows 4 * quad + i; only columns below ncol and rows that exist are
-// meant. All four waves take part in the barriers; on return LDS may still be read by slower
-// waves.
-template <int G, bool BF16, int CW, int NP, int KS, class Off, class Src, class RowAt, class Epi>
-__device__ __forceinline__ void stream_rows(char* lds, __amdgpu_buffer_rsrc_t rsrc, Off off,
-                                            int tiles, const Q4Tables& q, RowAt row_at,
-                                            const Src& src, int ncol, int K, Epi epilogue) {
-  using S = Stream<G, BF16, CW, NP, KS>;
+// Runs one item against ncol columns: this wave's 16 rows, or with KS = kWaves the same rows in
+// all waves, which split their k's. off: this lane's row (lane % 16) as a byte offset into the
+// matrix, kOutOfRange for none; srow: its row in the scale tables, negative for none.
+// epilogue(col, acc) gets, on every lane (of wave 0 for KS = kWaves), column col's sums of tile
+// rows 4 * quad + i; only columns below ncol and rows that exist are meant. All four waves take
+// part in the barriers; on return LDS may still be read by slower waves.
+template <int G, bool BF16, int CW, int NP, int KS, bool MULTI, class Src, class Epi>
+__device__ __forceinline__ void stream_rows(char* lds, __amdgpu_buffer_rsrc_t rsrc, uint32_t off,
+                                            const Q4Tables& q, int64_t srow, const Src& src,
+                                            int ncol, int K, Epi epilogue) {
+  using S = Stream<G, BF16, CW, NP, KS, MULTI>;
   // (opaque to the compiler, which would otherwise compute every variant's addresses ahead of the
   // loop over passes and spill them)
   int tid = threadIdx.x;
   asm volatile("" : "+v"(tid));
   const int lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, quad = lane >> 4;
-  const int loads = (K + S::KL - 1) / S::KL;
+  const int loads = (K + S::KL - 1) / S::KL, vend = K / S::VE;
   // loads per stage, and this wave's part of them: one stage is split evenly
   int cl = S::CL, part = S::Q, first = 0;
-  const bool one_stage = loads <= S::CL;
-  if (one_stage) {
+  if constexpr (!MULTI) {
     part = ((loads + KS - 1) / KS + S::U - 1) / S::U * S::U;
     cl = part * KS;
   }
@@ -348,29 +369,30 @@ __device__ __forceinline__ void stream_rows(char* lds, __amdgpu_buffer_rsrc_t rs
   // every load is issued: past the row (and for rows that are not there) it reads zeros and
   // moves nothing
   const int k_left = K - quad * (S::KL / 4);  // k's from this lane's part of load 0 on
-  auto load = [&](uint32_t row_off, int l) {
-    return buf16(rsrc, l * S::KL < k_left ? row_off + (uint32_t)quad * 16u + (uint32_t)l * 64u
-                                          : kOutOfRange);
+  const uint32_t lane_off = off + (uint32_t)quad * 16u;
+  auto load = [&](int l) __attribute__((always_inline)) {
+    return buf16(rsrc, l * S::KL < k_left ? lane_off + (uint32_t)l * 64u : kOutOfRange);
   };
-  uint32_t here = off(0), next = tiles > 1 ? off(1) : kOutOfRange;
   uint4 wr[S::U];
 #pragma unroll
-  for (int u = 0; u < S::U; ++u) wr[u] = load(here, first + u);
+  for (int u = 0; u < S::U; ++u) wr[u] = load(first + u);
   f32x4_t acc[S::T];
+#pragma unroll
+  for (int t = 0; t < S::T; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   // this lane's slots of x steps 0-3 (the rotation's period) relative to the step's first slot
   int slot[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) slot[i] = quad * CW + ((col & (CW - 1)) ^ x_rot<CW>(i, quad));
-  const uint4* xs = reinterpret_cast<const uint4*>(lds);
-  const float* sums = reinterpret_cast<const float*>(lds + kXBytes) + (col & (CW - 1));
-  float2* sc = reinterpret_cast<float2*>(lds + kXBytes + StreamLds<G>::kSums) +
-               (KS > 1 ? 0 : wv) * (kMaxGroups<G> * kTileRows);
-  constexpr int GPL = G ? kQ4Load / (G ? G : 1) : 0;  // groups of a load
+  uint4* const xs = reinterpret_cast<uint4*>(lds);
+  float* const sums = reinterpret_cast<float*>(lds + 2 * kXHalf);
+  float2* const sc = reinterpret_cast<float2*>(lds + 2 * kXHalf + StreamLds<G, BF16>::kSums) +
+                     (KS > 1 ? 0 : wv) * (kMaxGroups<G> * kTileRows);
 
   // the products of register u, in a round that starts at xb, sumb and scb
-  auto products = [&](int u, const uint4* xb, const float* sumb, const float2* scb) {
-    auto x_at = [&](int step, int t, int plane) {  // step within the round
-      return xb[slot[step & 3] + step * (4 * CW) + t * 16 + plane * (S::XS * 4 * CW)];
+  auto products = [&](int u, const uint4* xb, const float* sumb, const float2* scb)
+                      __attribute__((always_inline)) {
+    auto x_at = [&](int step, int t, int plane) __attribute__((always_inline)) {  // of the round
+      return xb[slot[step & 3] + step * (4 * CW) + t * 16 + plane * S::PLANE];
     };
     if constexpr (G == 0) {
 #pragma unroll
@@ -382,7 +404,7 @@ __device__ __forceinline__ void stream_rows(char* lds, __amdgpu_buffer_rsrc_t rs
       uint32_t r[4] = {wr[u].x, wr[u].y, wr[u].z, wr[u].w};
       if constexpr (G < 128) transpose_quads(r);
 #pragma unroll
-      for (int g = 0; g < GPL; ++g) {
+      for (int g = 0; g < S::GPL; ++g) {
         f32x4_t prod[S::T];
 #pragma unroll
         for (int t = 0; t < S::T; ++t) prod[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -412,10 +434,10 @@ __device__ __forceinline__ void stream_rows(char* lds, __amdgpu_buffer_rsrc_t rs
         }
         float2 f[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = scb[(u * GPL + g) * kTileRows + i];
+        for (int i = 0; i < 4; ++i) f[i] = scb[(u * S::GPL + g) * kTileRows + i];
 #pragma unroll
         for (int t = 0; t < S::T; ++t) {
-          const float sx = sumb[(u * GPL + g) * CW + t * 16];
+          const float sx = sumb[(u * S::GPL + g) * CW + t * 16];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             acc[t][i] = fmaf(-f[i].y, sx, fmaf(f[i].x, prod[t][i], acc[t][i]));
@@ -423,93 +445,122 @@ __device__ __forceinline__ void stream_rows(char* lds, __amdgpu_buffer_rsrc_t rs
       }
     }
   };
+  // a round: registers' loads b .. b + U - 1 of the stage at xs_, sums_, refilled from load `next` on
+  auto round = [&](const uint4* xs_, const float* sums_, int b, int next)
+                   __attribute__((always_inline)) {
+    // (the offset is opaque to the compiler, which would otherwise keep an address register for
+    // every access of the round)
+    int o = b;
+    asm volatile("" : "+s"(o));
+    const uint4* xb = xs_ + o * (S::LX * 4 * CW);
+    const float* sumb = sums_ + o * (S::GPL * CW) + (col & (CW - 1));
+    const float2* scb = sc + o * (S::GPL * kTileRows) + quad * 4;
+#pragma unroll
+    for (int u = 0; u < S::U; ++u) {
+      products(u, xb, sumb, scb);
+      wr[u] = load(next + u);
+    }
+  };
 
   ScaleRegs<G ? G : 32, BF16> regs;
-  for (int tile = 0; tile < tiles; ++tile) {
-#pragma unroll
-    for (int t = 0; t < S::T; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    for (int l0 = 0; l0 < loads; l0 += cl) {
-      const int g0 = l0 * GPL, gn = G ? min(cl * GPL, q.ng - g0) : 0;
-      if (!one_stage || tile == 0) {
-        __syncthreads();
-        StageX<S, G, BF16, CW, NP, Src> stage(src, ncol, K, l0, cl, tid);
-        if constexpr (G > 0) regs.load(q, row_at(tile), g0, gn, quad);
-        stage.load();
-        stage.arrived();
-        if constexpr (G > 0) regs.store(sc, gn, lane);  // (KS > 1: all waves the same values)
-        stage.store(lds);
-        __syncthreads();
-      } else if constexpr (G > 0) {
-        regs.store(sc, gn, lane);  // loaded while the last tile ran; this wave's own part of LDS
-      }
-      if constexpr (G > 0) {
-        if (one_stage && tile + 1 < tiles) regs.load(q, row_at(tile + 1), g0, gn, quad);
-      }
-      // this wave's loads of the stage, first .. n - 1, in whole rounds
-      const int n = min(first + part, loads - l0);
-      for (int b = first; b < n; b += S::U) {
-        // (the offset is opaque to the compiler, which would otherwise keep an address register
-        // for every access of the round)
-        int o = b;
-        asm volatile("" : "+s"(o));
-        const uint4* xb = xs + o * (S::LX * 4 * CW);
-        const float* sumb = sums + o * (GPL * CW);
-        const float2* scb = sc + o * (GPL * kTileRows) + quad * 4;
-        // the registers go on with the next round, the next stage or the next tile
-        const bool on = b + S::U < first + part, more = l0 + cl < loads;
-        const uint32_t ro = on || more ? here : next;
-        const int lo = on ? l0 + b + S::U : more ? l0 + cl + first : first;
-#pragma unroll
-        for (int u = 0; u < S::U; ++u) {
-          products(u, xb, sumb, scb);
-          wr[u] = load(ro, lo + u);
-        }
-      }
-    }
-    here = next;
-    if (tile + 2 < tiles) next = off(tile + 2);
-    if constexpr (KS > 1) {
+  auto groups_at = [&](int l0) { return min(cl * S::GPL, q.ng - l0 * S::GPL); };
+  if constexpr (G > 0) regs.load(q, srow, 0, groups_at(0), quad);
+  if constexpr (!MULTI) {
+    __syncthreads();
+    stage_row<S, G, BF16, CW, NP>(xs, sums, src, ncol, K, tid);
+    if constexpr (G > 0) regs.store(sc, groups_at(0), lane);  // (KS > 1: all waves the same values)
+    __syncthreads();
+    const int n = min(first + part, loads);
+    for (int b = first; b < n; b += S::U)
+      round(xs, sums, b, b + S::U < first + part ? b + S::U : loads);
+  } else {
+    // stages alternate between the two buffers; the next one's x and scales load while one works
+    StageRegs<S, G, BF16, CW, NP, Src> stage;
+    stage.load(src, ncol, 0, vend, tid);
+    __syncthreads();
+    stage.store(xs, sums, ncol, 0, vend, tid);
+    int buf = 0;
+    for (int l0 = 0; l0 < loads; l0 += S::CL, buf ^= 1) {
+      if constexpr (G > 0) regs.store(sc, groups_at(l0), lane);
       __syncthreads();
-      f32x4_t* red = reinterpret_cast<f32x4_t*>(lds);
-      red[wv * 64 + lane] = acc[0];
-      __syncthreads();
-      if (wv != 0) return;  // (one tile)
-#pragma unroll
-      for (int i = 1; i < kWaves; ++i) acc[0] += red[i * 64 + lane];
+      const int l1 = l0 + S::CL, v1 = l1 * (S::KL / S::VE);
+      const bool more = l1 < loads;
+      int t1 = tid;  // (opaque again: addresses are computed anew for each stage, not kept)
+      asm volatile("" : "+v"(t1));
+      if (more) {
+        if constexpr (G > 0) regs.load(q, srow, l1 * S::GPL, groups_at(l1), (t1 & 63) >> 4);
+        stage.load(src, ncol, v1, vend, t1);
+      }
+      const uint4* xh = xs + buf * (S::XS * 4 * CW);
+      const float* sh = sums + buf * (S::CLX * S::GPL * CW);
+#pragma unroll 1
+      for (int b = 0; b < S::Q; b += S::U)
+        round(xh, sh, first + b, b + S::U < S::Q ? l0 + first + b + S::U : l1 + first);
+      if (more)
+        stage.store(xs + (buf ^ 1) * (S::XS * 4 * CW), sums + (buf ^ 1) * (S::CLX * S::GPL * CW), ncol,
+                    v1, vend, t1);
+      // (KS > 1: the waves share the scales, which the next turn stores)
+      if constexpr (G > 0 && KS > 1) __syncthreads();
     }
-#pragma unroll
-    for (int t = 0; t < S::T; ++t) epilogue(tile, t * 16 + col, acc[t]);
   }
+  if constexpr (KS > 1) {
+    __syncthreads();
+    f32x4_t* red = reinterpret_cast<f32x4_t*>(lds);
+    red[wv * 64 + lane] = acc[0];
+    __syncthreads();
+    if (wv != 0) return;
+#pragma unroll
+    for (int i = 1; i < kWaves; ++i) acc[0] += red[i * 64 + lane];
+  }
+#pragma unroll
+  for (int t = 0; t < S::T; ++t) epilogue(t * 16 + col, acc[t]);
 }
 
 // The most columns of a pass.
-template <int NP, int KS>
-constexpr int kPassCols = KS > 1 ? 16 : kMaxCols / NP;
+template <int G, bool BF16, int NP, int KS>
+constexpr int kPassCols = KS > 1 ? 8 : (G && !BF16) || NP == 2 ? 32 : kMaxCols;
 
-// As many columns as the pass has: 8 (twice the k's per stage), 16, 32 or 64.
-template <int G, bool BF16, int NP, int KS, class Off, class Src, class RowAt, class Epi>
-__device__ __forceinline__ void stream_cols(char* lds, __amdgpu_buffer_rsrc_t rsrc, Off off,
-                                            int tiles, const Q4Tables& q, RowAt row_at,
-                                            const Src& src, int ncol, int K, Epi epi) {
-  if (ncol <= 8) {
-    stream_rows<G, BF16, 8, NP, KS>(lds, rsrc, off, tiles, q, row_at, src, ncol, K, epi);
-  } else if (KS > 1 || ncol <= 16) {
-    stream_rows<G, BF16, 16, NP, KS>(lds, rsrc, off, tiles, q, row_at, src, ncol, K, epi);
-  } else if constexpr (KS == 1) {
-    if (NP == 2 || ncol <= 32)
-      stream_rows<G, BF16, 32, NP, 1>(lds, rsrc, off, tiles, q, row_at, src, ncol, K, epi);
-    else if constexpr (NP == 1)
-      stream_rows<G, BF16, 64, NP, 1>(lds, rsrc, off, tiles, q, row_at, src, ncol, K, epi);
+// The stream of a row of K: staged at once where its x fits both buffers, else in several stages.
+template <int G, bool BF16, int CW, int NP, int KS, class Src, class Epi>
+__device__ __forceinline__ void stream_k(char* lds, __amdgpu_buffer_rsrc_t rsrc, uint32_t off,
+                                         const Q4Tables& q, int64_t srow, const Src& src, int ncol,
+                                         int K, Epi epi) {
+  using S = Stream<G, BF16, CW, NP, KS, false>;
+  if constexpr (CW <= 16) {
+    if (K <= S::ONE * S::KL) {
+      stream_rows<G, BF16, CW, NP, KS, false>(lds, rsrc, off, q, srow, src, ncol, K, epi);
+      return;
+    }
+  }
+  stream_rows<G, BF16, CW, NP, KS, true>(lds, rsrc, off, q, srow, src, ncol, K, epi);
+}
+
+// As many columns as the pass has: 4, 8, 16, 32 or 64.
+template <int G, bool BF16, int NP, int KS, class Src, class Epi>
+__device__ __forceinline__ void stream_cols(char* lds, __amdgpu_buffer_rsrc_t rsrc, uint32_t off,
+                                            const Q4Tables& q, int64_t srow, const Src& src,
+                                            int ncol, int K, Epi epi) {
+  constexpr int MOST = kPassCols<G, BF16, NP, KS>;
+  if (ncol <= 4) {
+    stream_k<G, BF16, 4, NP, KS>(lds, rsrc, off, q, srow, src, ncol, K, epi);
+  } else if (MOST == 8 || ncol <= 8) {
+    stream_k<G, BF16, 8, NP, KS>(lds, rsrc, off, q, srow, src, ncol, K, epi);
+  } else if constexpr (MOST > 8) {
+    if (ncol <= 16)
+      stream_k<G, BF16, 16, NP, 1>(lds, rsrc, off, q, srow, src, ncol, K, epi);
+    else if (MOST == 32 || ncol <= 32)
+      stream_k<G, BF16, 32, NP, 1>(lds, rsrc, off, q, srow, src, ncol, K, epi);
+    else if constexpr (MOST > 32)
+      stream_k<G, BF16, 64, NP, 1>(lds, rsrc, off, q, srow, src, ncol, K, epi);
   }
 }
 
-// Rows of a work item of `tiles` tiles a wave, and the first row of this wave's tile t in an item
-// that begins at row n0: a tile's rows are kItemRows apart, or (KS = kWaves) 16 rows for all.
-inline int item_rows(bool split, int tiles) { return split ? kTileRows : kItemRows * tiles; }
+// Rows of a work item, and the first row of this wave in an item that begins at row n0: 16 a wave,
+// or (KS = kWaves) 16 for all.
+constexpr int item_rows(bool split) { return split ? kTileRows : kItemRows; }
 template <int KS>
-__device__ __forceinline__ int tile_row0(int n0, int t) {
-  return KS > 1 ? n0
-                : n0 + t * kItemRows + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * kTileRows;
+__device__ __forceinline__ int wave_row0(int n0) {
+  return KS > 1 ? n0 : n0 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * kTileRows;
 }
 
 // bytes of one weight row of K elements
@@ -526,6 +577,9 @@ struct RowSrc {
   FastDiv row_div;
   __device__ __forceinline__ const char* row(int col) const {
     return x + (int64_t)fdiv(__builtin_amdgcn_readfirstlane(pair[col]), row_div) * ld_bytes;
+  }
+  __device__ __forceinline__ const char* lane_row(int col) const {
+    return x + (int64_t)fdiv(pair[col], row_div) * ld_bytes;
   }
   __device__ __forceinline__ XVec operator()(const char* row, int v) const {
     return {ld16(row + (uint32_t)v * 16u), make_uint4(0, 0, 0, 0)};

@@ -369,20 +369,33 @@ def mol_moe_gemm(xin, row_div: int, W, sorted_ids, expert_ids, num_post_padded, 
 
 def _on(dev, name: str, t: torch.Tensor, dtype, shape):
     """t is on dev, contiguous, of this dtype and shape."""
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev}, got {t.device}")
     _need(t, name, dtype)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+_fns = {}  # entry points by name
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
 def _call(dev, fn: str, *args) -> None:
     """The entry point on dev's current stream, with dev current for the launch."""
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        _check(fn, getattr(lib(), fn)(*args, torch.cuda.current_stream(dev).cuda_stream))
+    if dev.type != "cuda":
+        raise ValueError(f"{fn} needs device tensors, got {dev}")
+    f = _fns.get(fn)
+    if f is None:
+        f = _fns[fn] = getattr(lib(), fn)
+    if dev.index == torch.cuda.current_device():
+        status = f(*args, _raw_stream(dev.index))
     else:
         with torch.cuda.device(dev):
-            _check(fn, getattr(lib(), fn)(*args, torch.cuda.current_stream(dev).cuda_stream))
+            status = f(*args, _raw_stream(dev.index))
+    if status != MOL_OK:
+        raise MolError(fn, status)
 
 
 def mol_router_topk(logits, topk: int, scoring: int = MOL_SCORE_SOFTMAX,
@@ -390,19 +403,20 @@ def mol_router_topk(logits, topk: int, scoring: int = MOL_SCORE_SOFTMAX,
                     num_local: int = None, topk_ids=None, topk_weights=None):
     """The top-k experts of each token from router logits [M, E] (rows may be strided):
     (topk_ids int32 [M, topk], topk_weights float32 [M, topk])."""
-    _need(logits, "logits", contiguous=False)
     if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
         raise ValueError("logits must be 2-d with contiguous rows")
     M, E = logits.shape
     dev = logits.device
     if topk_ids is None:
         topk_ids = torch.empty((M, topk), dtype=torch.int32, device=dev)
+    else:
+        _on(dev, "topk_ids", topk_ids, torch.int32, (M, topk))
     if topk_weights is None:
         topk_weights = torch.empty((M, topk), dtype=torch.float32, device=dev)
-    _on(dev, "topk_ids", topk_ids, torch.int32, (M, topk))
-    _on(dev, "topk_weights", topk_weights, torch.float32, (M, topk))
+    else:
+        _on(dev, "topk_weights", topk_weights, torch.float32, (M, topk))
     _call(dev, "mol_router_topk", _dtype_code(logits), logits.data_ptr(),
-          max(logits.stride(0), E) if M <= 1 else logits.stride(0), M, E, topk, scoring,
+          logits.stride(0) if M > 1 else max(logits.stride(0), E), M, E, topk, scoring,
           1 if renormalize else 0, scale, first_expert, E if num_local is None else num_local,
           topk_ids.data_ptr(), topk_weights.data_ptr())
     return topk_ids, topk_weights
@@ -410,14 +424,15 @@ def mol_router_topk(logits, topk: int, scoring: int = MOL_SCORE_SOFTMAX,
 
 def _rows(t: torch.Tensor, name: str, dev, dtype, shape) -> int:
     """t is on dev, 2-d with contiguous rows, of this dtype and shape; its row stride."""
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    _need(t, name, dtype, contiguous=False)
-    if tuple(t.shape) != tuple(shape):
+    if t.dtype is not dtype or t.shape != shape or t.device != dev:
+        if t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+        _need(t, name, dtype, contiguous=False)
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    ld, step = t.stride()
+    if step != 1 and shape[1] > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+    return ld if shape[0] > 1 else max(ld, shape[1])
 
 
 def _q4(W, scales, zeros, name: str, dev):
@@ -447,15 +462,17 @@ def mol_moe_gemm_q4(xin, row_div: int, W, scales, sorted_ids, expert_ids, num_po
         raise ValueError(f"xin has {xin.shape[0]} rows: {numel} pairs need "
                          f"{-(-numel // row_div)}")
     ld_out = _rows(out, "out", dev, dtype, (numel, N))
-    blocks = mol_align_max_blocks(numel, E, block_m)
+    # the routing's bound on blocks, as mol_align_max_blocks has it (which the call checks again)
+    blocks = -(-(numel + min(numel, E + 1) * (block_m - 1)) // block_m) if block_m > 0 else 0
     for t, name, least in ((sorted_ids, "sorted_ids", blocks * block_m),
                            (expert_ids, "expert_ids", blocks),
                            (num_post_padded, "num_post_padded", 1)):
-        _on(dev, name, t, torch.int32, t.shape)
+        if t.dtype is not torch.int32 or t.device != dev or not t.is_contiguous():
+            _on(dev, name, t, torch.int32, t.shape)
         if t.numel() < least:
             raise ValueError(f"{name} has {t.numel()} entries, fewer than the routing's {least}")
     _call(dev, "mol_moe_gemm_q4", _dtype_code(scales), xin.data_ptr(), ld_x, row_div,
-          W.data_ptr(), scales.data_ptr(), _ptr(zeros), group, K, N, E, sorted_ids.data_ptr(),
+          W.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(), group, K, N, E, sorted_ids.data_ptr(),
           expert_ids.data_ptr(), num_post_padded.data_ptr(), numel, block_m, out.data_ptr(),
           ld_out)
     return out

@@ -133,6 +133,23 @@ def test_one_expert_takes_most_pairs(M):
         la.check(x, ids, w, lora, la.call(x, ids, w, lora))
 
 
+@pytest.mark.parametrize("M,E", [(10, 2), (20, 2), (45, 3), (300, 5)])
+@pytest.mark.parametrize("group", [0, 32, 64, 128])
+def test_many_pairs_over_long_rows(M, E, group):
+    """Columns of every width class over rows whose x takes several stages, the pairs found by
+    every wave itself (up to 512 of them) and in quarters."""
+    if M == 300:
+        la = Layer("bf16", 2048, 128, E, 2, 8, group=group, seed=M)
+        x, ids, w, lora = la.step(M, 2)
+        rows = torch.tensor([0, 1, 57, 150, 299])
+        got = la.call(x, ids, w, lora)[rows.cuda()]
+        la.check(x[rows], ids[rows], w[rows], lora[rows], got)
+        return
+    Layer("bf16", 2048, 256, E, 2, 8, group=group, seed=M).run(M, 2)
+    if group == 0:
+        Layer("f32", 1040, 516, E, 2, 8, seed=M).run(M, 2)
+
+
 def test_decode_layer_width():
     Layer("bf16", 2048, 768, 10, 2, 32, seed=5).run(3, 8)
     Layer("bf16", 6144, 256, 9, 2, 32, seed=6).run(2, 8)

@@ -51,26 +51,36 @@ __device__ __forceinline__ int pair_key(const LayerArgs& a, int p) {
   return t < 0 || rank == 0 ? -1 : t + l * a.E;
 }
 
-// The pairs of a matrix, in ascending order, those of rank j0 .. j0 + kMaxCols - 1 among them.
+// The pairs of a matrix, in ascending order, those of rank j0 .. j0 + kMaxCols - 1 among them (LDS).
 struct PairList {
   int pair[kMaxCols];
   int hits[kWaves];
-  int total;  // of the matrix
-  int first;  // the first of them
 };
-// Each wave looks through a quarter of the ids at a time, all of its loads in flight together. key:
-// t, or (VIRT) t + l E; the caller knows that slot l has a rank.
+// The matrix of a work item (negative: nothing to do), how many pairs use it and the first of them.
+struct PairsOf {
+  int key;
+  int total;
+  int first;
+};
+
+constexpr int kFewPairs = 512;  // every wave looks through all ids itself
+
+// Fills the list. key: t, or (VIRT) t + l E; the caller knows that slot l has a rank. All loads of a
+// batch of ids are in flight together. Up to kFewPairs there is no barrier: each wave finds the pairs,
+// wave 0 writes them down, and the list may be read after the caller's next barrier. Beyond, each
+// wave looks through a quarter of a batch, and the list may be read on return.
 template <bool VIRT>
-__device__ __forceinline__ void list_pairs(const LayerArgs& a, int key, int j0, PairList& list) {
-  constexpr int NB = VIRT ? 4 : 8;
+__device__ __forceinline__ PairsOf list_pairs(const LayerArgs& a, int key, int j0, PairList& list) {
+  constexpr int NB = kFewPairs / 64;
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = VIRT ? key / a.E : 0, t = VIRT ? key - l * a.E : key;
-  int n = 0;  // found so far
-  for (int i0 = 0; i0 < a.numel; i0 += kThreads * NB) {
+  const bool few = a.numel <= kFewPairs;
+  PairsOf found{key, 0, 0};
+  for (int i0 = 0; i0 < a.numel; i0 += kWaves * kFewPairs) {
     // this wave's ids: whole 64s, contiguous, as even as that allows
-    const int left = min(a.numel - i0, kThreads * NB);
-    const int per = (left + kThreads - 1) / kThreads;  // 64s a wave
-    const int base = i0 + wv * per * 64;
+    const int left = min(a.numel - i0, kWaves * kFewPairs);
+    const int per = few ? (left + 63) / 64 : (left + kThreads - 1) / kThreads;  // 64s a wave
+    const int base = few ? 0 : i0 + wv * per * 64;
     int id[NB], sl[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
@@ -87,35 +97,41 @@ __device__ __forceinline__ void list_pairs(const LayerArgs& a, int key, int j0, 
       m[b] = __builtin_amdgcn_ballot_w64(hit);
       mine += __popcll(m[b]);
     }
-    if (lane == 0) list.hits[wv] = mine;
-    __syncthreads();
-    int at = n;
+    int at = found.total, before = found.total;
+    if (few) {
+      found.total = mine;
+    } else {
+      if (lane == 0) list.hits[wv] = mine;
+      __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const int h = list.hits[w];
-      at += w < wv ? h : 0;
-      n += h;
+      for (int w = 0; w < kWaves; ++w) {
+        const int h = list.hits[w];
+        at += w < wv ? h : 0;
+        found.total += h;
+      }
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       if ((m[b] >> lane) & 1) {
-        const int r = at + __popcll(m[b] & ((1ull << lane) - 1));
-        const int i = base + b * 64 + lane;
-        if (r >= j0 && r - j0 < kMaxCols) list.pair[r - j0] = i;
-        if (r == 0) list.first = i;
+        const int r = at + __popcll(m[b] & ((1ull << lane) - 1)) - j0;
+        if (r >= 0 && r < kMaxCols && (!few || wv == 0)) list.pair[r] = base + b * 64 + lane;
       }
+      if (few && at == 0 && m[b]) found.first = b * 64 + __builtin_ctzll(m[b]);
       at += __popcll(m[b]);
     }
-    if (threadIdx.x == 0) list.total = n;
-    __syncthreads();
+    if (!few) {
+      __syncthreads();
+      if (before == 0 && found.total > 0 && j0 == 0) found.first = list.pair[0];
+    }
   }
+  return found;
 }
 
-// The matrix of this work item and its pairs; negative for a workgroup with nothing to do. By pair
-// (slot = a pair): an earlier pair with the same matrix takes it.
+// The matrix of this work item and its pairs. By pair (slot = a pair): an earlier pair with the same
+// matrix takes it.
 template <bool VIRT>
-__device__ __forceinline__ int find_pairs(const LayerArgs& a, int slot, bool by_pair,
-                                          PairList& list) {
+__device__ __forceinline__ PairsOf find_pairs(const LayerArgs& a, int slot, bool by_pair,
+                                              PairList& list) {
   int key = slot;
   if (by_pair) {
     key = pair_key<VIRT>(a, slot);
@@ -124,9 +140,10 @@ __device__ __forceinline__ int find_pairs(const LayerArgs& a, int slot, bool by_
     if (a.ranks && a.ranks[l] <= 0) key = -1;
   }
   key = __builtin_amdgcn_readfirstlane(key);
-  if (key < 0) return -1;
-  list_pairs<VIRT>(a, key, 0, list);
-  return list.total == 0 || (by_pair && list.first != slot) ? -1 : key;
+  if (key < 0) return {-1, 0, 0};
+  PairsOf found = list_pairs<VIRT>(a, key, 0, list);
+  if (found.total == 0 || (by_pair && found.first != slot)) found.key = -1;
+  return found;
 }
 
 // h of the pairs: bf16 as two planes of I, or fp32.
@@ -180,12 +197,13 @@ __global__ void __launch_bounds__(64) layer_act_kernel(LayerArgs a) {
 // of A and elements of B past the slot's rank are not read.
 template <bool BF16, int NP, class Src>
 __device__ __forceinline__ void rank_part(const LayerArgs& a, const RankPart& rp, PairList& list,
-                                          char* lds, int v, const Src& src) {
+                                          char* lds, const PairsOf& of, const Src& src) {
   constexpr int ESZ = BF16 ? 2 : 4, VE = 16 / ESZ, KL = 4 * VE, COLS = 16;
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quad = lane >> 4;
   int slot;
-  const int rl = __builtin_amdgcn_readfirstlane(pair_rank(a, list.first, slot));
+  const int v = of.key, total = of.total;
+  const int rl = __builtin_amdgcn_readfirstlane(pair_rank(a, of.first, slot));
   const float scale = a.scale[slot];
   const int R = rp.slices * a.r, w = rp.N / rp.slices;
   float* s = reinterpret_cast<float*>(lds + StreamLds<0, BF16>::kBytes);
@@ -193,7 +211,6 @@ __device__ __forceinline__ void rank_part(const LayerArgs& a, const RankPart& rp
   const __amdgpu_buffer_rsrc_t ra = expert_rsrc((const char*)rp.A + (int64_t)v * abytes, abytes);
   const __amdgpu_buffer_rsrc_t rb = expert_rsrc((const char*)rp.B + (int64_t)v * bbytes, bbytes);
   auto in_rank = [&](int row) { return row < R && row % a.r < rl; };
-  const int total = list.total;
   for (int j0 = 0; j0 < total; j0 += COLS) {
     if (j0 > 0) {
       __syncthreads();
@@ -267,15 +284,16 @@ __global__ void __launch_bounds__(kThreads, G ? 3 : 4) gate_up_kernel(LayerArgs 
   int b = (int)blockIdx.x;
   if constexpr (LORA) {
     if (b < a.rank_slots) {
-      const int v = find_pairs<true>(a, b, a.rank_by_pair, list);
-      if (v >= 0) rank_part<BF16, 1>(a, a.rank_gu, list, lds, v, src);
+      const PairsOf of = find_pairs<true>(a, b, a.rank_by_pair, list);
+      if (of.key >= 0) rank_part<BF16, 1>(a, a.rank_gu, list, lds, of, src);
       return;
     }
     b -= a.rank_slots;
   }
   const int slot = fdiv(b, a.f_gu_items);
   const int n0 = (b - slot * a.gu_items) * item_rows(KS > 1);
-  const int e = find_pairs<false>(a, slot, a.by_pair, list);
+  const PairsOf of = find_pairs<false>(a, slot, a.by_pair, list);
+  const int e = of.key, total = of.total;
   if (e < 0) return;
   const int lane = threadIdx.x & 63, quad = lane >> 4;
   // With adapters the tile is 16 consecutive rows of gate and up; without, 8 gate rows and their
@@ -294,7 +312,6 @@ __global__ void __launch_bounds__(kThreads, G ? 3 : 4) gate_up_kernel(LayerArgs 
   const Q4Tables q{a.sc_gu, a.z_gu, G ? a.H / (G ? G : 1) : 0};
   const uint32_t off = n >= 0 ? (uint32_t)(n * rb) : kOutOfRange;
   const int64_t srow = n >= 0 ? (int64_t)e * 2 * a.I + n : (int64_t)-1;
-  const int total = list.total;
   for (int j0 = 0; j0 < total; j0 += kPassCols<G, BF16, 1, KS>) {
     if (j0 > 0) {
       __syncthreads();
@@ -337,15 +354,16 @@ __global__ void __launch_bounds__(kThreads, G ? 3 : 4) down_kernel(LayerArgs a) 
   int b = (int)blockIdx.x;
   if constexpr (LORA) {
     if (b < a.rank_slots) {
-      const int v = find_pairs<true>(a, b, a.rank_by_pair, list);
-      if (v >= 0) rank_part<BF16, NP>(a, a.rank_dn, list, lds, v, src);
+      const PairsOf of = find_pairs<true>(a, b, a.rank_by_pair, list);
+      if (of.key >= 0) rank_part<BF16, NP>(a, a.rank_dn, list, lds, of, src);
       return;
     }
     b -= a.rank_slots;
   }
   const int slot = fdiv(b, a.f_dn_items);
   const int n0 = (b - slot * a.dn_items) * item_rows(KS > 1);
-  const int e = find_pairs<false>(a, slot, a.by_pair, list);
+  const PairsOf of = find_pairs<false>(a, slot, a.by_pair, list);
+  const int e = of.key, total = of.total;
   if (e < 0) return;
   const int lane = threadIdx.x & 63, quad = lane >> 4;
   const int64_t rb = row_bytes<G, BF16>(a.I), wbytes = a.H * rb;
@@ -354,7 +372,6 @@ __global__ void __launch_bounds__(kThreads, G ? 3 : 4) down_kernel(LayerArgs a) 
   const int r0 = wave_row0<KS>(n0), n = r0 + (lane & 15);
   const uint32_t off = n < a.H ? (uint32_t)(n * rb) : kOutOfRange;
   const int64_t srow = n < a.H ? (int64_t)e * a.H + n : (int64_t)-1;
-  const int total = list.total;
   for (int j0 = 0; j0 < total; j0 += kPassCols<G, BF16, NP, KS>) {
     if (j0 > 0) {
       __syncthreads();

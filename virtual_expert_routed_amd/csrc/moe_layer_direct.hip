@@ -18,7 +18,7 @@ __global__ void __launch_bounds__(kThreads) down_direct_kernel(LayerArgs a) {
   constexpr int KK = kTileRows / NR;         // pairs of a tile
   constexpr int NP = BF16 ? 2 : 1;           // planes of h: columns kk and KK + kk
   constexpr int ESZ = BF16 ? 2 : 4, VE = 16 / ESZ;
-  constexpr int KL = G ? kQ4Load : 4 * VE, U = G ? 2 : 8;
+  constexpr int KL = G ? kQ4Load : 4 * VE, U = G ? 2 : 12;
   __shared__ float red[kWaves * kTileRows * NP];
   const int xcd = (int)blockIdx.x % kXcds, i = (int)blockIdx.x / kXcds;
   const int cg = fdiv(i, a.f_m);

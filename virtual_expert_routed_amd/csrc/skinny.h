@@ -466,7 +466,7 @@ __device__ __forceinline__ void stream_rows(char* lds, __amdgpu_buffer_rsrc_t rs
   auto groups_at = [&](int l0) { return min(cl * S::GPL, q.ng - l0 * S::GPL); };
   if constexpr (G > 0) regs.load(q, srow, 0, groups_at(0), quad);
   if constexpr (!MULTI) {
-    __syncthreads();
+    __syncthreads();  // the columns' pairs are written down, and LDS is free
     stage_row<S, G, BF16, CW, NP>(xs, sums, src, ncol, K, tid);
     if constexpr (G > 0) regs.store(sc, groups_at(0), lane);  // (KS > 1: all waves the same values)
     __syncthreads();
@@ -476,8 +476,8 @@ __device__ __forceinline__ void stream_rows(char* lds, __amdgpu_buffer_rsrc_t rs
   } else {
     // stages alternate between the two buffers; the next one's x and scales load while one works
     StageRegs<S, G, BF16, CW, NP, Src> stage;
+    __syncthreads();  // the columns' pairs are written down, and LDS is free
     stage.load(src, ncol, 0, vend, tid);
-    __syncthreads();
     stage.store(xs, sums, ncol, 0, vend, tid);
     int buf = 0;
     for (int l0 = 0; l0 < loads; l0 += S::CL, buf ^= 1) {

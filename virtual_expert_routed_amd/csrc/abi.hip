@@ -774,7 +774,10 @@ MOL_API mol_status mol_moe_gemm_q4(int32_t dtype, const void* xin, int64_t ld_x,
   a.max_blocks = (int32_t)rc.max_blocks;
   // blocks that hold pairs: at most one partly filled per expert, beside the full ones
   const int64_t filled = std::min<int64_t>(numel, (int64_t)num_experts + numel / block_m);
-  a.items = (int32_t)mol::stream_items(filled, N, a.split_k);
+  const mol::StreamItems it = mol::stream_items(filled, numel, N, K / 2);
+  a.split_k = it.split;
+  a.tiles = it.tiles;
+  a.items = (int32_t)it.items;
   if (rc.max_blocks * a.items > kI32Max) return MOL_E_LIMIT;
   a.out = out;
   a.ld_out = ld_out;
@@ -893,17 +896,23 @@ MOL_API mol_status mol_moe_layer(const mol_moe_weights* w, const mol_moe_adapter
   a.rank_by_pair = a.numel <= V;
   a.rank_slots = adapters ? (int32_t)std::min<int64_t>(a.numel, V) : 0;
   a.direct = layer_direct(M, r);
-  const int64_t gu_items = mol::stream_items(a.slots, 2 * (int64_t)I, a.gu_split);
-  const int64_t dn_items = mol::stream_items(a.slots, H, a.dn_split);
+  auto row_bytes = [&](int64_t K) { return G ? K / 2 : K * esz; };
+  const mol::StreamItems gu =
+      mol::stream_items(a.slots, a.numel, 2 * (int64_t)I, row_bytes(H));
+  const mol::StreamItems dn = mol::stream_items(a.slots, a.numel, H, row_bytes(I));
   // every grid of the call: matrices x row groups, and direct down's columns x tokens
-  if (a.slots * gu_items + a.rank_slots > kI32Max || a.slots * dn_items + a.rank_slots > kI32Max ||
+  if (a.slots * gu.items + a.rank_slots > kI32Max || a.slots * dn.items + a.rank_slots > kI32Max ||
       ((int64_t)H + 128) * M > kI32Max)
     return MOL_E_LIMIT;
-  a.gu_items = (int32_t)gu_items;
-  a.dn_items = (int32_t)dn_items;
+  a.gu_split = gu.split;
+  a.gu_tiles = gu.tiles;
+  a.gu_items = (int32_t)gu.items;
+  a.dn_split = dn.split;
+  a.dn_tiles = dn.tiles;
+  a.dn_items = (int32_t)dn.items;
   a.f_topk = mol::make_fastdiv((uint32_t)topk);
-  a.f_gu_items = mol::make_fastdiv((uint32_t)gu_items);
-  a.f_dn_items = mol::make_fastdiv((uint32_t)dn_items);
+  a.f_gu_items = mol::make_fastdiv((uint32_t)gu.items);
+  a.f_dn_items = mol::make_fastdiv((uint32_t)dn.items);
   a.f_m = mol::make_fastdiv((uint32_t)M);
   return hip_status(mol::launch_moe_layer(a, bf16, (hipStream_t)stream));
 }

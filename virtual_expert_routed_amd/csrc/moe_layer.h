@@ -229,9 +229,9 @@ __device__ __forceinline__ void rank_part(const LayerArgs& a, const RankPart& rp
         }
       };
       if (ncol <= 4)
-        stream_k<0, BF16, 4, NP, 1>(lds, ra, off, Q4Tables{}, -1, src, ncol, rp.K, keep);
+        stream_k<0, BF16, 4, NP, 1>(lds, ra, off, Q4Tables{}, -1, src, ncol, rp.K, r0 > 0, keep);
       else
-        stream_k<0, BF16, 16, NP, 1>(lds, ra, off, Q4Tables{}, -1, src, ncol, rp.K, keep);
+        stream_k<0, BF16, 16, NP, 1>(lds, ra, off, Q4Tables{}, -1, src, ncol, rp.K, r0 > 0, keep);
     }
     __syncthreads();
     // B s: the operand rows of B are 16 bytes of rank a lane and step, s in two planes (bf16)
@@ -291,57 +291,60 @@ __global__ void __launch_bounds__(kThreads, G ? 3 : 4) gate_up_kernel(LayerArgs 
     b -= a.rank_slots;
   }
   const int slot = fdiv(b, a.f_gu_items);
-  const int n0 = (b - slot * a.gu_items) * item_rows(KS > 1);
+  const int n0 = (b - slot * a.gu_items) * (KS > 1 ? kTileRows : kItemRows * a.gu_tiles);
   const PairsOf of = find_pairs<false>(a, slot, a.by_pair, list);
   const int e = of.key, total = of.total;
   if (e < 0) return;
   const int lane = threadIdx.x & 63, quad = lane >> 4;
-  // With adapters the tile is 16 consecutive rows of gate and up; without, 8 gate rows and their
-  // up rows, the two of a column in one lane: rows 4 q, 4 q + 1 are gate columns i0 + 2 q, + 1 and
-  // rows 4 q + 2, 4 q + 3 the same up columns (i0 half of the tile's first row).
-  const int r0 = wave_row0<KS>(n0), r = lane & 15;
-  int n;  // this lane's weight row, or -1
-  if constexpr (LORA) {
-    n = r0 + r < 2 * a.I ? r0 + r : -1;
-  } else {
-    const int i = r0 / 2 + (r >> 2) * 2 + (r & 1);
-    n = i < a.I ? ((r & 2) ? a.I : 0) + i : -1;
-  }
   const int64_t rb = row_bytes<G, BF16>(a.H), wbytes = 2 * a.I * rb;
   const __amdgpu_buffer_rsrc_t rsrc = expert_rsrc((const char*)a.W_gu + (int64_t)e * wbytes, wbytes);
   const Q4Tables q{a.sc_gu, a.z_gu, G ? a.H / (G ? G : 1) : 0};
-  const uint32_t off = n >= 0 ? (uint32_t)(n * rb) : kOutOfRange;
-  const int64_t srow = n >= 0 ? (int64_t)e * 2 * a.I + n : (int64_t)-1;
   for (int j0 = 0; j0 < total; j0 += kPassCols<G, BF16, 1, KS>) {
     if (j0 > 0) {
       __syncthreads();
       list_pairs<false>(a, e, j0, list);
     }
     const int ncol = min(kPassCols<G, BF16, 1, KS>, total - j0);
-    stream_cols<G, BF16, 1, KS>(lds, rsrc, off, q, srow, src, ncol, a.H,
-                                [&](int c, const f32x4_t& acc) {
-      if (c >= ncol) return;
-      const int64_t p = list.pair[c];
+#pragma unroll 1
+    for (int t = 0; t < (KS > 1 ? 1 : a.gu_tiles); ++t) {
+      // With adapters the tile is 16 consecutive rows of gate and up; without, 8 gate rows and
+      // their up rows, the two of a column in one lane: rows 4 q, 4 q + 1 are gate columns i0 + 2 q,
+      // + 1 and rows 4 q + 2, 4 q + 3 the same up columns (i0 half of the tile's first row).
+      const int r0 = wave_row0<KS>(n0 + t * kItemRows), r = lane & 15;
+      int n;  // this lane's weight row, or -1
       if constexpr (LORA) {
-        const int at = r0 + quad * 4;  // 2 I is a multiple of 4
-        if (at < 2 * a.I) *reinterpret_cast<f32x4_t*>(a.gu + p * 2 * a.I + at) = acc;
+        n = r0 + r < 2 * a.I ? r0 + r : -1;
       } else {
-        const int i = r0 / 2 + quad * 2;  // I is a multiple of 2
-        if (i >= a.I) return;
-        float h[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) h[j] = silu(acc[j]) * acc[2 + j];
-        if constexpr (BF16) {
-          const float f[8] = {h[0], h[1], 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          const XVec s = split_vec<true>(f);
-          uint16_t* o = (uint16_t*)a.h + p * 2 * a.I + i;
-          *reinterpret_cast<uint32_t*>(o) = s.hi.x;
-          *reinterpret_cast<uint32_t*>(o + a.I) = s.lo.x;
-        } else {
-          *reinterpret_cast<float2*>((float*)a.h + p * a.I + i) = make_float2(h[0], h[1]);
-        }
+        const int i = r0 / 2 + (r >> 2) * 2 + (r & 1);
+        n = i < a.I ? ((r & 2) ? a.I : 0) + i : -1;
       }
-    });
+      stream_cols<G, BF16, 1, KS>(
+          lds, rsrc, n >= 0 ? (uint32_t)(n * rb) : kOutOfRange, q,
+          n >= 0 ? (int64_t)e * 2 * a.I + n : (int64_t)-1, src, ncol, a.H, t > 0,
+          [&](int c, const f32x4_t& acc) {
+            if (c >= ncol) return;
+            const int64_t p = list.pair[c];
+            if constexpr (LORA) {
+              const int at = r0 + quad * 4;  // 2 I is a multiple of 4
+              if (at < 2 * a.I) *reinterpret_cast<f32x4_t*>(a.gu + p * 2 * a.I + at) = acc;
+            } else {
+              const int i = r0 / 2 + quad * 2;  // I is a multiple of 2
+              if (i >= a.I) return;
+              float h[2];
+#pragma unroll
+              for (int j = 0; j < 2; ++j) h[j] = silu(acc[j]) * acc[2 + j];
+              if constexpr (BF16) {
+                const float f[8] = {h[0], h[1], 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                const XVec s = split_vec<true>(f);
+                uint16_t* o = (uint16_t*)a.h + p * 2 * a.I + i;
+                *reinterpret_cast<uint32_t*>(o) = s.hi.x;
+                *reinterpret_cast<uint32_t*>(o + a.I) = s.lo.x;
+              } else {
+                *reinterpret_cast<float2*>((float*)a.h + p * a.I + i) = make_float2(h[0], h[1]);
+              }
+            }
+          });
+    }
   }
 }
 
@@ -361,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, G ? 3 : 4) down_kernel(LayerArgs a) 
     b -= a.rank_slots;
   }
   const int slot = fdiv(b, a.f_dn_items);
-  const int n0 = (b - slot * a.dn_items) * item_rows(KS > 1);
+  const int n0 = (b - slot * a.dn_items) * (KS > 1 ? kTileRows : kItemRows * a.dn_tiles);
   const PairsOf of = find_pairs<false>(a, slot, a.by_pair, list);
   const int e = of.key, total = of.total;
   if (e < 0) return;
@@ -369,21 +372,24 @@ __global__ void __launch_bounds__(kThreads, G ? 3 : 4) down_kernel(LayerArgs a) 
   const int64_t rb = row_bytes<G, BF16>(a.I), wbytes = a.H * rb;
   const __amdgpu_buffer_rsrc_t rsrc = expert_rsrc((const char*)a.W_dn + (int64_t)e * wbytes, wbytes);
   const Q4Tables q{a.sc_dn, a.z_dn, G ? a.I / (G ? G : 1) : 0};
-  const int r0 = wave_row0<KS>(n0), n = r0 + (lane & 15);
-  const uint32_t off = n < a.H ? (uint32_t)(n * rb) : kOutOfRange;
-  const int64_t srow = n < a.H ? (int64_t)e * a.H + n : (int64_t)-1;
   for (int j0 = 0; j0 < total; j0 += kPassCols<G, BF16, NP, KS>) {
     if (j0 > 0) {
       __syncthreads();
       list_pairs<false>(a, e, j0, list);
     }
     const int ncol = min(kPassCols<G, BF16, NP, KS>, total - j0);
-    stream_cols<G, BF16, NP, KS>(lds, rsrc, off, q, srow, src, ncol, a.I,
-                                 [&](int c, const f32x4_t& acc) {
-      const int at = r0 + quad * 4;  // H is a multiple of 4
-      if (c < ncol && at < a.H)
-        *reinterpret_cast<f32x4_t*>(a.z + (int64_t)list.pair[c] * a.H + at) = acc;
-    });
+#pragma unroll 1
+    for (int t = 0; t < (KS > 1 ? 1 : a.dn_tiles); ++t) {
+      const int r0 = wave_row0<KS>(n0 + t * kItemRows), n = r0 + (lane & 15);
+      stream_cols<G, BF16, NP, KS>(
+          lds, rsrc, n < a.H ? (uint32_t)(n * rb) : kOutOfRange, q,
+          n < a.H ? (int64_t)e * a.H + n : (int64_t)-1, src, ncol, a.I, t > 0,
+          [&](int c, const f32x4_t& acc) {
+            const int at = r0 + quad * 4;  // H is a multiple of 4
+            if (c < ncol && at < a.H)
+              *reinterpret_cast<f32x4_t*>(a.z + (int64_t)list.pair[c] * a.H + at) = acc;
+          });
+    }
   }
 }
 

@@ -4,8 +4,8 @@
 // dense grouped GEMM (the aligned blocks of one base expert each).
 //
 // At decode it reads half a byte of each touched weight once and little else, so a work item is
-// (block, 64 output columns): 64 rows of W_t, read once for up to 64 pairs of the block. Where that
-// makes too few items to fill the chip (split_k), an item is 16 rows whose k's the four waves
+// (block, 64 to 256 output columns): rows of W_t, read once for up to 64 pairs of the block. Where 64
+// make too few items to fill the chip (split_k), an item is 16 rows whose k's the four waves
 // split.
 #pragma once
 
@@ -20,7 +20,7 @@ __global__ void __launch_bounds__(kThreads, 3) q4_gemm_kernel(Q4GemmArgs a) {
   __shared__ int pair[kCols];
   __shared__ __attribute__((aligned(16))) char lds[StreamLds<G, BF16>::kBytes];
   const int blk = fdiv((int)blockIdx.x, a.f_items);
-  const int n0 = ((int)blockIdx.x - blk * a.items) * item_rows(KS > 1);
+  const int n0 = ((int)blockIdx.x - blk * a.items) * (KS > 1 ? kTileRows : kItemRows * a.tiles);
   const int npp = *a.npp;
   const int er = a.expert_ids[blk];
   const int32_t* sorted = a.sorted + (int64_t)blk * a.BM;
@@ -33,9 +33,6 @@ __global__ void __launch_bounds__(kThreads, 3) q4_gemm_kernel(Q4GemmArgs a) {
   const __amdgpu_buffer_rsrc_t rsrc = expert_rsrc((const char*)a.W + (int64_t)e * wbytes, wbytes);
   const int lane = threadIdx.x & 63, quad = lane >> 4;
   const Q4Tables q{a.scales, a.zeros, a.K / G};
-  const int r0 = wave_row0<KS>(n0), n = r0 + (lane & 15);
-  const uint32_t off = n < a.N ? (uint32_t)(n * rb) : kOutOfRange;
-  const int64_t srow = n < a.N ? (int64_t)e * a.N + n : (int64_t)-1;
   const RowSrc src{(const char*)a.x, a.ld_x * (BF16 ? 2 : 4), pair, a.f_rd};
   for (int j0 = 0; j0 < a.BM; j0 += kCols) {
     if (j0 > 0) {
@@ -50,15 +47,21 @@ __global__ void __launch_bounds__(kThreads, 3) q4_gemm_kernel(Q4GemmArgs a) {
     const int ncol = __popcll(
         __builtin_amdgcn_ballot_w64(j < kCols && real_pair(pair[j < kCols ? j : 0], a.numel)));
     if (ncol == 0) return;
-    stream_cols<G, BF16, 1, KS>(lds, rsrc, off, q, srow, src, ncol, a.K,
-                                [&](int c, const f32x4_t& acc) {
-      if (c >= ncol) return;
-      const int n = r0 + quad * 4;
-      const int64_t at = (int64_t)pair[c] * a.ld_out + n;
+#pragma unroll 1
+    for (int t = 0; t < (KS > 1 ? 1 : a.tiles); ++t) {
+      const int r0 = wave_row0<KS>(n0 + t * kItemRows), n = r0 + (lane & 15);
+      stream_cols<G, BF16, 1, KS>(
+          lds, rsrc, n < a.N ? (uint32_t)(n * rb) : kOutOfRange, q,
+          n < a.N ? (int64_t)e * a.N + n : (int64_t)-1, src, ncol, a.K, t > 0,
+          [&](int c, const f32x4_t& acc) {
+            if (c >= ncol) return;
+            const int m = r0 + quad * 4;
+            const int64_t at = (int64_t)pair[c] * a.ld_out + m;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (n + i < a.N) store_elem<BF16>(a.out, at + i, acc[i]);
-    });
+            for (int i = 0; i < 4; ++i)
+              if (m + i < a.N) store_elem<BF16>(a.out, at + i, acc[i]);
+          });
+    }
     if (ncol < kCols) return;
   }
 }

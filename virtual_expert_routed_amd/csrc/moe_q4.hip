@@ -12,6 +12,4 @@ hipError_t launch_q4_gemm(const Q4GemmArgs& a, bool bf16, hipStream_t st) {
   }
 }
 
-int stream_item_rows(bool split) { return item_rows(split); }
-
 }  // namespace mol

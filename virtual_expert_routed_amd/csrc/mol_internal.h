@@ -199,15 +199,26 @@ struct RouterArgs {
   float* weights;          // [M, topk]
 };
 
-// Work items of a stream of weight rows: 64 rows, or 16 rows whose k's four waves split. Both
-// read the same bytes; the smaller ones are for launches whose larger ones would leave the chip's
-// 256 CUs with too few.
-int stream_item_rows(bool split);
-inline int64_t stream_items(int64_t matrices, int64_t rows, bool& split) {
-  auto items = [&] { return (rows + stream_item_rows(split) - 1) / stream_item_rows(split); };
-  split = false;
-  split = matrices * items() < 1024;
-  return items();
+// The work items of a stream of weight rows: 64 rows times `tiles`, or 16 rows whose k's four waves
+// split. All read the same bytes.
+//  - 16 rows where 64 would make fewer than 1024 items for the chip's 256 CUs.
+//  - Several tiles where 64 rows hold few bytes, so that finding the pairs and staging x (microseconds
+//    of latency for each item) is paid once for up to 128 KiB of weights; only while matrices have
+//    few columns (`pairs` at most four a matrix on average): items over many columns are long, and
+//    fewer of them leave CUs idle.
+struct StreamItems {
+  bool split;
+  int32_t tiles;
+  int64_t items;  // per matrix
+};
+inline StreamItems stream_items(int64_t matrices, int64_t pairs, int64_t rows, int64_t row_bytes) {
+  auto items = [&](int64_t n) { return (rows + n - 1) / n; };
+  if (matrices * items(64) < 1024) return {true, 1, items(16)};
+  int32_t tiles = 1;
+  while (tiles < 4 && pairs <= 4 * matrices && 64 * row_bytes * tiles * 2 <= 131072 &&
+         matrices * items(64 * tiles * 2) >= 512)
+    tiles *= 2;
+  return {false, tiles, items(64 * tiles)};
 }
 
 // The base grouped GEMM over 4-bit weights (group scales along K).
@@ -228,6 +239,7 @@ struct Q4GemmArgs {
   int32_t BM;
   int32_t max_blocks;
   bool split_k;            // stream_items()
+  int32_t tiles;
   int32_t items;           // work items per block
   void* out;               // [numel, ld_out]
   int64_t ld_out;
@@ -280,6 +292,7 @@ struct LayerArgs {
   bool rank_by_pair;
   bool direct;             // down per token, with the combine
   bool gu_split, dn_split; // stream_items() of gate/up and of down
+  int32_t gu_tiles, dn_tiles;
   int32_t gu_items;        // row groups of gate/up and of down
   int32_t dn_items;
   FastDiv f_topk, f_gu_items, f_dn_items, f_m;

@@ -146,8 +146,8 @@ __device__ __forceinline__ XVec split_vec(const float (&f)[BF16 ? 8 : 4]) {
 
 // The shape of a stream: G the group of 4-bit weights (0: dense), CW columns, NP planes of x, KS
 // the waves that share 16 rows and split their k's (1 or kWaves), MULTI whether a row of x takes
-// several stages.
-template <int G, bool BF16, int CW, int NP, int KS, bool MULTI>
+// several stages, UM the most loads of W in flight.
+template <int G, bool BF16, int CW, int NP, int KS, bool MULTI, int UM>
 struct Stream {
   static constexpr int VE = BF16 ? 8 : 4;                 // elements of a vector of x
   static constexpr int KL = G ? kQ4Load : 4 * VE;         // k's of a load of W
@@ -160,16 +160,13 @@ struct Stream {
   static constexpr int Q = CL / KS;                       // of them, one wave's
   // a row of up to this many loads is staged at once, through both buffers
   static constexpr int ONE = G && 2 * CL > CLG ? CLG : 2 * CL;
-  // loads of W in flight, as many as the registers allow beside the next stage's x (4-bit: each
-  // load's products take many of them)
-  static constexpr int UM = G == 0 ? 8 : MULTI || G == 32 ? 2 : G == 64 ? 4 : 8;
   static constexpr int U = Q < UM ? Q : UM;               // a round of loads
   static constexpr int T = CW > 16 ? CW / 16 : 1;         // matrix-core tiles of columns
   static constexpr int PERIOD = LX % 4 ? 4 : 1;           // loads between equal x rotations
   static constexpr int PLANE = 2 * XS * 4 * CW;           // 16-byte slots of a plane (both buffers)
   static constexpr int NV = CL * KL / VE;                 // vectors of a column in a stage
   static constexpr int PER = (CW * NV + kThreads - 1) / kThreads;  // a thread's of a whole stage
-  static_assert(Q >= 1 && Q % U == 0 && Q % PERIOD == 0 && U % PERIOD == 0,
+  static_assert(Q >= 1 && U % PERIOD == 0 && (MULTI ? Q % U == 0 : U <= ONE),
                 "a wave's part of a stage is whole rounds of loads");
   static_assert(KS == 1 || T == 1, "split k's: one tile of columns");
   static_assert((NV & (NV - 1)) == 0, "a stage's vectors are told apart by shifts");
@@ -347,11 +344,11 @@ struct ScaleRegs {
 // epilogue(col, acc) gets, on every lane (of wave 0 for KS = kWaves), column col's sums of tile
 // rows 4 * quad + i; only columns below ncol and rows that exist are meant. All four waves take
 // part in the barriers; on return LDS may still be read by slower waves.
-template <int G, bool BF16, int CW, int NP, int KS, bool MULTI, class Src, class Epi>
+template <int G, bool BF16, int CW, int NP, int KS, bool MULTI, int UM, class Src, class Epi>
 __device__ __forceinline__ void stream_rows(char* lds, __amdgpu_buffer_rsrc_t rsrc, uint32_t off,
                                             const Q4Tables& q, int64_t srow, const Src& src,
-                                            int ncol, int K, Epi epilogue) {
-  using S = Stream<G, BF16, CW, NP, KS, MULTI>;
+                                            int ncol, int K, bool staged, Epi epilogue) {
+  using S = Stream<G, BF16, CW, NP, KS, MULTI, UM>;
   // (opaque to the compiler, which would otherwise compute every variant's addresses ahead of the
   // loop over passes and spill them)
   int tid = threadIdx.x;
@@ -466,10 +463,13 @@ __device__ __forceinline__ void stream_rows(char* lds, __amdgpu_buffer_rsrc_t rs
   auto groups_at = [&](int l0) { return min(cl * S::GPL, q.ng - l0 * S::GPL); };
   if constexpr (G > 0) regs.load(q, srow, 0, groups_at(0), quad);
   if constexpr (!MULTI) {
-    __syncthreads();  // the columns' pairs are written down, and LDS is free
-    stage_row<S, G, BF16, CW, NP>(xs, sums, src, ncol, K, tid);
-    if constexpr (G > 0) regs.store(sc, groups_at(0), lane);  // (KS > 1: all waves the same values)
-    __syncthreads();
+    if (!staged) {
+      __syncthreads();  // the columns' pairs are written down, and LDS is free
+      stage_row<S, G, BF16, CW, NP>(xs, sums, src, ncol, K, tid);
+    }
+    // (this wave's own part of LDS; KS > 1: all waves write the same values)
+    if constexpr (G > 0) regs.store(sc, groups_at(0), lane);
+    if (!staged) __syncthreads();
     const int n = min(first + part, loads);
     for (int b = first; b < n; b += S::U)
       round(xs, sums, b, b + S::U < first + part ? b + S::U : loads);
@@ -521,43 +521,52 @@ template <int G, bool BF16, int NP, int KS>
 constexpr int kPassCols = KS > 1 ? 8 : (G && !BF16) || NP == 2 ? 32 : kMaxCols;
 
 // The stream of a row of K: staged at once where its x fits both buffers, else in several stages.
+// Loads of W in flight: as many as the registers allow (4-bit: each load's products take many of
+// them; fewer beside the next stage's x), and six where the row has no more.
 template <int G, bool BF16, int CW, int NP, int KS, class Src, class Epi>
 __device__ __forceinline__ void stream_k(char* lds, __amdgpu_buffer_rsrc_t rsrc, uint32_t off,
                                          const Q4Tables& q, int64_t srow, const Src& src, int ncol,
-                                         int K, Epi epi) {
-  using S = Stream<G, BF16, CW, NP, KS, false>;
+                                         int K, bool staged, Epi epi) {
+  constexpr int UM = G == 0 || G == 128 ? 8 : G == 64 ? 4 : 2;
+  using S = Stream<G, BF16, CW, NP, KS, false, UM>;
   if constexpr (CW <= 16) {
+    if constexpr (G >= 64 && BF16 && KS == 1 && S::ONE >= 6) {
+      if (K > 4 * kQ4Load && K <= 6 * kQ4Load) {
+        stream_rows<G, BF16, CW, NP, KS, false, 6>(lds, rsrc, off, q, srow, src, ncol, K, staged, epi);
+        return;
+      }
+    }
     if (K <= S::ONE * S::KL) {
-      stream_rows<G, BF16, CW, NP, KS, false>(lds, rsrc, off, q, srow, src, ncol, K, epi);
+      stream_rows<G, BF16, CW, NP, KS, false, UM>(lds, rsrc, off, q, srow, src, ncol, K, staged, epi);
       return;
     }
   }
-  stream_rows<G, BF16, CW, NP, KS, true>(lds, rsrc, off, q, srow, src, ncol, K, epi);
+  stream_rows<G, BF16, CW, NP, KS, true, (G ? 2 : 8)>(lds, rsrc, off, q, srow, src, ncol, K, false,
+                                                      epi);
 }
 
 // As many columns as the pass has: 4, 8, 16, 32 or 64.
 template <int G, bool BF16, int NP, int KS, class Src, class Epi>
 __device__ __forceinline__ void stream_cols(char* lds, __amdgpu_buffer_rsrc_t rsrc, uint32_t off,
                                             const Q4Tables& q, int64_t srow, const Src& src,
-                                            int ncol, int K, Epi epi) {
+                                            int ncol, int K, bool staged, Epi epi) {
   constexpr int MOST = kPassCols<G, BF16, NP, KS>;
   if (ncol <= 4) {
-    stream_k<G, BF16, 4, NP, KS>(lds, rsrc, off, q, srow, src, ncol, K, epi);
+    stream_k<G, BF16, 4, NP, KS>(lds, rsrc, off, q, srow, src, ncol, K, staged, epi);
   } else if (MOST == 8 || ncol <= 8) {
-    stream_k<G, BF16, 8, NP, KS>(lds, rsrc, off, q, srow, src, ncol, K, epi);
+    stream_k<G, BF16, 8, NP, KS>(lds, rsrc, off, q, srow, src, ncol, K, staged, epi);
   } else if constexpr (MOST > 8) {
     if (ncol <= 16)
-      stream_k<G, BF16, 16, NP, 1>(lds, rsrc, off, q, srow, src, ncol, K, epi);
+      stream_k<G, BF16, 16, NP, 1>(lds, rsrc, off, q, srow, src, ncol, K, staged, epi);
     else if (MOST == 32 || ncol <= 32)
-      stream_k<G, BF16, 32, NP, 1>(lds, rsrc, off, q, srow, src, ncol, K, epi);
+      stream_k<G, BF16, 32, NP, 1>(lds, rsrc, off, q, srow, src, ncol, K, staged, epi);
     else if constexpr (MOST > 32)
-      stream_k<G, BF16, 64, NP, 1>(lds, rsrc, off, q, srow, src, ncol, K, epi);
+      stream_k<G, BF16, 64, NP, 1>(lds, rsrc, off, q, srow, src, ncol, K, staged, epi);
   }
 }
 
-// Rows of a work item, and the first row of this wave in an item that begins at row n0: 16 a wave,
-// or (KS = kWaves) 16 for all.
-constexpr int item_rows(bool split) { return split ? kTileRows : kItemRows; }
+// A work item is `tiles` times 64 rows, 16 a wave and tile, or (KS = kWaves) 16 for all. The first
+// row of this wave in the tile that begins at row n0:
 template <int KS>
 __device__ __forceinline__ int wave_row0(int n0) {
   return KS > 1 ? n0 : n0 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * kTileRows;

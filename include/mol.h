@@ -404,17 +404,18 @@ MOL_API mol_status mol_moe_gemm_q4(int32_t dtype, const void *xin, int64_t ld_x,
 
 /* ---------------------------------------------------------------------------------
  * mol_moe_layer - a whole layer for a few tokens, from the routed ids to the combined rows, with
- * no aligned routing: two launches up to 32 tokens (gate/up with the activation, down with
- * the combine), the combine as a third beyond; with adapters, a rank product more before each
- * of the two. For pair p = m * topk + k with a local base expert t = topk_ids[m, k] in [0, E),
+ * no aligned routing: two launches for a token, or up to three of them, without adapters (gate/up
+ * with the activation, down with the combine); three beyond (the combine on its own); four with
+ * adapters (the activation too; their products run beside the base ones). For pair p = m * topk + k with a local base expert t = topk_ids[m, k] in [0, E),
  * and l = lora_ids[m] (the adapter terms only for l in [0, S) and slot rank rl > 0, v = t + l * E):
  *   g    = gate_up[t, 0:I] x_m + slot_scale[l] * gate_up_B[v, 0:I, :rl] (gate_up_A[v, 0:rl] x_m)
  *   u    = gate_up[t, I:2I] x_m + slot_scale[l] * gate_up_B[v, I:2I, :rl] (gate_up_A[v, r:r+rl] x_m)
- *   h_p  = round( g / (1 + exp(-g)) * u )
+ *   h_p  = g / (1 + exp(-g)) * u
  *   y_m  = round( sum_k topk_weights[m, k] * (down[t] h_p
  *                  + slot_scale[l] * down_B[v, :, :rl] (down_A[v, 0:rl] h_p)) )
  * Pairs without a local expert contribute nothing; a token that has none gets a row of
- * zeros. Sums are fp32; h and y alone are rounded (bf16: to nearest even).
+ * zeros. Sums, g, u and h are fp32; bf16 products take h as two bf16 terms (16 of its bits), and
+ * y alone is rounded to bf16 (to nearest even).
  *   w             (host) the weights; read during the call only. dtype: MOL_F32 or MOL_BF16 of x,
  *                 y, the scales, the adapters, and of the weights themselves when group is 0.
  *                 gate_up [E, 2 * inter, hidden] (gate rows first), down [E, hidden, inter],

@@ -144,20 +144,26 @@ mol_status q4_check(int32_t K, int32_t group, int64_t N) {
 static_assert(MOL_LAYER_MAX_PAIRS == mol::kLayerMaxPairs && MOL_LAYER_MAX_TOPK == mol::kLayerMaxTopk,
               "the layer's limits");
 
-// Whether the layer's down stage runs per token, with the combine.
-bool layer_direct(int32_t M, int32_t r) { return r == 0 && M <= 4; }
+// Whether the layer's down stage runs per token, with the combine: for one token, and for up to three
+// where an item of four columns over the token's experts holds at least 32 KiB of weights. Measured
+// against the grouped form and a combine (128 experts, top-8, hidden 2048, inter 768, whole layer): 42
+// against 48 us at two tokens, 53 against 62 at three, 67 against 65 at four. With 16 KiB an item
+// (hidden 6144, inter 256) its many small items lose: 56 against 41 us at two tokens.
+bool layer_direct(int32_t M, int32_t r, int32_t topk, int64_t row_bytes) {
+  return r == 0 && (M == 1 || (M <= 3 && (int64_t)topk * 4 * row_bytes >= 32768));
+}
 
-// The layer's scratch: byte offsets and the total. h is first, then z (not for a direct down), and
-// with adapters gu and both of their parts. All of it is four bytes an element (h in bf16 is two
-// planes), so the type does not matter.
+// The layer's scratch: byte offsets and the total. h is first, then z, and with adapters gu and
+// both of their parts. All of it is four bytes an element (h in bf16 is two planes), so the type
+// does not matter.
 struct LayerWorkspace {
   int64_t z, gu, d1, d2, bytes;
 };
-LayerWorkspace layer_workspace(int64_t numel, int32_t M, int32_t H, int32_t I, int32_t r) {
+LayerWorkspace layer_workspace(int64_t numel, int32_t H, int32_t I, int32_t r) {
   LayerWorkspace w;
   const int64_t wide = r ? round256(numel * 2 * I * 4) : 0, out = round256(numel * H * 4);
   w.z = round256(numel * I * 4);
-  w.gu = w.z + (layer_direct(M, r) ? 0 : out);
+  w.gu = w.z + out;
   w.d1 = w.gu + wide;
   w.d2 = w.d1 + wide;
   w.bytes = w.d2 + (r ? out : 0);
@@ -797,7 +803,7 @@ MOL_API int64_t mol_moe_layer_workspace_bytes(int32_t dtype, int32_t M, int32_t 
   if (topk > MOL_LAYER_MAX_TOPK || (int64_t)M * topk > MOL_LAYER_MAX_PAIRS ||
       (int64_t)rank * esz > MOL_MAX_RANK_BYTES)
     return -MOL_E_LIMIT;
-  return layer_workspace((int64_t)M * topk, M, hidden, inter, rank).bytes;
+  return layer_workspace((int64_t)M * topk, hidden, inter, rank).bytes;
 }
 
 MOL_API mol_status mol_moe_layer(const mol_moe_weights* w, const mol_moe_adapters* adapters,
@@ -852,7 +858,7 @@ MOL_API mol_status mol_moe_layer(const mol_moe_weights* w, const mol_moe_adapter
   if (!aligned16(x) || !aligned_to(y, esz) || !aligned_to(topk_ids, 4) ||
       !aligned_to(topk_weights, 4) || !aligned_to(lora_ids, 4))
     return MOL_E_ALIGN;
-  const LayerWorkspace ws = layer_workspace((int64_t)M * topk, M, H, I, r);
+  const LayerWorkspace ws = layer_workspace((int64_t)M * topk, H, I, r);
   if (!workspace || workspace_bytes < (size_t)ws.bytes) return MOL_E_WORKSPACE;
   if (!aligned16(workspace)) return MOL_E_ALIGN;
 
@@ -895,8 +901,8 @@ MOL_API mol_status mol_moe_layer(const mol_moe_weights* w, const mol_moe_adapter
   const int64_t V = (int64_t)E * (adapters ? adapters->num_slots : 0);
   a.rank_by_pair = a.numel <= V;
   a.rank_slots = adapters ? (int32_t)std::min<int64_t>(a.numel, V) : 0;
-  a.direct = layer_direct(M, r);
   auto row_bytes = [&](int64_t K) { return G ? K / 2 : K * esz; };
+  a.direct = layer_direct(M, r, topk, row_bytes(I));
   const mol::StreamItems gu =
       mol::stream_items(a.slots, a.numel, 2 * (int64_t)I, row_bytes(H));
   const mol::StreamItems dn = mol::stream_items(a.slots, a.numel, H, row_bytes(I));

@@ -58,12 +58,18 @@ def product(W, mag, x):
 
 
 def layer(x, gate_up, down, ids, weights, eps, adapters=None, lora=None, rows_rounded=False):
-    """y [M, H] of a whole layer in 64 bits, and a bound on what an implementation with fp32 sums,
-    h and y rounded to a type of half-ulp eps / 2, may be off by. gate_up and down: functions
+    """y [M, H] of a whole layer in 64 bits, and a bound on what an implementation with fp32 sums
+    and y rounded to a type of half-ulp eps / 2 may be off by. Where that type is bf16, h and the
+    adapters' s enter their products as two bf16 terms: the first is cut off to 8 bits, which
+    leaves less than 2^-7 of the value, and that is rounded to 8 bits, so 2^-16 of the value is
+    lost at most (or, as the second term may fall below the smallest normal number, 2^-126).
+    gate_up and down: functions
     from an expert to (W, magnitudes). adapters: (A1, B1, A2, B2, scale, ranks or None). rows_rounded: each
-    stage's rows are rounded to the type before and after the adapter part is added."""
+    stage's rows, and h, are rounded to the type before and after the adapter part is added."""
     M, k = ids.shape
     half = eps / 2
+    cut = 2.0 ** -16 if eps > 1e-6 else 0.0
+    tiny = 2.0 ** -126
     y = err = None
     for m in range(M):
         for j in range(k):
@@ -88,6 +94,7 @@ def layer(x, gate_up, down, ids, weights, eps, adapters=None, lora=None, rows_ro
                 v, c = t + l * E, float(scale[l])
                 for part, rows in ((slice(0, I), slice(0, rl)), (slice(I, 2 * I), slice(r, r + rl))):
                     s, es = product(A1[v, rows], np.abs(A1[v, rows]), x[m])
+                    es = es + cut * (np.abs(s) + es) + tiny
                     d, ed = product(B1[v, part, :rl], np.abs(B1[v, part, :rl]), s)
                     gu[part] += c * d
                     egu[part] += abs(c) * (ed + es @ np.abs(B1[v, part, :rl]).T) + 2 * U24 * np.abs(c * d)
@@ -99,7 +106,7 @@ def layer(x, gate_up, down, ids, weights, eps, adapters=None, lora=None, rows_ro
             h = silu * u
             eh = (1.1 * egu[:I] * np.abs(u) + np.abs(silu) * egu[I:] + 1.1 * egu[:I] * egu[I:] +
                   16 * U24 * np.abs(h))
-            eh = eh + half * (np.abs(h) + eh)
+            eh = eh + (half if rows_rounded else cut) * (np.abs(h) + eh) + tiny
             z, ez = product(W2, mag2, h)
             ez = ez + eh @ np.abs(W2).T * (1 + 1e-3)
             if rows_rounded:
@@ -107,6 +114,7 @@ def layer(x, gate_up, down, ids, weights, eps, adapters=None, lora=None, rows_ro
             if rl:
                 s, es = product(A2[v, :rl], np.abs(A2[v, :rl]), h)
                 es = es + eh @ np.abs(A2[v, :rl]).T
+                es = es + cut * (np.abs(s) + es) + tiny
                 d, ed = product(B2[v, :, :rl], np.abs(B2[v, :, :rl]), s)
                 z = z + c * d
                 ez = ez + abs(c) * (ed + es @ np.abs(B2[v, :, :rl]).T) + 2 * U24 * np.abs(c * d)

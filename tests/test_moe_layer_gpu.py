@@ -150,6 +150,74 @@ def test_many_pairs_over_long_rows(M, E, group):
         Layer("f32", 1040, 516, E, 2, 8, seed=M).run(M, 2)
 
 
+@pytest.mark.parametrize("dtype,group", [("bf16", 0), ("bf16", 32), ("bf16", 64), ("bf16", 128),
+                                         ("f32", 0), ("f32", 32)])
+@pytest.mark.parametrize("M,topk,E", [(1, 64, 70), (1, 17, 5), (1, 1, 3), (2, 8, 9), (3, 8, 6),
+                                      (3, 2, 4), (3, 64, 64), (4, 8, 9)])
+def test_few_tokens_without_adapters(dtype, group, M, topk, E):
+    """Down per token, over one tile of experts to sixteen, and the counts around its choice."""
+    Layer(dtype, 128, 1152, E, group=group, zeros=True, seed=topk).run(M, topk, seed=M)
+
+
+@pytest.mark.parametrize("M,topk", [(64, 64), (4096, 1), (1365, 3)])
+@pytest.mark.parametrize("adapters", [False, True])
+def test_the_most_pairs(M, topk, adapters):
+    la = Layer("bf16", 64, 32, 70, 3 if adapters else 0, 8, ranks=(8, 0, 3), seed=M)
+    x, ids, w, lora = la.step(M, topk)
+    ids[M // 2:, 0] = 4                           # an expert of very many pairs
+    got = la.call(x, ids, w, lora)
+    rows = torch.cat((torch.arange(0, 20), torch.arange(M - 20, M)))
+    la.check(x[rows], ids[rows], w[rows], None if lora is None else lora[rows], got[rows.cuda()])
+
+
+@pytest.mark.parametrize("group", [0, 32])
+@pytest.mark.parametrize("M", [2, 50])
+def test_the_most_virtual_experts(group, M):
+    Layer("bf16", 32, 32, 4095, 2, 8, group=group, seed=5).run(M, 8)
+    Layer("f32", 32, 32, 2, 4095, 4, group=group, seed=6).run(M, 2)
+
+
+def test_a_workspace_of_more_tokens():
+    la = Layer("bf16", 96, 64, 6, 2, 16, seed=18)
+    ws = mb.new_moe_layer_workspace(la.w, 50, 4, la.ad)
+    for M, topk in ((50, 4), (1, 4), (7, 2), (100, 2)):
+        b = la.step(M, topk, seed=M)
+        assert torch.equal(la.call(*b, workspace=ws), la.call(*b))
+
+
+@pytest.mark.parametrize("M", [1, 2, 9])
+@pytest.mark.parametrize("group", [0, 128])
+def test_router_and_layer_in_one_graph(M, group):
+    """A decode step without adapters, captured once, replayed over new inputs between eager
+    steps that use the same workspace."""
+    la = Layer("bf16", 256, 1024, 16, group=group, seed=19)
+    x = torch.zeros(M, 256, dtype=torch.bfloat16, device="cuda")
+    logits = torch.zeros(M, 16, device="cuda")
+    ids = torch.zeros(M, 8, dtype=torch.int32, device="cuda")
+    w = torch.zeros(M, 8, device="cuda")
+    y = torch.zeros_like(x)
+    ws = mb.new_moe_layer_workspace(la.w, M, 8)
+
+    def step(y):
+        mb.mol_router_topk(logits, 8, topk_ids=ids, topk_weights=w)
+        return mb.mol_moe_layer(la.w, x, ids, w, y=y, workspace=ws)
+    step(y)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(y)
+    gen = torch.Generator().manual_seed(20)
+    for _ in range(4):
+        x.copy_(torch.randn(M, 256, generator=gen))
+        logits.copy_(torch.randn(M, 16, generator=gen))
+        y.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        got = y.clone()
+        assert torch.equal(got, step(torch.empty_like(y)))
+        la.check(x.cpu(), ids.cpu(), w.cpu(), None, got)
+
+
 def test_decode_layer_width():
     Layer("bf16", 2048, 768, 10, 2, 32, seed=5).run(3, 8)
     Layer("bf16", 6144, 256, 9, 2, 32, seed=6).run(2, 8)

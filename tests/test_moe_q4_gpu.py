@@ -84,6 +84,31 @@ def test_hidden_sizes_of_the_decode_layers():
     check(*(lambda s: (s, call(s)))(draw(1, 4, 2, 8192, 16, 32, True, "f32", 2, seed=7)))
 
 
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("pairs,block_m", [(3, 16), (70, 1), (70, 64)])
+def test_the_longest_rows(group, dtype, pairs, block_m):
+    """256 groups a row: scales and x in many stages, split k's and whole (blocks of one pair make
+    enough items for that)."""
+    st = draw(1100 if block_m == 1 else pairs, 2, 1, 256 * group, 72, group, True, dtype, 1,
+              seed=group)
+    st["ids"][pairs:] = -1
+    check(st, call(st, block_m))
+
+
+def test_two_calls_at_once():
+    a, b = (draw(23, 16, 8, 256, 64, 128, True, "bf16", 8, seed=s) for s in (21, 22))
+    wa, wb = call(a), call(b)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(s1):
+        ga = call(a)
+    with torch.cuda.stream(s2):
+        gb = call(b)
+    torch.cuda.synchronize()
+    assert torch.equal(ga, wa) and torch.equal(gb, wb)
+
+
 def test_ids_past_the_experts_and_no_pairs():
     st = draw(4, 5, 2, 64, 20, 32, False, "f32", 2, seed=8)
     st["ids"] = torch.tensor([[5, -7], [100, 2], [-1, -1], [0, 4]], dtype=torch.int32)

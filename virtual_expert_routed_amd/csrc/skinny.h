@@ -118,8 +118,8 @@ __device__ __forceinline__ float vec_sum(const uint4& v, float s) {
 }
 
 // VE fp32 values as a vector of x: in bf16 as hi + lo, hi cut off rather than rounded (it cannot
-// overflow, and the difference is exact) and lo rounded: 2^-17 of the value is lost. An infinity
-// has no lo.
+// overflow, and the difference, below 2^-7 of it, is exact) and lo rounded: at most 2^-16 of the
+// value is lost. An infinity has no lo.
 template <bool BF16>
 __device__ __forceinline__ XVec split_vec(const float (&f)[BF16 ? 8 : 4]) {
   if constexpr (BF16) {

@@ -277,7 +277,7 @@ __device__ __forceinline__ void rank_part(const LayerArgs& a, const RankPart& rp
 }
 
 template <int G, bool BF16, bool LORA, int KS>
-__global__ void __launch_bounds__(kThreads, G ? 3 : 4) gate_up_kernel(LayerArgs a) {
+__global__ void __launch_bounds__(kThreads, G == 0 || G == 128 ? 4 : 3) gate_up_kernel(LayerArgs a) {
   __shared__ PairList list;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const RowSrc src{(const char*)a.x, a.ld_x * (BF16 ? 2 : 4), list.pair, a.f_topk};
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, G ? 3 : 4) gate_up_kernel(LayerArgs 
 }
 
 template <int G, bool BF16, bool LORA, int KS>
-__global__ void __launch_bounds__(kThreads, G ? 3 : 4) down_kernel(LayerArgs a) {
+__global__ void __launch_bounds__(kThreads, G == 0 || G == 128 ? 4 : 3) down_kernel(LayerArgs a) {
   constexpr int NP = BF16 ? 2 : 1;
   __shared__ PairList list;
   extern __shared__ __attribute__((aligned(16))) char lds[];

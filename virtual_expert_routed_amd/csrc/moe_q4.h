@@ -15,7 +15,7 @@ namespace mol {
 namespace {
 
 template <int G, bool BF16, int KS>
-__global__ void __launch_bounds__(kThreads, 3) q4_gemm_kernel(Q4GemmArgs a) {
+__global__ void __launch_bounds__(kThreads, G == 128 ? 4 : 3) q4_gemm_kernel(Q4GemmArgs a) {
   constexpr int kCols = kPassCols<G, BF16, 1, KS>;
   __shared__ int pair[kCols];
   __shared__ __attribute__((aligned(16))) char lds[StreamLds<G, BF16>::kBytes];

@@ -172,12 +172,35 @@ struct Stream {
   static_assert((NV & (NV - 1)) == 0, "a stage's vectors are told apart by shifts");
 };
 
+// The scale and the offset c + z of a group in LDS. bf16: the scale's 16 bits over the offset as fp16
+// (integers up to 271: exact), half the LDS of two floats.
+template <bool BF16>
+struct Q4Scale {
+  float2 v;
+  __device__ __forceinline__ float scale() const { return v.x; }
+  __device__ __forceinline__ float offset() const { return v.y; }
+  static __device__ __forceinline__ Q4Scale of(float scale, float offset) {
+    return {make_float2(scale, offset)};
+  }
+};
+template <>
+struct Q4Scale<true> {
+  uint32_t v;
+  __device__ __forceinline__ float scale() const { return __uint_as_float(v & 0xffff0000u); }
+  __device__ __forceinline__ float offset() const {
+    return (float)__builtin_bit_cast(_Float16, (uint16_t)v);
+  }
+  static __device__ __forceinline__ Q4Scale of(float scale, float offset) {
+    return {__float_as_uint(scale) | __builtin_bit_cast(uint16_t, (_Float16)offset)};
+  }
+};
+
 // Bytes of LDS: x, then sums of x per group and column, then each wave's scales.
 template <int G, bool BF16>
 struct StreamLds {
   // (a stage of CW columns and NP planes has kXHalf / (64 CW NP) x steps)
   static constexpr int kSums = G ? 2 * (kXHalf / 64 / (BF16 ? 4 : 8)) * (kQ4Load / (G ? G : 1)) * 4 : 0;
-  static constexpr int kScales = G ? kWaves * kMaxGroups<G> * kTileRows * 8 : 0;
+  static constexpr int kScales = G ? kWaves * kMaxGroups<G> * kTileRows * (int)sizeof(Q4Scale<BF16>) : 0;
   static constexpr int kBytes = 2 * kXHalf + kSums + kScales;
 };
 
@@ -329,12 +352,11 @@ struct ScaleRegs {
       for (int i = 0; i < N; ++i) z[i] = (float)(q.zeros + at)[min(i * 4 + quad, gn - 1)];
     }
   }
-  __device__ __forceinline__ void store(float2* sc, int gn, int lane) const {  // scale, (c + z) * scale
+  __device__ __forceinline__ void store(Q4Scale<BF16>* sc, int gn, int lane) const {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {  // groups past the row: zeros
-      const float f = i * 4 + (lane >> 4) < gn ? s[i] : 0.f;
-      sc[i * 64 + lane] = make_float2(f, f * (kQ4Offset<BF16> + z[i]));
-    }
+    for (int i = 0; i < N; ++i)  // groups past the row: a scale of zero
+      sc[i * 64 + lane] = Q4Scale<BF16>::of(i * 4 + (lane >> 4) < gn ? s[i] : 0.f,
+                                            kQ4Offset<BF16> + z[i]);
   }
 };
 
@@ -382,11 +404,12 @@ __device__ __forceinline__ void stream_rows(char* lds, __amdgpu_buffer_rsrc_t rs
   for (int i = 0; i < 4; ++i) slot[i] = quad * CW + ((col & (CW - 1)) ^ x_rot<CW>(i, quad));
   uint4* const xs = reinterpret_cast<uint4*>(lds);
   float* const sums = reinterpret_cast<float*>(lds + 2 * kXHalf);
-  float2* const sc = reinterpret_cast<float2*>(lds + 2 * kXHalf + StreamLds<G, BF16>::kSums) +
+  using Scale = Q4Scale<BF16>;
+  Scale* const sc = reinterpret_cast<Scale*>(lds + 2 * kXHalf + StreamLds<G, BF16>::kSums) +
                      (KS > 1 ? 0 : wv) * (kMaxGroups<G> * kTileRows);
 
   // the products of register u, in a round that starts at xb, sumb and scb
-  auto products = [&](int u, const uint4* xb, const float* sumb, const float2* scb)
+  auto products = [&](int u, const uint4* xb, const float* sumb, const Scale* scb)
                       __attribute__((always_inline)) {
     auto x_at = [&](int step, int t, int plane) __attribute__((always_inline)) {  // of the round
       return xb[slot[step & 3] + step * (4 * CW) + t * 16 + plane * S::PLANE];
@@ -429,15 +452,14 @@ __device__ __forceinline__ void stream_rows(char* lds, __amdgpu_buffer_rsrc_t rs
             }
           }
         }
-        float2 f[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = scb[(u * S::GPL + g) * kTileRows + i];
+        struct alignas(16) { Scale row[4]; } f;  // (one or two 16-byte reads)
+        __builtin_memcpy(&f, __builtin_assume_aligned(scb + (u * S::GPL + g) * kTileRows, 16), sizeof f);
 #pragma unroll
         for (int t = 0; t < S::T; ++t) {
           const float sx = sumb[(u * S::GPL + g) * CW + t * 16];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            acc[t][i] = fmaf(-f[i].y, sx, fmaf(f[i].x, prod[t][i], acc[t][i]));
+            acc[t][i] = fmaf(f.row[i].scale(), fmaf(-f.row[i].offset(), sx, prod[t][i]), acc[t][i]);
         }
       }
     }
@@ -451,7 +473,7 @@ __device__ __forceinline__ void stream_rows(char* lds, __amdgpu_buffer_rsrc_t rs
     asm volatile("" : "+s"(o));
     const uint4* xb = xs_ + o * (S::LX * 4 * CW);
     const float* sumb = sums_ + o * (S::GPL * CW) + (col & (CW - 1));
-    const float2* scb = sc + o * (S::GPL * kTileRows) + quad * 4;
+    const Scale* scb = sc + o * (S::GPL * kTileRows) + quad * 4;
 #pragma unroll
     for (int u = 0; u < S::U; ++u) {
       products(u, xb, sumb, scb);

@@ -201,11 +201,15 @@ struct RouterArgs {
 
 // The work items of a stream of weight rows: 64 rows times `tiles`, or 16 rows whose k's four waves
 // split. All read the same bytes.
-//  - 16 rows where 64 would make fewer than 1024 items for the chip's 256 CUs.
+//  - 16 rows where 64 would make fewer than 384 items for the chip's 256 CUs. 4-bit rows of K 2048,
+//    items of 64 against split ones: 16 items 33.5 and 17.3 us (fp32), 192 items 9.8 and 8.7; as whole
+//    calls 384 items 14.3 and 15.5, 768 items 16.4 and 23.0.
 //  - Several tiles where 64 rows hold few bytes, so that finding the pairs and staging x (microseconds
-//    of latency for each item) is paid once for up to 128 KiB of weights; only while matrices have
-//    few columns (`pairs` at most four a matrix on average): items over many columns are long, and
-//    fewer of them leave CUs idle.
+//    of latency for each item) is paid once for up to 96 KiB of weights (4-bit down of 23 tokens,
+//    K 768: 26 against 33 us with one tile; K 2048, whose tile is 64 KiB: two take 44, one 41 us);
+//    only while matrices have few columns (`pairs` at most four a matrix on average): items over many
+//    columns are long, and fewer of them leave CUs idle (128 tokens, popular experts: 62 with one
+//    tile, 82 us with two).
 struct StreamItems {
   bool split;
   int32_t tiles;
@@ -213,9 +217,9 @@ struct StreamItems {
 };
 inline StreamItems stream_items(int64_t matrices, int64_t pairs, int64_t rows, int64_t row_bytes) {
   auto items = [&](int64_t n) { return (rows + n - 1) / n; };
-  if (matrices * items(64) < 1024) return {true, 1, items(16)};
+  if (matrices * items(64) < 384) return {true, 1, items(16)};
   int32_t tiles = 1;
-  while (tiles < 4 && pairs <= 4 * matrices && 64 * row_bytes * tiles * 2 <= 131072 &&
+  while (tiles < 4 && pairs <= 4 * matrices && 64 * row_bytes * tiles * 2 <= 98304 &&
          matrices * items(64 * tiles * 2) >= 512)
     tiles *= 2;
   return {false, tiles, items(64 * tiles)};

@@ -406,8 +406,8 @@ MOL_API mol_status mol_moe_gemm_q4(int32_t dtype, const void *xin, int64_t ld_x,
  * mol_moe_layer - a whole layer for a few tokens, from the routed ids to the combined rows, with
  * no aligned routing: two launches for a token, or up to three of them, without adapters (gate/up
  * with the activation, down with the combine); three beyond (the combine on its own); four with
- * adapters (the activation too; their products run beside the base ones). For pair p = m * topk + k with a local base expert t = topk_ids[m, k] in [0, E),
- * and l = lora_ids[m] (the adapter terms only for l in [0, S) and slot rank rl > 0, v = t + l * E):
+ * adapters (the activation too; their products run beside the base ones). For pair
+ * p = m * topk + k with a local base expert t = topk_ids[m, k] in [0, E), and l = lora_ids[m] (the adapter terms only for l in [0, S) and slot rank rl > 0, v = t + l * E):
  *   g    = gate_up[t, 0:I] x_m + slot_scale[l] * gate_up_B[v, 0:I, :rl] (gate_up_A[v, 0:rl] x_m)
  *   u    = gate_up[t, I:2I] x_m + slot_scale[l] * gate_up_B[v, I:2I, :rl] (gate_up_A[v, r:r+rl] x_m)
  *   h_p  = g / (1 + exp(-g)) * u

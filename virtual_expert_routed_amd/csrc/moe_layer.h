@@ -7,16 +7,27 @@
 // planes (16 bits of it), so y carries one rounding to bf16.
 //
 // Launches: gate/up, down, and the combine (with adapters the activation too); without adapters,
-// and for very few tokens, down and the combine are one (moe_layer_direct.hip). No launch routes: a workgroup finds its pairs among the M
-// * topk ids itself, which is cheaper than a launch.
+// and for very few tokens, down and the combine are one (moe_layer_direct.hip). No launch routes: a
+// workgroup finds its pairs among the M * topk ids itself, which is cheaper than a launch.
 //
-// Gate/up and down stream weight rows (skinny.h): a work item is 64 rows of one expert for all the
-// pairs that use it (16 rows and split k's where 64 make too few items). Up to E pairs the
-// items are per pair, and a pair whose expert an earlier pair has exits; beyond, per expert.
-// The adapters run beside the base product, in the same launch: an item per virtual expert forms
-// s = A x for its pairs, keeps it in LDS and writes c B s as fp32 rows, which the activation (then
-// a launch of its own) and the combine add to the base rows. Their latency (a dependent chain over a few hundred KiB)
-// hides behind the base product's stream, so these items come first in the grid.
+// Gate/up and down stream weight rows (skinny.h): a work item is 64 rows of one expert or more, for
+// all the pairs that use it (16 rows and split k's where 64 make too few items). Up to E pairs the
+// items are per pair, and a pair whose expert an earlier pair has exits; beyond, per expert (128
+// experts, top-8, calls per pair and per expert: 1 token 23.5 and 40.2 us, 8 tokens 103 and 112, 16
+// tokens 156 and 160). The adapters run beside the base product, in the same launch: an item per
+// virtual expert forms s = A x for its pairs, keeps it in LDS and writes c B s as fp32 rows, which the
+// activation (then a launch of its own) and the combine add to the base rows. Their latency (a
+// dependent chain over a few hundred KiB) hides behind the base product's stream, so these items come
+// first in the grid; as launches of their own before each stage they took 13 and 6 us more at 23 tokens, 59
+// and 23 at 128.
+//
+// Bound by the stream of weights out of HBM. bf16, 128 experts, hidden 2048, inter 768, top-8:
+//   1 token, no adapters      gate/up 13.0 us (50 MB, 3.9 TB/s), direct down 7.8
+//   23 tokens, rank 32 of 8   gate/up 122 us (660 MB, 5.4 TB/s), down 64 (340 MB, 5.3), act 4.9,
+//                             combine 4.8
+//   128 tokens, rank 32 of 16 gate/up 190 us, down 107, act 6.3, combine 5.6
+// 4-bit base weights, 23 tokens: gate/up 56 us, down 35 (240 + 90 MB with the adapters: bound like
+// the 4-bit product, by the latency of items and the unpacking).
 #pragma once
 
 #include <algorithm>
@@ -63,7 +74,9 @@ struct PairsOf {
   int first;
 };
 
-constexpr int kFewPairs = 512;  // every wave looks through all ids itself
+// Up to this many every wave looks through all ids itself, without a barrier: eight loads in flight
+// (one token: 21.3 us a layer, against 23.1 with quarters and barriers).
+constexpr int kFewPairs = 512;
 
 // Fills the list. key: t, or (VIRT) t + l E; the caller knows that slot l has a rank. All loads of a
 // batch of ids are in flight together. Up to kFewPairs there is no barrier: each wave finds the pairs,

@@ -1,4 +1,5 @@
-// A whole mixture-of-experts layer for a few tokens: dense weights, and the choice between the weight formats.
+// A whole mixture-of-experts layer for a few tokens: dense weights, and the choice between the
+// weight formats.
 #include "moe_layer.h"
 
 namespace mol {

@@ -5,7 +5,12 @@
 // blocks of the product are the wanted sums, every loaded weight is used, and the weighted sum
 // over the pairs ends in the item, so neither the pairs' rows nor a combine launch are needed.
 // An expert that several tokens share is read once by each of them; items of a column group are
-// neighbours on one XCD, so most of that comes from its L2.
+// neighbours on one XCD, so most of that comes from its L2. Per token rather than per expert: for one
+// token that saves a launch and a pass over the pairs' rows.
+//
+// Bound by the latency of its one round of loads: 7.8 us for one token (top-8, hidden 2048, inter 768
+// in bf16: 25 MB, 3.2 TB/s). Twelve loads of weights and twelve of h in flight a lane are all of a
+// wave's share there.
 #include "skinny.h"
 
 namespace mol {
@@ -160,7 +165,8 @@ hipError_t launch(const LayerArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-// as many experts in a tile as the token has, up to four
+// As many experts in a tile as the token has, up to four (calls of one token: top-1 13.2 us, against
+// 13.9 with room for four; top-2 14.6 and 15.9).
 template <int G, bool BF16>
 hipError_t by_topk(const LayerArgs& a, hipStream_t st) {
   if (a.topk == 1) return launch<G, BF16, 16>(a, st);

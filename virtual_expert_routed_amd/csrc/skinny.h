@@ -544,7 +544,8 @@ constexpr int kPassCols = KS > 1 ? 8 : (G && !BF16) || NP == 2 ? 32 : kMaxCols;
 
 // The stream of a row of K: staged at once where its x fits both buffers, else in several stages.
 // Loads of W in flight: as many as the registers allow (4-bit: each load's products take many of
-// them; fewer beside the next stage's x), and six where the row has no more.
+// them; fewer beside the next stage's x), and six where the row has no more (rows of 768, groups of
+// 64 or 128, with the items of several tiles: 38 us in rounds of four, 32.5 in one of six).
 template <int G, bool BF16, int CW, int NP, int KS, class Src, class Epi>
 __device__ __forceinline__ void stream_k(char* lds, __amdgpu_buffer_rsrc_t rsrc, uint32_t off,
                                          const Q4Tables& q, int64_t srow, const Src& src, int ncol,
@@ -567,7 +568,9 @@ __device__ __forceinline__ void stream_k(char* lds, __amdgpu_buffer_rsrc_t rsrc,
                                                       epi);
 }
 
-// As many columns as the pass has: 4, 8, 16, 32 or 64.
+// As many columns as the pass has: 4, 8, 16, 32 or 64. A narrow pass leaves room in LDS for longer rows
+// of x in one stage; passes of 64 read a weight once where 16 would read it four times (layer of 128
+// tokens, popular experts: 308 us, and 325 before passes of 64 and the second buffer of x).
 template <int G, bool BF16, int NP, int KS, class Src, class Epi>
 __device__ __forceinline__ void stream_cols(char* lds, __amdgpu_buffer_rsrc_t rsrc, uint32_t off,
                                             const Q4Tables& q, int64_t srow, const Src& src,

@@ -358,6 +358,25 @@ def test_router_then_layer_matches_the_aligned_path(M):
     plain64.within(y2.float().cpu().numpy(), ref, bound)
 
 
+@pytest.mark.parametrize("M", [1, 6])
+def test_weights_past_32_bits(M):
+    """Experts whose rows lie more than 4 GiB into the weights: bit for bit what they give alone."""
+    E, H, I = 400, 2048, 1408
+    gu = torch.zeros(E, 2 * I, H, dtype=torch.bfloat16, device="cuda")
+    dn = torch.zeros(E, H, I, dtype=torch.bfloat16, device="cuda")
+    assert gu.numel() * 2 > 2**32
+    gen = torch.Generator("cuda").manual_seed(21)
+    gu[E - 1].normal_(0, 0.05, generator=gen)
+    dn[E - 1].normal_(0, 0.05, generator=gen)
+    x = torch.randn(M, H, generator=gen, device="cuda").bfloat16()
+    w = torch.ones(M, 1, device="cuda")
+    ids = torch.full((M, 1), E - 1, dtype=torch.int32, device="cuda")
+    got = mb.mol_moe_layer(mb.MoeWeights(gu, dn), x, ids, w)
+    alone = mb.mol_moe_layer(mb.MoeWeights(gu[E - 1:].clone(), dn[E - 1:].clone()), x,
+                             torch.zeros_like(ids), w)
+    assert torch.equal(got, alone) and torch.all(torch.isfinite(got)) and got.abs().max() > 0
+
+
 def test_refusals():
     la = Layer("bf16", 64, 32, 4, 2, 8, seed=16)
     b = [t.cuda() for t in la.step(3, 2)]

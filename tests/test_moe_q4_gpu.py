@@ -96,6 +96,26 @@ def test_the_longest_rows(group, dtype, pairs, block_m):
     check(st, call(st, block_m))
 
 
+def test_weights_past_32_bits():
+    """An expert more than 4 GiB into the weights: bit for bit what it gives alone."""
+    E, N, K, G = 520, 4096, 4096, 128
+    W = torch.zeros(E, N, K // 2, dtype=torch.uint8, device="cuda")
+    sc = torch.zeros(E, N, K // G, dtype=torch.bfloat16, device="cuda")
+    assert W.numel() > 2**32
+    gen = torch.Generator("cuda").manual_seed(22)
+    W[E - 1].random_(0, 256, generator=gen)
+    sc[E - 1].normal_(0, 0.01, generator=gen)
+    x = torch.randn(5, K, generator=gen, device="cuda").bfloat16()
+    outs = []
+    for w, s in ((W, sc), (W[E - 1:].clone(), sc[E - 1:].clone())):
+        ids = torch.full((5, 1), w.shape[0] - 1, dtype=torch.int32, device="cuda")
+        out = torch.zeros(5, N, dtype=torch.bfloat16, device="cuda")
+        outs.append(mb.mol_moe_gemm_q4(x, 1, w, s, *mb.mol_align_block_size(ids, None,
+                                                                           w.shape[0], 1, 16),
+                                       5, 16, out))
+    assert torch.equal(*outs) and outs[0].abs().max() > 0
+
+
 def test_two_calls_at_once():
     a, b = (draw(23, 16, 8, 256, 64, 128, True, "bf16", 8, seed=s) for s in (21, 22))
     wa, wb = call(a), call(b)

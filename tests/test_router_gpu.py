@@ -139,3 +139,17 @@ def test_on_another_stream_and_in_a_graph():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(ids, i2) and torch.equal(w, w2)
+
+
+def test_logits_past_32_bits():
+    """Rows of a buffer of more than 4 GiB."""
+    M, E, ld = 280_000, 16, 8192
+    buf = torch.zeros(M, ld, dtype=torch.bfloat16, device="cuda")
+    assert buf.numel() * 2 > 2**32
+    logits = buf[:, 8:8 + E]
+    logits[:] = torch.randn(M, E, generator=torch.Generator().manual_seed(23)).bfloat16().cuda()
+    ids, w = mb.mol_router_topk(logits, 4)
+    near, wn = mb.mol_router_topk(logits.contiguous(), 4)
+    assert torch.equal(ids, near) and torch.equal(w, wn)
+    want = logits[-1000:].float().cpu().sort(dim=1, descending=True, stable=True).indices[:, :4]
+    assert torch.equal(ids[-1000:].cpu().long(), want)

@@ -385,8 +385,10 @@ MOL_API mol_status mol_router_topk(int32_t dtype, const void *logits, int64_t ld
  * mol_moe_gemm_q4 - mol_moe_gemm's base product over such weights:
  *   out[p, n] = round( sum_k (q[t,n,k] - z[t,n,k/G]) * scale[t,n,k/G] * xin[p / row_div, k] )
  * for every pair p with a local base expert t in [0, E); other rows are untouched. Summed in
- * fp32, the scale applied to a group's sum, rounded once. num_experts = 1 and ids of zero give the
- * product with a single matrix.
+ * fp32, the scale applied to a group's sum, rounded once; a sum that is not finite then (an infinite
+ * x, or values near the largest float) is formed again from its terms, each weight scaled first, so
+ * infinities and NaN are the formula's. num_experts = 1 and ids of zero give the product with a
+ * single matrix.
  *   dtype         MOL_F32 or MOL_BF16: xin, scales and out
  *   W             uint8 [E, N, K / 2], 16-byte aligned;  scales [E, N, K / group], aligned to
  *                 its element;  zeros uint8 [E, N, K / group] or NULL

@@ -231,8 +231,11 @@ __device__ __forceinline__ void rank_part(const LayerArgs& a, const RankPart& rp
     }
     const int ncol = min(COLS, total - j0);
     for (int r0 = 0; r0 < R; r0 += kItemRows) {
-      const int row0 = wave_row0<1>(r0), row = row0 + col;
-      const uint32_t off = in_rank(row) ? (uint32_t)row * (uint32_t)(rp.K * ESZ) : kOutOfRange;
+      const int row0 = wave_row0<1>(r0);
+      auto row_at = [&](int i) {
+        const int row = row0 + i;
+        return RowAt{in_rank(row) ? (uint32_t)row * (uint32_t)(rp.K * ESZ) : kOutOfRange, -1};
+      };
       auto keep = [&](int c, const f32x4_t& acc) {
         if (c >= ncol) return;
 #pragma unroll
@@ -242,9 +245,9 @@ __device__ __forceinline__ void rank_part(const LayerArgs& a, const RankPart& rp
         }
       };
       if (ncol <= 4)
-        stream_k<0, BF16, 4, NP, 1>(lds, ra, off, Q4Tables{}, -1, src, ncol, rp.K, r0 > 0, keep);
+        stream_k<0, BF16, 4, NP, 1>(lds, ra, row_at(col), row_at, Q4Tables{}, src, ncol, rp.K, r0 > 0, keep);
       else
-        stream_k<0, BF16, 16, NP, 1>(lds, ra, off, Q4Tables{}, -1, src, ncol, rp.K, r0 > 0, keep);
+        stream_k<0, BF16, 16, NP, 1>(lds, ra, row_at(col), row_at, Q4Tables{}, src, ncol, rp.K, r0 > 0, keep);
     }
     __syncthreads();
     // B s: the operand rows of B are 16 bytes of rank a lane and step, s in two planes (bf16)
@@ -323,17 +326,19 @@ __global__ void __launch_bounds__(kThreads, G == 0 || G == 128 ? 4 : 3) gate_up_
       // With adapters the tile is 16 consecutive rows of gate and up; without, 8 gate rows and
       // their up rows, the two of a column in one lane: rows 4 q, 4 q + 1 are gate columns i0 + 2 q,
       // + 1 and rows 4 q + 2, 4 q + 3 the same up columns (i0 half of the tile's first row).
-      const int r0 = wave_row0<KS>(n0 + t * kItemRows), r = lane & 15;
-      int n;  // this lane's weight row, or -1
-      if constexpr (LORA) {
-        n = r0 + r < 2 * a.I ? r0 + r : -1;
-      } else {
-        const int i = r0 / 2 + (r >> 2) * 2 + (r & 1);
-        n = i < a.I ? ((r & 2) ? a.I : 0) + i : -1;
-      }
+      const int r0 = wave_row0<KS>(n0 + t * kItemRows);
+      auto row_at = [&](int r) {
+        int n;
+        if constexpr (LORA) {
+          n = r0 + r < 2 * a.I ? r0 + r : -1;
+        } else {
+          const int i = r0 / 2 + (r >> 2) * 2 + (r & 1);
+          n = i < a.I ? ((r & 2) ? a.I : 0) + i : -1;
+        }
+        return n >= 0 ? RowAt{(uint32_t)(n * rb), (int64_t)e * 2 * a.I + n} : RowAt{kOutOfRange, -1};
+      };
       stream_cols<G, BF16, 1, KS>(
-          lds, rsrc, n >= 0 ? (uint32_t)(n * rb) : kOutOfRange, q,
-          n >= 0 ? (int64_t)e * 2 * a.I + n : (int64_t)-1, src, ncol, a.H, t > 0,
+          lds, rsrc, row_at(lane & 15), row_at, q, src, ncol, a.H, t > 0,
           [&](int c, const f32x4_t& acc) {
             if (c >= ncol) return;
             const int64_t p = list.pair[c];
@@ -393,10 +398,13 @@ __global__ void __launch_bounds__(kThreads, G == 0 || G == 128 ? 4 : 3) down_ker
     const int ncol = min(kPassCols<G, BF16, NP, KS>, total - j0);
 #pragma unroll 1
     for (int t = 0; t < (KS > 1 ? 1 : a.dn_tiles); ++t) {
-      const int r0 = wave_row0<KS>(n0 + t * kItemRows), n = r0 + (lane & 15);
+      const int r0 = wave_row0<KS>(n0 + t * kItemRows);
+      auto row_at = [&](int i) {
+        const int n = r0 + i;
+        return n < a.H ? RowAt{(uint32_t)(n * rb), (int64_t)e * a.H + n} : RowAt{kOutOfRange, -1};
+      };
       stream_cols<G, BF16, NP, KS>(
-          lds, rsrc, n < a.H ? (uint32_t)(n * rb) : kOutOfRange, q,
-          n < a.H ? (int64_t)e * a.H + n : (int64_t)-1, src, ncol, a.I, t > 0,
+          lds, rsrc, row_at(lane & 15), row_at, q, src, ncol, a.I, t > 0,
           [&](int c, const f32x4_t& acc) {
             const int at = r0 + quad * 4;  // H is a multiple of 4
             if (c < ncol && at < a.H)

@@ -56,10 +56,13 @@ __global__ void __launch_bounds__(kThreads, G == 128 ? 4 : 3) q4_gemm_kernel(Q4G
     if (ncol == 0) return;
 #pragma unroll 1
     for (int t = 0; t < (KS > 1 ? 1 : a.tiles); ++t) {
-      const int r0 = wave_row0<KS>(n0 + t * kItemRows), n = r0 + (lane & 15);
+      const int r0 = wave_row0<KS>(n0 + t * kItemRows);
+      auto row_at = [&](int i) {
+        const int n = r0 + i;
+        return n < a.N ? RowAt{(uint32_t)(n * rb), (int64_t)e * a.N + n} : RowAt{kOutOfRange, -1};
+      };
       stream_cols<G, BF16, 1, KS>(
-          lds, rsrc, n < a.N ? (uint32_t)(n * rb) : kOutOfRange, q,
-          n < a.N ? (int64_t)e * a.N + n : (int64_t)-1, src, ncol, a.K, t > 0,
+          lds, rsrc, row_at(lane & 15), row_at, q, src, ncol, a.K, t > 0,
           [&](int c, const f32x4_t& acc) {
             if (c >= ncol) return;
             const int m = r0 + quad * 4;

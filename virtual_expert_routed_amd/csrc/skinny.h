@@ -26,7 +26,8 @@
 // fp32, q is converted. The products with x are summed per group, and
 //   sum_k (q - z) x = sum_k (q + c) x - (c + z) sum_k x,    c = 16 (bf16) or 0 (fp32)
 // with sum_k x formed in fp32 while x is staged. Everything after the operands is fp32, and the
-// scale is applied once per group.
+// scale is applied once per group. An infinite x makes both terms infinite, and a large one may take them
+// past fp32's range: sums that are not finite at the end are formed again term by term (form_again).
 #pragma once
 
 #include "delta_common.h"
@@ -332,6 +333,80 @@ struct Q4Tables {
   int ng;  // groups of a row
 };
 
+// Where a weight row is: its byte offset in the matrix (kOutOfRange: there is none), and its row in
+// the scale tables (negative: none).
+struct RowAt {
+  uint32_t off;
+  int64_t srow;
+};
+
+// ---- sums that are not finite, term by term ----
+
+// The elements of a vector of x, of its planes together (exact: 16 bits of them at most).
+template <bool BF16, int NP>
+__device__ __forceinline__ void x_elems(const XVec& x, float (&f)[BF16 ? 8 : 4]) {
+  const uint32_t h[4] = {x.hi.x, x.hi.y, x.hi.z, x.hi.w}, l[4] = {x.lo.x, x.lo.y, x.lo.z, x.lo.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (BF16) {
+      f[2 * i] = NP == 2 ? bf16_lo(h[i]) + bf16_lo(l[i]) : bf16_lo(h[i]);
+      f[2 * i + 1] = NP == 2 ? bf16_hi(h[i]) + bf16_hi(l[i]) : bf16_hi(h[i]);
+    } else {
+      f[i] = __uint_as_float(h[i]);
+    }
+  }
+}
+
+// Whether the row of x holds a NaN (a wave together).
+template <bool BF16, int NP, class Src>
+__device__ __forceinline__ bool holds_nan(const Src& src, const char* row, int K, int lane) {
+  constexpr int VE = BF16 ? 8 : 4;
+  bool nan = false;
+  for (int v = lane; v < K / VE; v += 64) {
+    float f[VE];
+    x_elems<BF16, NP>(src(row, v), f);
+#pragma unroll
+    for (int i = 0; i < VE; ++i) nan |= f[i] != f[i];
+  }
+  return __builtin_amdgcn_ballot_w64(nan) != 0;
+}
+
+// sum_k W[k] x[k] by a wave, each weight formed first: (q - z) * s of 4-bit ones.
+template <int G, bool BF16, int NP, class Src>
+__device__ __forceinline__ float sum_of_terms(__amdgpu_buffer_rsrc_t rsrc, const RowAt& at,
+                                              const Q4Tables& q, const Src& src, const char* row,
+                                              int K, int lane) {
+  constexpr int VE = BF16 ? 8 : 4, KU = G ? 32 : VE;  // k's of 16 bytes of W
+  float sum = 0.f;
+  for (int u = lane; u < K / KU; u += 64) {
+    const uint4 wv = buf16(rsrc, at.off + (uint32_t)u * 16u);
+    const uint32_t w[4] = {wv.x, wv.y, wv.z, wv.w};
+    float s = 0.f, z = 8.f;
+    if constexpr (G > 0) {
+      const int64_t g = at.srow * q.ng + u * KU / G;
+      s = BF16 ? __uint_as_float((uint32_t)((const uint16_t*)q.scales)[g] << 16)
+               : ((const float*)q.scales)[g];
+      if (q.zeros) z = (float)q.zeros[g];
+    }
+#pragma unroll
+    for (int v = 0; v < KU / VE; ++v) {
+      float f[VE];
+      x_elems<BF16, NP>(src(row, u * (KU / VE) + v), f);
+#pragma unroll
+      for (int i = 0; i < VE; ++i) {
+        float e;
+        if constexpr (G > 0) e = ((float)((w[(v * VE + i) / 8] >> (4 * ((v * VE + i) % 8))) & 15u) - z) * s;
+        else if constexpr (BF16) e = i % 2 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+        else e = __uint_as_float(w[i]);
+        sum = fmaf(e, f[i], sum);
+      }
+    }
+  }
+  return group_sum<64>(sum);
+}
+
+// ---- the stream of weight rows ----
+
 // Scales of a stage's groups on their way to LDS: this lane's row (lane % 16), every fourth group.
 template <int G, bool BF16>
 struct ScaleRegs {
@@ -361,15 +436,14 @@ struct ScaleRegs {
 };
 
 // Runs one item against ncol columns: this wave's 16 rows, or with KS = kWaves the same rows in
-// all waves, which split their k's. off: this lane's row (lane % 16) as a byte offset into the
-// matrix, kOutOfRange for none; srow: its row in the scale tables, negative for none.
+// all waves, which split their k's. me: this lane's row (lane % 16); row_at(i): row i of the 16.
 // epilogue(col, acc) gets, on every lane (of wave 0 for KS = kWaves), column col's sums of tile
 // rows 4 * quad + i; only columns below ncol and rows that exist are meant. All four waves take
 // part in the barriers; on return LDS may still be read by slower waves.
-template <int G, bool BF16, int CW, int NP, int KS, bool MULTI, int UM, class Src, class Epi>
-__device__ __forceinline__ void stream_rows(char* lds, __amdgpu_buffer_rsrc_t rsrc, uint32_t off,
-                                            const Q4Tables& q, int64_t srow, const Src& src,
-                                            int ncol, int K, bool staged, Epi epilogue) {
+template <int G, bool BF16, int CW, int NP, int KS, bool MULTI, int UM, class Rows, class Src, class Epi>
+__device__ __forceinline__ void stream_rows(char* lds, __amdgpu_buffer_rsrc_t rsrc,
+                                            const RowAt& me, const Rows& row_at,
+                                            const Q4Tables& q, const Src& src, int ncol, int K, bool staged, Epi epilogue) {
   using S = Stream<G, BF16, CW, NP, KS, MULTI, UM>;
   // (opaque to the compiler, which would otherwise compute every variant's addresses ahead of the
   // loop over passes and spill them)
@@ -388,7 +462,7 @@ __device__ __forceinline__ void stream_rows(char* lds, __amdgpu_buffer_rsrc_t rs
   // every load is issued: past the row (and for rows that are not there) it reads zeros and
   // moves nothing
   const int k_left = K - quad * (S::KL / 4);  // k's from this lane's part of load 0 on
-  const uint32_t lane_off = off + (uint32_t)quad * 16u;
+  const uint32_t lane_off = me.off + (uint32_t)quad * 16u;
   auto load = [&](int l) __attribute__((always_inline)) {
     return buf16(rsrc, l * S::KL < k_left ? lane_off + (uint32_t)l * 64u : kOutOfRange);
   };
@@ -483,7 +557,7 @@ __device__ __forceinline__ void stream_rows(char* lds, __amdgpu_buffer_rsrc_t rs
 
   ScaleRegs<G ? G : 32, BF16> regs;
   auto groups_at = [&](int l0) { return min(cl * S::GPL, q.ng - l0 * S::GPL); };
-  if constexpr (G > 0) regs.load(q, srow, 0, groups_at(0), quad);
+  if constexpr (G > 0) regs.load(q, me.srow, 0, groups_at(0), quad);
   if constexpr (!MULTI) {
     if (!staged) {
       __syncthreads();  // the columns' pairs are written down, and LDS is free
@@ -510,7 +584,7 @@ __device__ __forceinline__ void stream_rows(char* lds, __amdgpu_buffer_rsrc_t rs
       int t1 = tid;  // (opaque again: addresses are computed anew for each stage, not kept)
       asm volatile("" : "+v"(t1));
       if (more) {
-        if constexpr (G > 0) regs.load(q, srow, l1 * S::GPL, groups_at(l1), (t1 & 63) >> 4);
+        if constexpr (G > 0) regs.load(q, me.srow, l1 * S::GPL, groups_at(l1), (t1 & 63) >> 4);
         stage.load(src, ncol, v1, vend, t1);
       }
       const uint4* xh = xs + buf * (S::XS * 4 * CW);
@@ -536,6 +610,48 @@ __device__ __forceinline__ void stream_rows(char* lds, __amdgpu_buffer_rsrc_t rs
   }
 #pragma unroll
   for (int t = 0; t < S::T; ++t) epilogue(t * 16 + col, acc[t]);
+
+  // Sums that are not finite once more, each from its terms, and out again over the first: an infinite x, or
+  // a sum past fp32's range on the way, then gives what the definition gives. Columns whose x holds a
+  // NaN are left: all their sums are NaN.
+  if constexpr (G > 0) {
+    bool odd = false;
+#pragma unroll
+    for (int t = 0; t < S::T; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) odd |= t * 16 + col < ncol && !__builtin_isfinite(acc[t][i]);
+    if (!__builtin_amdgcn_ballot_w64(odd)) return;
+#pragma unroll 1
+    for (int c = 0; c < ncol; ++c) {
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = acc[0][i];
+#pragma unroll
+        for (int t = 1; t < S::T; ++t) v[i] = c >> 4 == t ? acc[t][i] : v[i];
+      }
+      uint32_t rows = 0;  // those of the tile to form again
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t m = __builtin_amdgcn_ballot_w64(!__builtin_isfinite(v[i])) >> (c & 15);
+        rows |= ((uint32_t)(m & 1) | (uint32_t)(m >> 16 & 1) << 4 | (uint32_t)(m >> 32 & 1) << 8 |
+                 (uint32_t)(m >> 48 & 1) << 12) << i;
+      }
+      if (rows == 0) continue;
+      const char* x = src.row(c);
+      if (holds_nan<BF16, NP>(src, x, K, lane)) continue;
+#pragma unroll 1
+      for (; rows; rows &= rows - 1) {
+        const int r = __builtin_ctz(rows);
+        const RowAt at = row_at(r);
+        if (at.off == kOutOfRange) continue;
+        const float sum = sum_of_terms<G, BF16, NP>(rsrc, at, q, src, x, K, lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = quad * 4 + i == r ? sum : v[i];
+      }
+      epilogue(col == (c & 15) ? c : ncol, f32x4_t{v[0], v[1], v[2], v[3]});
+    }
+  }
 }
 
 // The most columns of a pass.
@@ -546,47 +662,47 @@ constexpr int kPassCols = KS > 1 ? 8 : (G && !BF16) || NP == 2 ? 32 : kMaxCols;
 // Loads of W in flight: as many as the registers allow (4-bit: each load's products take many of
 // them; fewer beside the next stage's x), and six where the row has no more (rows of 768, groups of
 // 64 or 128, with the items of several tiles: 38 us in rounds of four, 32.5 in one of six).
-template <int G, bool BF16, int CW, int NP, int KS, class Src, class Epi>
-__device__ __forceinline__ void stream_k(char* lds, __amdgpu_buffer_rsrc_t rsrc, uint32_t off,
-                                         const Q4Tables& q, int64_t srow, const Src& src, int ncol,
-                                         int K, bool staged, Epi epi) {
+template <int G, bool BF16, int CW, int NP, int KS, class Rows, class Src, class Epi>
+__device__ __forceinline__ void stream_k(char* lds, __amdgpu_buffer_rsrc_t rsrc, const RowAt& me,
+                                         const Rows& row_at, const Q4Tables& q, const Src& src,
+                                         int ncol, int K, bool staged, Epi epi) {
   constexpr int UM = G == 0 || G == 128 ? 8 : G == 64 ? 4 : 2;
   using S = Stream<G, BF16, CW, NP, KS, false, UM>;
   if constexpr (CW <= 16) {
     if constexpr (G >= 64 && BF16 && KS == 1 && S::ONE >= 6) {
       if (K > 4 * kQ4Load && K <= 6 * kQ4Load) {
-        stream_rows<G, BF16, CW, NP, KS, false, 6>(lds, rsrc, off, q, srow, src, ncol, K, staged, epi);
+        stream_rows<G, BF16, CW, NP, KS, false, 6>(lds, rsrc, me, row_at, q, src, ncol, K, staged, epi);
         return;
       }
     }
     if (K <= S::ONE * S::KL) {
-      stream_rows<G, BF16, CW, NP, KS, false, UM>(lds, rsrc, off, q, srow, src, ncol, K, staged, epi);
+      stream_rows<G, BF16, CW, NP, KS, false, UM>(lds, rsrc, me, row_at, q, src, ncol, K, staged, epi);
       return;
     }
   }
-  stream_rows<G, BF16, CW, NP, KS, true, (G ? 2 : 8)>(lds, rsrc, off, q, srow, src, ncol, K, false,
+  stream_rows<G, BF16, CW, NP, KS, true, (G ? 2 : 8)>(lds, rsrc, me, row_at, q, src, ncol, K, false,
                                                       epi);
 }
 
 // As many columns as the pass has: 4, 8, 16, 32 or 64. A narrow pass leaves room in LDS for longer rows
 // of x in one stage; passes of 64 read a weight once where 16 would read it four times (layer of 128
 // tokens, popular experts: 308 us, and 325 before passes of 64 and the second buffer of x).
-template <int G, bool BF16, int NP, int KS, class Src, class Epi>
-__device__ __forceinline__ void stream_cols(char* lds, __amdgpu_buffer_rsrc_t rsrc, uint32_t off,
-                                            const Q4Tables& q, int64_t srow, const Src& src,
-                                            int ncol, int K, bool staged, Epi epi) {
+template <int G, bool BF16, int NP, int KS, class Rows, class Src, class Epi>
+__device__ __forceinline__ void stream_cols(char* lds, __amdgpu_buffer_rsrc_t rsrc,
+                                            const RowAt& me, const Rows& row_at,
+                                            const Q4Tables& q, const Src& src, int ncol, int K, bool staged, Epi epi) {
   constexpr int MOST = kPassCols<G, BF16, NP, KS>;
   if (ncol <= 4) {
-    stream_k<G, BF16, 4, NP, KS>(lds, rsrc, off, q, srow, src, ncol, K, staged, epi);
+    stream_k<G, BF16, 4, NP, KS>(lds, rsrc, me, row_at, q, src, ncol, K, staged, epi);
   } else if (MOST == 8 || ncol <= 8) {
-    stream_k<G, BF16, 8, NP, KS>(lds, rsrc, off, q, srow, src, ncol, K, staged, epi);
+    stream_k<G, BF16, 8, NP, KS>(lds, rsrc, me, row_at, q, src, ncol, K, staged, epi);
   } else if constexpr (MOST > 8) {
     if (ncol <= 16)
-      stream_k<G, BF16, 16, NP, 1>(lds, rsrc, off, q, srow, src, ncol, K, staged, epi);
+      stream_k<G, BF16, 16, NP, 1>(lds, rsrc, me, row_at, q, src, ncol, K, staged, epi);
     else if (MOST == 32 || ncol <= 32)
-      stream_k<G, BF16, 32, NP, 1>(lds, rsrc, off, q, srow, src, ncol, K, staged, epi);
+      stream_k<G, BF16, 32, NP, 1>(lds, rsrc, me, row_at, q, src, ncol, K, staged, epi);
     else if constexpr (MOST > 32)
-      stream_k<G, BF16, 64, NP, 1>(lds, rsrc, off, q, srow, src, ncol, K, staged, epi);
+      stream_k<G, BF16, 64, NP, 1>(lds, rsrc, me, row_at, q, src, ncol, K, staged, epi);
   }
 }
 

@@ -116,3 +116,60 @@ def test_infinite_x_over_a_4bit_layer(dtype, group, adapters, M, topk, E, H, I):
     ref, bound = layer64(la, x[rows], ids[rows], w[rows], None if lora is None else lora[rows])
     assert np.isinf(ref[0]).all() and np.isnan(ref[1]).all()
     agrees(got[rows.cuda()].float().cpu().numpy(), ref, bound)
+
+
+# ---- down per token (one token; up to three with large items), without adapters
+
+
+@pytest.mark.parametrize("M,topk,E,I", [(1, 1, 3, 128), (1, 2, 3, 256), (1, 8, 9, 128), (1, 20, 24, 128), (2, 8, 9, 2048),
+                                        (3, 8, 9, 2048)])
+@pytest.mark.parametrize("dtype,group", [("bf16", 32), ("bf16", 64), ("bf16", 128), ("f32", 32), ("f32", 128)])
+def test_infinite_x_of_one_token_over_a_4bit_layer(dtype, group, M, topk, E, I):
+    la = Layer(dtype, 128, I, E, group=group, seed=I + topk)
+    positive_4bit(la, 2)
+    x, ids, w, lora = la.step(M, topk, sentinels=False)
+    ids[0, topk // 2] = -1 if topk > 2 else ids[0, topk // 2]
+    x = x.abs() * 0.1
+    clean = la.call(x, ids, w, lora)
+    la.check(x, ids, w, lora, clean)
+    x[M - 1, 9] = INF
+    got = la.call(x, ids, w, lora)
+    assert torch.equal(got[:M - 1], clean[:M - 1])
+    ref, bound = layer64(la, x[M - 1:], ids[M - 1:], w[M - 1:], None)
+    assert np.isinf(ref).all()
+    agrees(got[M - 1:].float().cpu().numpy(), ref, bound)
+    x[M - 1, 9] = NAN
+    assert torch.all(torch.isnan(la.call(x, ids, w, lora)[M - 1]))
+
+
+@pytest.mark.parametrize("M", [1, 5])
+@pytest.mark.parametrize("dtype,group", [("bf16", 0), ("f32", 0), ("bf16", 64), ("f32", 32)])
+def test_an_infinite_router_weight(dtype, group, M):
+    la = Layer(dtype, 96 if not group else 128, 64, 6, group=group, seed=33)
+    x, ids, w, lora = la.step(M, 3, sentinels=False)
+    w[0, 1] = INF
+    ref, bound = layer64(la, x, ids, w, lora)
+    assert np.isinf(ref[0]).all()
+    agrees(la.call(x, ids, w, lora).float().cpu().numpy(), ref, bound)
+
+
+def exact_h(M, E=4, H=64, I=32, S=0):
+    """A bf16 layer and tokens whose h is exact in bf16 at one place: gate 32 and up 2 there, from x = 1 at
+    its first element, so h = silu(32) * 2 = 64 and its second bf16 term is zero."""
+    la = Layer("bf16", H, I, E, S, 8 if S else 0, seed=34)
+    la.gu[:, 5], la.gu[:, I + 5] = 0, 0
+    la.gu[:, 5, 0], la.gu[:, I + 5, 0] = 32, 2
+    la.w.tensors[0].copy_(la.gu)
+    x, ids, w, lora = la.step(M, 2, sentinels=False)
+    x[:, 0] = 1
+    return la, x, ids, w, lora
+
+
+@pytest.mark.parametrize("M", [1])
+def test_an_infinite_down_weight(M):
+    la, x, ids, w, lora = exact_h(M)
+    la.dn[:, 7, 5], la.dn[:, 9, 5], la.dn[:, 60, 4] = INF, -INF, INF
+    la.w.tensors[1].copy_(la.dn)
+    ref, bound = layer64(la, x, ids, w, lora)
+    assert np.isinf(ref[:, [7, 9]]).all() and np.isfinite(ref).sum() == 61 * M
+    agrees(la.call(x, ids, w, lora).float().cpu().numpy(), ref, bound)

@@ -159,7 +159,7 @@ __device__ __forceinline__ PairsOf find_pairs(const LayerArgs& a, int slot, bool
   return found;
 }
 
-// h of the pairs: bf16 as two planes of I, or fp32.
+// h of the pairs.
 template <bool BF16>
 struct HSrc {
   const LayerArgs& a;
@@ -171,8 +171,7 @@ struct HSrc {
     return (const char*)a.h + (int64_t)pair[col] * a.I * 4;
   }
   __device__ __forceinline__ XVec operator()(const char* row, int v) const {
-    const uint4 hi = ld16(row + (uint32_t)v * 16u);
-    return {hi, BF16 ? ld16(row + (uint32_t)a.I * 2u + (uint32_t)v * 16u) : hi};
+    return PlaneSrc<BF16>{a.I}(row, v);
   }
 };
 

@@ -148,12 +148,36 @@ __global__ void __launch_bounds__(kThreads) down_direct_kernel(LayerArgs a) {
     if (col == pl * KK + quad * 4 / NR)
       *reinterpret_cast<f32x4_t*>(red + (wv * NP + pl) * kTileRows + quad * 4) = tot;
   __syncthreads();
-  if ((int)threadIdx.x < NR && n0 + (int)threadIdx.x < a.H) {
-    float y = 0.f;
+  if (wv != 0) return;
+  const bool live = lane < NR && n0 + lane < a.H;
+  float y = 0.f;
+  if (live) {
 #pragma unroll
-    for (int j = 0; j < kWaves * NP * KK; ++j) y += red[j * NR + threadIdx.x];
-    store_elem<BF16>(a.y, (int64_t)m * a.ld_y + n0 + threadIdx.x, y);
+    for (int j = 0; j < kWaves * NP * KK; ++j) y += red[j * NR + lane];
   }
+  // A column that is not finite once more, from its terms in their order: the parts above also give NaN
+  // where the definition does not (an infinite h over 4-bit weights, an infinite weight beside a second
+  // plane of zeros, an infinite router weight beside a wave's part of zero).
+  uint64_t odd = __builtin_amdgcn_ballot_w64(live && !__builtin_isfinite(y));
+  const Q4Tables q{a.sc_dn, a.z_dn, ng};
+  const PlaneSrc<BF16> src{a.I};
+#pragma unroll 1
+  for (; odd; odd &= odd - 1) {
+    const int j = __builtin_ctzll(odd);
+    float sum = 0.f;
+#pragma unroll 1
+    for (int k = 0; k < a.topk && sum == sum; ++k) {  // (a NaN stays)
+      const int e = expert_of(k);
+      if (e < 0) continue;
+      const __amdgpu_buffer_rsrc_t rsrc =
+          expert_rsrc((const char*)a.W_dn + (int64_t)e * a.H * rb, a.H * rb);
+      const RowAt at{(uint32_t)((n0 + j) * rb), (int64_t)e * a.H + n0 + j};
+      const char* h = (const char*)a.h + (int64_t)(p0 + k) * NP * a.I * ESZ;
+      sum = fmaf(a.weights[p0 + k], sum_of_terms<G, BF16, NP>(rsrc, at, q, src, h, a.I, lane), sum);
+    }
+    y = lane == j ? sum : y;
+  }
+  if (live) store_elem<BF16>(a.y, (int64_t)m * a.ld_y + n0 + lane, y);
 }
 
 template <int G, bool BF16, int NR>

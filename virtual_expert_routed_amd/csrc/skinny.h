@@ -736,6 +736,16 @@ struct RowSrc {
   }
 };
 
+// The activation h of the pairs, from a row's first byte: bf16 as two planes of I elements, or fp32.
+template <bool BF16>
+struct PlaneSrc {
+  int I;
+  __device__ __forceinline__ XVec operator()(const char* row, int v) const {
+    const uint4 hi = ld16(row + (uint32_t)v * 16u);
+    return {hi, BF16 ? ld16(row + (uint32_t)I * 2u + (uint32_t)v * 16u) : hi};
+  }
+};
+
 // silu(g) = g / (1 + exp(-g)), to about 2^-22: the hardware's exp2 of -g log2(e), corrected by what
 // the product with log2(e) rounds away, and its reciprocal.
 __device__ __forceinline__ float silu(float g) {

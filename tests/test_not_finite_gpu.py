@@ -173,3 +173,46 @@ def test_an_infinite_down_weight(M):
     ref, bound = layer64(la, x, ids, w, lora)
     assert np.isinf(ref[:, [7, 9]]).all() and np.isfinite(ref).sum() == 61 * M
     agrees(la.call(x, ids, w, lora).float().cpu().numpy(), ref, bound)
+
+
+# ---- an infinite weight where h or s is exact in bf16 (its second term is zero)
+
+
+@pytest.mark.parametrize("M", [3, 5, 40])
+def test_an_infinite_down_weight_of_more_tokens(M):
+    test_an_infinite_down_weight(M)
+
+
+def adapters64(la, i, t):
+    """Adapter tensor i of the layer becomes t (host)."""
+    la.ad.tensors[i].copy_(t)
+    la.ad64 = tuple(t.double().numpy() if j == i else v for j, v in enumerate(la.ad64))
+
+
+@pytest.mark.parametrize("M", [5, 40])
+@pytest.mark.parametrize("which", ["gate_up_B", "down_A", "down_B"])
+def test_an_infinite_adapter_weight(which, M):
+    """s of the adapters is exact too: A's first rows pick x[0] = 1, and h[5] = 64."""
+    la, x, ids, w, lora = exact_h(M, S=2)
+    x[:, 1:] = 0
+    lora[:] = torch.arange(M).int() % 3 - 1
+    host = [t.cpu() for t in la.ad.tensors[:4]]
+    A1, B1, A2, B2 = host
+    A1[:, :, 0] = 0.5
+    B1[:, (5, 32 + 5)] = 0                   # g and u of column 5 stay 32 and 2
+    A2[:] = 0
+    A2[:, :, 5] = 0.25                       # s = 16 exactly
+    if which == "gate_up_B":
+        B1[:, 11, 3] = INF                   # g = inf there: h = inf * u
+        A2[:, :, 11], B2[:] = 0.25, 0.5
+    elif which == "down_A":
+        A2[:, 2, 5] = INF                    # s = inf at rank 2
+    else:
+        B2[:, 7, 1], B2[:, 9, 1] = INF, -INF
+    for i, t in enumerate(host):
+        adapters64(la, i, t)
+    ref, bound = layer64(la, x, ids, w, lora)
+    with_adapter = lora.numpy() >= 0
+    assert not np.isfinite(ref[with_adapter]).all(axis=1).any() and np.isfinite(ref[~with_adapter]).all()
+    assert np.isinf(ref[with_adapter]).any()
+    agrees(la.call(x, ids, w, lora).float().cpu().numpy(), ref, bound)

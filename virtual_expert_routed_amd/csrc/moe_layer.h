@@ -278,6 +278,32 @@ __device__ __forceinline__ void rank_part(const LayerArgs& a, const RankPart& rp
             if constexpr (BF16) acc[t] = mma16<BF16>(bk, sv.lo, acc[t]);
           }
         }
+        // An infinite element of B gives NaN beside a second plane of zeros: sums that are not finite once
+        // more, term by term (where s holds a NaN they all are, and stay).
+        bool odd = false;
+        if constexpr (BF16) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) odd |= col < ncol && !__builtin_isfinite(acc[t][i]);
+        }
+        if (odd) {
+          bool nan = false;
+          for (int k = 0; k < rl; ++k) nan |= sc[g * a.r + k] != sc[g * a.r + k];
+          const uint16_t* B = (const uint16_t*)rp.B + (int64_t)v * rp.N * a.r;
+#pragma unroll 1
+          for (int j = 0; j < 4 * NT && !nan; ++j) {
+            const int n = (t0 + (j >> 2) * kWaves) * kTileRows + quad * 4 + (j & 3);
+            float sum = 0.f;
+            for (int k = 0; n < w && k < rl; ++k)
+              sum = fmaf(bf16_lo(B[(g * w + n) * a.r + k]), sc[g * a.r + k], sum);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                acc[t][i] = t * 4 + i == j && !__builtin_isfinite(acc[t][i]) ? sum : acc[t][i];
+          }
+        }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           const int n = (t0 + t * kWaves) * kTileRows + quad * 4;

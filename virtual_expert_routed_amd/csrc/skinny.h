@@ -611,10 +611,10 @@ __device__ __forceinline__ void stream_rows(char* lds, __amdgpu_buffer_rsrc_t rs
 #pragma unroll
   for (int t = 0; t < S::T; ++t) epilogue(t * 16 + col, acc[t]);
 
-  // Sums that are not finite once more, each from its terms, and out again over the first: an infinite x, or
-  // a sum past fp32's range on the way, then gives what the definition gives. Columns whose x holds a
-  // NaN are left: all their sums are NaN.
-  if constexpr (G > 0) {
+  // Sums that are not finite once more, each from its terms, and out again over the first: an infinite x, an
+  // infinite weight beside a second plane of zeros, or a sum past fp32's range on the way, then gives what
+  // the definition gives. Columns whose x holds a NaN are left: all their sums are NaN.
+  if constexpr (G > 0 || NP == 2) {
     bool odd = false;
 #pragma unroll
     for (int t = 0; t < S::T; ++t)

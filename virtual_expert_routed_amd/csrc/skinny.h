@@ -746,15 +746,19 @@ struct PlaneSrc {
   }
 };
 
-// silu(g) = g / (1 + exp(-g)), to about 2^-22: the hardware's exp2 of -g log2(e), corrected by what
-// the product with log2(e) rounds away, and its reciprocal.
+// silu(g) = g / (1 + exp(-g)), within 2^-20 of itself (2^-126 where it is below the normal numbers): the
+// hardware's exp2 of t = -g log2(e), corrected by what the product with log2(e) rounds away, and its
+// reciprocal. From t = 126 on the 1 is lost beside exp(-g), whose reciprocal leaves the normal numbers before
+// g exp(g) does: that is formed from 2^(64 - t), scaled at the end (0 from t = 256 on, NaN at -infinity).
 __device__ __forceinline__ float silu(float g) {
   constexpr float kL = 1.44269502f, kLlo = 1.92596303e-8f, kLn2 = 0.693147182f;
   const float t = -g * kL;
   const float lost = fmaf(-g, kLlo, fmaf(-g, kL, -t)) * kLn2;
-  const float e = __builtin_amdgcn_exp2f(t);
-  const float x = fabsf(t) < 126.f ? fmaf(e, lost, e) : e;  // (0 and infinity stay as they are)
-  return g * __builtin_amdgcn_rcpf(1.f + x);
+  const bool far = !(t < 126.f);
+  const float e = __builtin_amdgcn_exp2f(far ? 64.f - t : t);
+  const float c = fmaf(e, far ? -lost : lost, e);
+  const float x = t > -126.f && t < 256.f ? c : far ? 0.f : e;  // (0 and infinity stay as they are)
+  return far ? g * x * 0x1p-64f : g * __builtin_amdgcn_rcpf(1.f + x);
 }
 
 template <bool BF16>

@@ -458,6 +458,8 @@ def mol_moe_gemm_q4(xin, row_div: int, W, scales, sorted_ids, expert_ids, num_po
     E = W.shape[0]
     dtype = scales.dtype
     ld_x = _rows(xin, "xin", dev, dtype, (xin.shape[0], K))
+    if row_div < 1:
+        raise ValueError(f"row_div must be at least 1, got {row_div}")
     if xin.shape[0] * row_div < numel:
         raise ValueError(f"xin has {xin.shape[0]} rows: {numel} pairs need "
                          f"{-(-numel // row_div)}")

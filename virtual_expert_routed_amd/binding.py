@@ -377,6 +377,12 @@ def _on(dev, name: str, t: torch.Tensor, dtype, shape):
     raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _fit(fn: str, *values) -> None:
+    """Whole numbers that an int32 argument holds (ctypes would wrap others)."""
+    if max(values) > 0x7fffffff or min(values) < -0x80000000:
+        raise ValueError(f"{fn}: {max(values, key=abs)} does not fit 32 bits")
+
+
 _fns = {}  # entry points by name
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda i: torch.cuda.current_stream(i).cuda_stream)
@@ -406,6 +412,9 @@ def mol_router_topk(logits, topk: int, scoring: int = MOL_SCORE_SOFTMAX,
     if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
         raise ValueError("logits must be 2-d with contiguous rows")
     M, E = logits.shape
+    if num_local is None:
+        num_local = E
+    _fit("mol_router_topk", M, E, topk, scoring, first_expert, num_local)
     dev = logits.device
     if topk_ids is None:
         topk_ids = torch.empty((M, topk), dtype=torch.int32, device=dev)
@@ -417,7 +426,7 @@ def mol_router_topk(logits, topk: int, scoring: int = MOL_SCORE_SOFTMAX,
         _on(dev, "topk_weights", topk_weights, torch.float32, (M, topk))
     _call(dev, "mol_router_topk", _dtype_code(logits), logits.data_ptr(),
           logits.stride(0) if M > 1 else max(logits.stride(0), E), M, E, topk, scoring,
-          1 if renormalize else 0, scale, first_expert, E if num_local is None else num_local,
+          1 if renormalize else 0, scale, first_expert, num_local,
           topk_ids.data_ptr(), topk_weights.data_ptr())
     return topk_ids, topk_weights
 
@@ -440,6 +449,7 @@ def _q4(W, scales, zeros, name: str, dev):
     if W.dim() != 3 or scales.dim() != 3 or scales.shape[2] < 1:
         raise ValueError(f"{name} must be [E, N, K/2] with scales [E, N, K/group]")
     E, N, half = W.shape
+    _fit(name, E, N, 2 * half)
     _on(dev, name, W, torch.uint8, (E, N, half))
     _on(dev, name + " scales", scales, scales.dtype, (E, N, scales.shape[2]))
     if zeros is not None:
@@ -453,6 +463,7 @@ def mol_moe_gemm_q4(xin, row_div: int, W, scales, sorted_ids, expert_ids, num_po
                     numel: int, block_m: int, out, zeros=None):
     """The base grouped GEMM of a stage into out [numel, N] over 4-bit weights W uint8
     [E, N, K/2] with scales [E, N, K/group] (routing by base expert)."""
+    _fit("mol_moe_gemm_q4", row_div, numel, block_m)
     dev = W.device
     N, K, group = _q4(W, scales, zeros, "W", dev)
     E = W.shape[0]
@@ -558,6 +569,7 @@ class MoeAdapters:
 
 
 def mol_moe_layer_workspace_bytes(w: MoeWeights, M: int, topk: int, adapters=None) -> int:
+    _fit("mol_moe_layer_workspace_bytes", M, topk)
     v = lib().mol_moe_layer_workspace_bytes(w.c.dtype, M, topk, w.hidden, w.inter,
                                             0 if adapters is None else adapters.rank)
     if v < 0:
@@ -576,6 +588,7 @@ def mol_moe_layer(w: MoeWeights, x, topk_ids, topk_weights, adapters=None, lora_
     """A whole layer for a few tokens: y [M, hidden] from x [M, hidden] and its routing."""
     dev = w.device
     M, topk = topk_ids.shape
+    _fit("mol_moe_layer", M, topk)
     ld_x = _rows(x, "x", dev, w.dtype, (M, w.hidden))
     _on(dev, "topk_ids", topk_ids, torch.int32, (M, topk))
     _on(dev, "topk_weights", topk_weights, torch.float32, (M, topk))

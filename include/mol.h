@@ -363,7 +363,8 @@ MOL_API mol_status mol_lora_expand_combine(int32_t dtype, const float *s, int32_
  *   topk_ids      int32 [M, topk] out;  topk_weights  float32 [M, topk] out
  * Scores and sums are fp32. logits is aligned to its element, at any row stride >= num_experts.
  * Errors: MOL_E_ARG, MOL_E_DTYPE, MOL_E_ALIGN, MOL_E_LIMIT (num_experts + 1 > MOL_MAX_BUCKETS,
- * topk > MOL_MAX_ROUTER_TOPK, M * topk past 32 bits). M = 0 is a no-op.
+ * topk > MOL_MAX_ROUTER_TOPK, M * topk past 32 bits, 2^28 tokens or more, 2^26 with over 256
+ * experts or 16 slots). M = 0 is a no-op.
  * ------------------------------------------------------------------------------- */
 enum { MOL_SCORE_SOFTMAX = 0, MOL_SCORE_SIGMOID = 1 };
 #define MOL_MAX_ROUTER_TOPK 64
@@ -395,7 +396,8 @@ MOL_API mol_status mol_router_topk(int32_t dtype, const void *logits, int64_t ld
  *   others        as for mol_moe_gemm (rows of xin on 16-byte boundaries)
  * Built for decode-sized batches; blocks of any block_m are taken.
  * Errors: MOL_E_ARG (a group that is not 32, 64 or 128, K not a multiple of it), MOL_E_LIMIT
- * (more than 256 groups a row, one expert's weights 2 GiB or more), others as for mol_moe_gemm.
+ * (more than 256 groups a row, one expert's weights 2 GiB or more, 2^24 work items or more), others
+ * as for mol_moe_gemm.
  * ------------------------------------------------------------------------------- */
 MOL_API mol_status mol_moe_gemm_q4(int32_t dtype, const void *xin, int64_t ld_x, int32_t row_div,
                                    const uint8_t *W, const void *scales, const uint8_t *zeros,
@@ -437,7 +439,8 @@ MOL_API mol_status mol_moe_gemm_q4(int32_t dtype, const void *xin, int64_t ld_x,
  * bf16, 4 fp32), with 4-bit weights hidden and inter multiples of group.
  * Errors: MOL_E_ARG, MOL_E_DTYPE, MOL_E_ALIGN, MOL_E_WORKSPACE, MOL_E_LIMIT (M * topk >
  * MOL_LAYER_MAX_PAIRS, topk > MOL_LAYER_MAX_TOPK, E * S + 1 > MOL_MAX_BUCKETS, rank over
- * MOL_MAX_RANK_BYTES, one expert's matrix 2 GiB or more). M = 0 is a no-op.
+ * MOL_MAX_RANK_BYTES, one expert's matrix 2 GiB or more, 2^24 work items or more in a launch). M = 0
+ * is a no-op.
  * For more tokens: mol_align_block_size, mol_moe_gemm or mol_moe_gemm_q4, mol_lora_delta and
  * mol_moe_combine.
  * ------------------------------------------------------------------------------- */

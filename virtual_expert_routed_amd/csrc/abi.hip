@@ -13,6 +13,8 @@
 namespace {
 
 constexpr int64_t kI32Max = std::numeric_limits<int32_t>::max();
+// workgroups of 256 threads in one launch: HIP takes fewer than 2^32 threads
+constexpr int64_t kGridMax = (int64_t(1) << 24) - 1;
 
 int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round256(int64_t a) { return (a + 255) / 256 * 256; }
@@ -714,7 +716,8 @@ MOL_API mol_status mol_router_topk(int32_t dtype, const void* logits, int64_t ld
       (int64_t)first_expert + num_local > num_experts)
     return MOL_E_ARG;
   if ((int64_t)num_experts + 1 > MOL_MAX_BUCKETS || topk > MOL_MAX_ROUTER_TOPK ||
-      (int64_t)M * topk > kI32Max)
+      (int64_t)M * topk > kI32Max ||
+      cdiv64(M, mol::router_rows(num_experts, topk)) > kGridMax)
     return MOL_E_LIMIT;
   if (M == 0) return MOL_OK;
   if (!logits || !topk_ids || !topk_weights) return MOL_E_ARG;
@@ -784,7 +787,7 @@ MOL_API mol_status mol_moe_gemm_q4(int32_t dtype, const void* xin, int64_t ld_x,
   a.split_k = it.split;
   a.tiles = it.tiles;
   a.items = (int32_t)it.items;
-  if (rc.max_blocks * a.items > kI32Max) return MOL_E_LIMIT;
+  if (rc.max_blocks * a.items > kGridMax) return MOL_E_LIMIT;
   a.out = out;
   a.ld_out = ld_out;
   a.f_rd = mol::make_fastdiv((uint32_t)row_div);
@@ -906,9 +909,10 @@ MOL_API mol_status mol_moe_layer(const mol_moe_weights* w, const mol_moe_adapter
   const mol::StreamItems gu =
       mol::stream_items(a.slots, a.numel, 2 * (int64_t)I, row_bytes(H));
   const mol::StreamItems dn = mol::stream_items(a.slots, a.numel, H, row_bytes(I));
-  // every grid of the call: matrices x row groups, and direct down's columns x tokens
-  if (a.slots * gu.items + a.rank_slots > kI32Max || a.slots * dn.items + a.rank_slots > kI32Max ||
-      ((int64_t)H + 128) * M > kI32Max)
+  // every grid of the call: matrices x row groups, and direct down's columns (four or more an item,
+  // rounded up to whole rounds of the XCDs) x tokens
+  if (a.slots * gu.items + a.rank_slots > kGridMax || a.slots * dn.items + a.rank_slots > kGridMax ||
+      (a.direct && ((int64_t)H / 4 + 8) * M > kGridMax))
     return MOL_E_LIMIT;
   a.gu_split = gu.split;
   a.gu_tiles = gu.tiles;

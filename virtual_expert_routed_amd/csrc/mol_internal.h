@@ -199,6 +199,10 @@ struct RouterArgs {
   float* weights;          // [M, topk]
 };
 
+// Rows of a workgroup of the router: 16 lanes each up to 256 experts and 16 slots, else a wave each.
+inline bool router_narrow(int32_t E, int32_t topk) { return topk <= 16 && E <= 256; }
+inline int router_rows(int32_t E, int32_t topk) { return router_narrow(E, topk) ? 16 : 4; }
+
 // The work items of a stream of weight rows: 64 rows times `tiles`, or 16 rows whose k's four waves
 // split. All read the same bytes.
 //  - 16 rows where 64 would make fewer than 384 items for the chip's 256 CUs. 4-bit rows of K 2048,

@@ -170,7 +170,7 @@ hipError_t launch(const RouterArgs& a, hipStream_t st) {
 // lanes against a wave a row: 128 experts, top-8 9.8 and 21.7 us; 256, top-16 18.0 and 35.7.
 template <bool BF16>
 hipError_t dispatch(const RouterArgs& a, hipStream_t st) {
-  if (a.topk <= 16 && a.E <= 256) {
+  if (router_narrow(a.E, a.topk)) {
     if (a.E <= 64) return launch<BF16, 16, 4>(a, st);
     if (a.E <= 128) return launch<BF16, 16, 8>(a, st);
     return launch<BF16, 16, 16>(a, st);

@@ -363,8 +363,8 @@ MOL_API mol_status mol_lora_expand_combine(int32_t dtype, const float *s, int32_
  *   topk_ids      int32 [M, topk] out;  topk_weights  float32 [M, topk] out
  * Scores and sums are fp32. logits is aligned to its element, at any row stride >= num_experts.
  * Errors: MOL_E_ARG, MOL_E_DTYPE, MOL_E_ALIGN, MOL_E_LIMIT (num_experts + 1 > MOL_MAX_BUCKETS,
- * topk > MOL_MAX_ROUTER_TOPK, M * topk past 32 bits, 2^28 tokens or more, 2^26 with over 256
- * experts or 16 slots). M = 0 is a no-op.
+ * topk > MOL_MAX_ROUTER_TOPK, M * topk past 32 bits, more than 2^28 - 16 tokens, or 2^26 - 4 with over
+ * 256 experts or 16 slots). M = 0 is a no-op.
  * ------------------------------------------------------------------------------- */
 enum { MOL_SCORE_SOFTMAX = 0, MOL_SCORE_SIGMOID = 1 };
 #define MOL_MAX_ROUTER_TOPK 64
@@ -411,15 +411,18 @@ MOL_API mol_status mol_moe_gemm_q4(int32_t dtype, const void *xin, int64_t ld_x,
  * no aligned routing: two launches for a token, or up to three of them, without adapters (gate/up
  * with the activation, down with the combine); three beyond (the combine on its own); four with
  * adapters (the activation too; their products run beside the base ones). For pair
- * p = m * topk + k with a local base expert t = topk_ids[m, k] in [0, E), and l = lora_ids[m] (the adapter terms only for l in [0, S) and slot rank rl > 0, v = t + l * E):
+ * p = m * topk + k with a local base expert t = topk_ids[m, k] in [0, E), and l = lora_ids[m] (the
+ * adapter terms only for l in [0, S) and slot rank rl > 0, v = t + l * E):
  *   g    = gate_up[t, 0:I] x_m + slot_scale[l] * gate_up_B[v, 0:I, :rl] (gate_up_A[v, 0:rl] x_m)
  *   u    = gate_up[t, I:2I] x_m + slot_scale[l] * gate_up_B[v, I:2I, :rl] (gate_up_A[v, r:r+rl] x_m)
  *   h_p  = g / (1 + exp(-g)) * u
  *   y_m  = round( sum_k topk_weights[m, k] * (down[t] h_p
  *                  + slot_scale[l] * down_B[v, :, :rl] (down_A[v, 0:rl] h_p)) )
  * Pairs without a local expert contribute nothing; a token that has none gets a row of
- * zeros. Sums, g, u and h are fp32; bf16 products take h as two bf16 terms (16 of its bits), and
- * y alone is rounded to bf16 (to nearest even).
+ * zeros. Sums, g, u and h are fp32 (SiLU within 2^-20 of itself); bf16 products take h, and
+ * the adapters' products A x and A h where B multiplies them, as two bf16 terms each (at least 16 of
+ * their bits); y alone is rounded to bf16 (to nearest even). Sums over 4-bit weights and over two terms
+ * that are not finite are formed again from their terms: infinities and NaN are the formula's.
  *   w             (host) the weights; read during the call only. dtype: MOL_F32 or MOL_BF16 of x,
  *                 y, the scales, the adapters, and of the weights themselves when group is 0.
  *                 gate_up [E, 2 * inter, hidden] (gate rows first), down [E, hidden, inter],

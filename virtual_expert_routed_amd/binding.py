@@ -486,8 +486,8 @@ def mol_moe_gemm_q4(xin, row_div: int, W, scales, sorted_ids, expert_ids, num_po
             raise ValueError(f"{name} has {t.numel()} entries, fewer than the routing's {least}")
     _call(dev, "mol_moe_gemm_q4", _dtype_code(scales), xin.data_ptr(), ld_x, row_div,
           W.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(), group, K,
-          N, E, sorted_ids.data_ptr(), expert_ids.data_ptr(), num_post_padded.data_ptr(), numel, block_m, out.data_ptr(),
-          ld_out)
+          N, E, sorted_ids.data_ptr(), expert_ids.data_ptr(), num_post_padded.data_ptr(), numel,
+          block_m, out.data_ptr(), ld_out)
     return out
 
 

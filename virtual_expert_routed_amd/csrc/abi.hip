@@ -148,9 +148,12 @@ static_assert(MOL_LAYER_MAX_PAIRS == mol::kLayerMaxPairs && MOL_LAYER_MAX_TOPK =
 
 // Whether the layer's down stage runs per token, with the combine: for one token, and for up to three
 // where an item of four columns over the token's experts holds at least 32 KiB of weights. Measured
-// against the grouped form and a combine (128 experts, top-8, hidden 2048, inter 768, whole layer): 42
-// against 48 us at two tokens, 53 against 62 at three, 67 against 65 at four. With 16 KiB an item
-// (hidden 6144, inter 256) its many small items lose: 56 against 41 us at two tokens.
+// against the grouped form and a combine as queued calls of the whole layer (128 experts, top-8, hidden
+// 2048, inter 768; us): one token bf16 20.9 against 24.8, fp32 37.9 and 38.4, 4-bit in groups of 128
+// 16.5 and 19.6, 64 20.0 and 23.8, 32 27.2 and 30.8; two tokens bf16 38.3 and 40.4; three 55.0 and 54.2;
+// four 60.6 and 58.5. 4-bit rows stay below 32 KiB an item there: at two tokens 25.2, 27.0 and 39.7 per
+// token, 25.4, 26.3 and 32.0 grouped. With 16 KiB an item in bf16 (160 experts, hidden 6144, inter 256)
+// its many small items lose: 54.2 against 38.0 at two tokens, and at one, 32.4 against 25.2.
 bool layer_direct(int32_t M, int32_t r, int32_t topk, int64_t row_bytes) {
   return r == 0 && (M == 1 || (M <= 3 && (int64_t)topk * 4 * row_bytes >= 32768));
 }

@@ -13,21 +13,21 @@
 // Gate/up and down stream weight rows (skinny.h): a work item is 64 rows of one expert or more, for
 // all the pairs that use it (16 rows and split k's where 64 make too few items). Up to E pairs the
 // items are per pair, and a pair whose expert an earlier pair has exits; beyond, per expert (128
-// experts, top-8, calls per pair and per expert: 1 token 23.5 and 40.2 us, 8 tokens 103 and 112, 16
-// tokens 156 and 160). The adapters run beside the base product, in the same launch: an item per
-// virtual expert forms s = A x for its pairs, keeps it in LDS and writes c B s as fp32 rows, which the
-// activation (then a launch of its own) and the combine add to the base rows. Their latency (a
-// dependent chain over a few hundred KiB) hides behind the base product's stream, so these items come
-// first in the grid; as launches of their own before each stage they took 13 and 6 us more at 23 tokens, 59
-// and 23 at 128.
+// experts, top-8, queued calls per pair and per expert: 1 token 21.1 and 31.9 us, 4 tokens 60 and 76, 8
+// tokens 100 and 107, 16 tokens 150 and 152). The adapters run beside the base product, in the same
+// launch: an item per virtual expert forms s = A x for its pairs, keeps it in LDS and writes c B s as
+// fp32 rows, which the activation (then a launch of its own) and the combine add to the base rows. Their
+// latency (a dependent chain over a few hundred KiB) hides behind the base product's stream, so these
+// items come first in the grid; as launches of their own before each stage they took 13 and 6 us more at 23
+// tokens, 59 and 23 at 128.
 //
 // Bound by the stream of weights out of HBM. bf16, 128 experts, hidden 2048, inter 768, top-8:
-//   1 token, no adapters      gate/up 13.0 us (50 MB, 3.9 TB/s), direct down 7.8
-//   23 tokens, rank 32 of 8   gate/up 122 us (660 MB, 5.4 TB/s), down 64 (340 MB, 5.3), act 4.9,
+//   1 token, no adapters      gate/up 13.3 us (50 MB, 3.8 TB/s), direct down 7.9
+//   23 tokens, rank 32 of 8   gate/up 122 us (660 MB, 5.4 TB/s), down 65 (340 MB, 5.2), act 4.8,
 //                             combine 4.8
-//   128 tokens, rank 32 of 16 gate/up 190 us, down 107, act 6.3, combine 5.6
-// 4-bit base weights, 23 tokens: gate/up 56 us, down 35 (240 + 90 MB with the adapters: bound like
-// the 4-bit product, by the latency of items and the unpacking).
+//   128 tokens, rank 32 of 16 gate/up 192 us, down 109, act 6.5, combine 5.5
+// 4-bit base weights, 23 tokens: gate/up 55 us, down 35 (230 + 90 MB with the adapters: bound like
+// the 4-bit product, by the latency of items and the unpacking; groups of 32 spill registers there too).
 #pragma once
 
 #include <algorithm>
@@ -244,9 +244,11 @@ __device__ __forceinline__ void rank_part(const LayerArgs& a, const RankPart& rp
         }
       };
       if (ncol <= 4)
-        stream_k<0, BF16, 4, NP, 1>(lds, ra, row_at(col), row_at, Q4Tables{}, src, ncol, rp.K, r0 > 0, keep);
+        stream_k<0, BF16, 4, NP, 1>(lds, ra, row_at(col), row_at, Q4Tables{}, src, ncol, rp.K, r0 > 0,
+                                    keep);
       else
-        stream_k<0, BF16, 16, NP, 1>(lds, ra, row_at(col), row_at, Q4Tables{}, src, ncol, rp.K, r0 > 0, keep);
+        stream_k<0, BF16, 16, NP, 1>(lds, ra, row_at(col), row_at, Q4Tables{}, src, ncol, rp.K,
+                                     r0 > 0, keep);
     }
     __syncthreads();
     // B s: the operand rows of B are 16 bytes of rank a lane and step, s in two planes (bf16)

@@ -8,7 +8,7 @@
 // neighbours on one XCD, so most of that comes from its L2. Per token rather than per expert: for one
 // token that saves a launch and a pass over the pairs' rows.
 //
-// Bound by the latency of its one round of loads: 7.8 us for one token (top-8, hidden 2048, inter 768
+// Bound by the latency of its one round of loads: 7.9 us for one token (top-8, hidden 2048, inter 768
 // in bf16: 25 MB, 3.2 TB/s). Twelve loads of weights and twelve of h in flight a lane are all of a
 // wave's share there.
 #include "skinny.h"
@@ -189,8 +189,8 @@ hipError_t launch(const LayerArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-// As many experts in a tile as the token has, up to four (calls of one token: top-1 13.2 us, against
-// 13.9 with room for four; top-2 14.6 and 15.9).
+// As many experts in a tile as the token has, up to four (calls of one token when that was chosen: top-1
+// 13.2 us, against 13.9 with room for four; top-2 14.6 and 15.9).
 template <int G, bool BF16>
 hipError_t by_topk(const LayerArgs& a, hipStream_t st) {
   if (a.topk == 1) return launch<G, BF16, 16>(a, st);

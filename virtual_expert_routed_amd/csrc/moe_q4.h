@@ -10,10 +10,11 @@
 //
 // What bounds it: an item's own latency (routing reads, then x and the first weights, then LDS), of
 // which four workgroups a CU (groups of 128; three otherwise) hide a part, and the unpacking of q.
-// 128 experts, top-8, N 1536, K 2048, groups of 128: 1 token 8.7 us (13 MB, 1.5 TB/s), 23 tokens 41
-// (161 MB, 3.9), 128 tokens of popular experts 62. Groups of 64
-// and 32 at 23 tokens: 49 and 77 us (their dwords move between the quads, and two or four
-// scales a load).
+// 128 experts, top-8, N 1536, K 2048, groups of 128, queued calls: 1 token 9.7 us (13 MB, 1.3 TB/s; the
+// kernel 8.8), 23 tokens 38 (161 MB, 4.2), 128 tokens of popular experts 57 (196 MB, 3.4). Groups of 64
+// and 32 at 23 tokens: 44 and 70 us. Their dwords move between the quads, with two or four scales a
+// load, and the kernels for groups of 32 run out of registers: all but the fp32 one over items of 64
+// rows keep 13 to 69 vector registers in scratch.
 #pragma once
 
 #include "skinny.h"

@@ -205,15 +205,19 @@ inline int router_rows(int32_t E, int32_t topk) { return router_narrow(E, topk) 
 
 // The work items of a stream of weight rows: 64 rows times `tiles`, or 16 rows whose k's four waves
 // split. All read the same bytes.
-//  - 16 rows where 64 would make fewer than 384 items for the chip's 256 CUs. 4-bit rows of K 2048,
-//    items of 64 against split ones: 16 items 33.5 and 17.3 us (fp32), 192 items 9.8 and 8.7; as whole
-//    calls 384 items 14.3 and 15.5, 768 items 16.4 and 23.0.
+//  - 16 rows where 64 would make fewer than 384 items for the chip's 256 CUs. Queued calls over 4-bit
+//    rows of K 2048 in groups of 128, items of 64 against split ones: 192 items (one token) 10.7 and
+//    11.1 us, 384 items 11.8 and 13.9, 768 items 15.1 and 21.4; one fp32 matrix of 16 items, 7 columns
+//    30.8 and 15.0; one bf16 matrix of 64 items, 8 columns 16.9 and 10.7. The rule looks at items
+//    alone, and a split item takes 8 columns a pass: with more columns it loses (that matrix at 64
+//    columns 59.0 and 63.5; dense layers of 8 experts, top-2, 16 tokens 25.0 and 28.9, 64 tokens 31.7
+//    and 49.5).
 //  - Several tiles where 64 rows hold few bytes, so that finding the pairs and staging x (microseconds
 //    of latency for each item) is paid once for up to 96 KiB of weights (4-bit down of 23 tokens,
-//    K 768: 26 against 33 us with one tile; K 2048, whose tile is 64 KiB: two take 44, one 41 us);
-//    only while matrices have few columns (`pairs` at most four a matrix on average): items over many
-//    columns are long, and fewer of them leave CUs idle (128 tokens, popular experts: 62 with one
-//    tile, 82 us with two).
+//    K 768: 29.9 against 32.5 us with one tile; K 2048, whose tile is 64 KiB, two tiles 44, one 41 us
+//    when that was chosen); only while matrices have few columns (`pairs` at most four a matrix on
+//    average): items over many columns are long, and fewer of them leave CUs idle (128 tokens, popular
+//    experts, when that was chosen: 62 with one tile, 82 us with two).
 struct StreamItems {
   bool split;
   int32_t tiles;
@@ -259,7 +263,7 @@ struct Q4GemmArgs {
 // A whole layer for a few tokens.
 constexpr int kLayerMaxPairs = 4096;
 constexpr int kLayerMaxTopk = 64;
-constexpr int kMaxQ4Groups = 256;  // groups of one row
+constexpr int kMaxQ4Groups = 256;  // groups of one row: the longest rows that are tested
 
 // The adapters of one of its stages: d = c B (A x) per pair.
 struct RankPart {

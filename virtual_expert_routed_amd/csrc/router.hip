@@ -15,9 +15,11 @@
 // experts: ties fall to the lowest), and a rescan of that lane's VPL registers. Slot j ends in
 // lane j of the row, so topk <= LPR.
 //
-// Bound by latency: 3.5 us for one token (128 experts, top-8), the launch and a chain of topk
-// selections of about 0.15 us; 7.6 us for 16384 tokens (5.2 MB, 0.7 TB/s). Per call a binding's 7 us
-// stand in front of either.
+// A kernel's time (rocprofv3): 3.6 us for one token of 128 experts, top-8: the launch and a chain of topk
+// selections of about 0.15 us. 6.5 us for 138 tokens of 160 experts (16 registers a lane, sigmoid). 7.6 us
+// for 16384 tokens of 128 (5.2 MB, 0.7 TB/s), bound by issue: all of its 1024 workgroups are resident, and
+// on each selection almost every wave runs the rescan of VPL registers for one lane of 16. Calls queued one
+// after another take 6.6 to 7.1 us at each of these sizes: the host's time for a call.
 #include "delta_common.h"
 
 namespace mol {
@@ -166,8 +168,8 @@ hipError_t launch(const RouterArgs& a, hipStream_t st) {
 }
 
 // Rows of up to 256 experts and 16 slots take 16 lanes (four rows a wave, all moves inside a
-// lane row); others a wave each, whose lanes hold up to 128 experts. Calls of 16384 tokens, 16
-// lanes against a wave a row: 128 experts, top-8 9.8 and 21.7 us; 256, top-16 18.0 and 35.7.
+// lane row); others a wave each, whose lanes hold up to 128 experts. Queued calls of 16384 tokens, 16
+// lanes against a wave a row: 128 experts, top-8 7.6 and 19.4 us; 256, top-16 15.5 and 32.2.
 template <bool BF16>
 hipError_t dispatch(const RouterArgs& a, hipStream_t st) {
   if (router_narrow(a.E, a.topk)) {

@@ -101,7 +101,7 @@ __device__ __forceinline__ uint4 q4_order(const uint4& x) {
 
 // ---- x in LDS ----
 
-// One 16-byte vector of x: its planes, and the fp32 sum of its elements (4-bit weights).
+// One 16-byte vector of x: its planes.
 struct XVec {
   uint4 hi, lo;
 };
@@ -440,10 +440,12 @@ struct ScaleRegs {
 // epilogue(col, acc) gets, on every lane (of wave 0 for KS = kWaves), column col's sums of tile
 // rows 4 * quad + i; only columns below ncol and rows that exist are meant. All four waves take
 // part in the barriers; on return LDS may still be read by slower waves.
-template <int G, bool BF16, int CW, int NP, int KS, bool MULTI, int UM, class Rows, class Src, class Epi>
+template <int G, bool BF16, int CW, int NP, int KS, bool MULTI, int UM, class Rows, class Src,
+          class Epi>
 __device__ __forceinline__ void stream_rows(char* lds, __amdgpu_buffer_rsrc_t rsrc,
                                             const RowAt& me, const Rows& row_at,
-                                            const Q4Tables& q, const Src& src, int ncol, int K, bool staged, Epi epilogue) {
+                                            const Q4Tables& q, const Src& src, int ncol, int K,
+                                            bool staged, Epi epilogue) {
   using S = Stream<G, BF16, CW, NP, KS, MULTI, UM>;
   // (opaque to the compiler, which would otherwise compute every variant's addresses ahead of the
   // loop over passes and spill them)
@@ -613,7 +615,9 @@ __device__ __forceinline__ void stream_rows(char* lds, __amdgpu_buffer_rsrc_t rs
 
   // Sums that are not finite once more, each from its terms, and out again over the first: an infinite x, an
   // infinite weight beside a second plane of zeros, or a sum past fp32's range on the way, then gives what
-  // the definition gives. Columns whose x holds a NaN are left: all their sums are NaN.
+  // the definition gives. Columns whose x holds a NaN are left: all their sums are NaN. Where
+  // all is finite the look does not show (4-bit gate/up of 128 tokens 57 us with and without; groups of 32
+  // lose up to 3 % to registers in scratch); half of the rows with a NaN 92 us, with an infinity 557.
   if constexpr (G > 0 || NP == 2) {
     bool odd = false;
 #pragma unroll
@@ -660,8 +664,9 @@ constexpr int kPassCols = KS > 1 ? 8 : (G && !BF16) || NP == 2 ? 32 : kMaxCols;
 
 // The stream of a row of K: staged at once where its x fits both buffers, else in several stages.
 // Loads of W in flight: as many as the registers allow (4-bit: each load's products take many of
-// them; fewer beside the next stage's x), and six where the row has no more (rows of 768, groups of
-// 64 or 128, with the items of several tiles: 38 us in rounds of four, 32.5 in one of six).
+// them; fewer beside the next stage's x), and six where the row has five or six (4-bit down of 23
+// tokens in rounds of four and in one of six: K 768, groups of 64 36.5 and 30.1 us, of 128 28.0 and 22.7;
+// K 640, groups of 128 25.1 and 20.3).
 template <int G, bool BF16, int CW, int NP, int KS, class Rows, class Src, class Epi>
 __device__ __forceinline__ void stream_k(char* lds, __amdgpu_buffer_rsrc_t rsrc, const RowAt& me,
                                          const Rows& row_at, const Q4Tables& q, const Src& src,
@@ -686,11 +691,12 @@ __device__ __forceinline__ void stream_k(char* lds, __amdgpu_buffer_rsrc_t rsrc,
 
 // As many columns as the pass has: 4, 8, 16, 32 or 64. A narrow pass leaves room in LDS for longer rows
 // of x in one stage; passes of 64 read a weight once where 16 would read it four times (layer of 128
-// tokens, popular experts: 308 us, and 325 before passes of 64 and the second buffer of x).
+// tokens, popular experts: 308 us with passes of 64 and the second buffer of x, 325 without either).
 template <int G, bool BF16, int NP, int KS, class Rows, class Src, class Epi>
 __device__ __forceinline__ void stream_cols(char* lds, __amdgpu_buffer_rsrc_t rsrc,
                                             const RowAt& me, const Rows& row_at,
-                                            const Q4Tables& q, const Src& src, int ncol, int K, bool staged, Epi epi) {
+                                            const Q4Tables& q, const Src& src, int ncol, int K,
+                                            bool staged, Epi epi) {
   constexpr int MOST = kPassCols<G, BF16, NP, KS>;
   if (ncol <= 4) {
     stream_k<G, BF16, 4, NP, KS>(lds, rsrc, me, row_at, q, src, ncol, K, staged, epi);

@@ -76,7 +76,7 @@ MOL_API const char *mol_status_string(mol_status status);
 /* (host) ABI version of this header, 7 (2 added the per-slot ranks, 3 the combine, 4 the
  * base grouped GEMM with the fused delta, 5 the allocation-free stage delta, 6 the work
  * plan, 7 the plan as runs of blocks only, read by the expand). Entry points that leave the
- * earlier ones as they are (mol_router_topk, mol_moe_gemm_q4, mol_moe_layer) come within a version. */
+ * earlier ones as they are (mol_router_topk and those after it) come within a version. */
 MOL_API int32_t mol_abi_version(void);
 
 /* ---------------------------------------------------------------------------------
@@ -376,6 +376,55 @@ MOL_API mol_status mol_router_topk(int32_t dtype, const void *logits, int64_t ld
                                    float *topk_weights, void *stream);
 
 /* ---------------------------------------------------------------------------------
+ * The balance loss of a routed batch (the auxiliary loss that keeps a router's experts evenly
+ * used), the experts' counts, and the gradient in the logits. A token counts if its mask is not zero
+ * and its row has a candidate (a logit that is neither NaN nor -infinity, as above). Over the n tokens
+ * that count, with c_e the number of their ids that are e and p_me their scores over the row's candidates
+ * (MOL_SCORE_SOFTMAX: softmax; MOL_SCORE_SIGMOID: sigmoids divided by their sum):
+ *   P_e  = sum_m p_me
+ *   loss = alpha * E / (topk * n^2) * sum_e c_e P_e            (alpha for an even batch; 0 if n = 0)
+ *   d loss / d l_mj = p_mj q_mj (a_j - sum_e p_me a_e),  a_e = alpha * E * c_e / (topk * n^2),
+ *                     q = 1 (softmax) or 1 - sigmoid(l_mj); 0 for masked logits and tokens that
+ *                     do not count
+ * Counts are constants to the gradient, as ids are.
+ *
+ * mol_router_balance -
+ *   logits        [M, ld_logits] (dtype), aligned to its element;  topk_ids  int32 [M, topk], the ids
+ *                 chosen for the tokens over all experts (ids outside [0, E) are not counted: -1
+ *                 for slots past the last candidate)
+ *   token_mask    uint8 [M]: 0 for tokens that do not count (padding), or NULL
+ *   alpha         finite factor of the loss
+ *   counts        int32 [num_experts + 1] out: c_e, then n
+ *   prob_sums     float32 [num_experts] out: P_e;   loss  float32 [1] out
+ *   workspace     device scratch of mol_router_balance_workspace_bytes(), 16-byte aligned (NULL when
+ *                 that is 0); needs no initial contents. Calls that may overlap must not share it.
+ * Results do not depend on timing: bit-for-bit reproducible. M = 0 writes zeros. Sums are fp32 in parts
+ * of at most M / 512 + 1 tokens, joined in 64 bits.
+ *
+ * mol_router_balance_grad - grad_logits [M, ld_grad] (dtype) out, every element of [M, num_experts]:
+ *   counts        int32 [num_experts + 1] of mol_router_balance, or their sums over the ranks that
+ *                 share the batch (the loss is then that of the whole batch: its P_e are sums too)
+ *   grad_loss     float32 [1], the gradient that arrives at the loss, or NULL for 1
+ *   others        as above. M = 0 enqueues nothing.
+ * Errors of both: MOL_E_ARG, MOL_E_DTYPE, MOL_E_ALIGN, MOL_E_WORKSPACE, MOL_E_LIMIT (num_experts + 1 >
+ * MOL_MAX_BUCKETS, topk > MOL_MAX_ROUTER_TOPK, M * topk past 32 bits).
+ * ------------------------------------------------------------------------------- */
+/* bytes of a workspace for up to M tokens, or -mol_status */
+MOL_API int64_t mol_router_balance_workspace_bytes(int32_t M, int32_t num_experts);
+MOL_API mol_status mol_router_balance(int32_t dtype, const void *logits, int64_t ld_logits,
+                                      const int32_t *topk_ids, const uint8_t *token_mask,
+                                      int32_t M, int32_t num_experts, int32_t topk,
+                                      int32_t scoring, float alpha, int32_t *counts,
+                                      float *prob_sums, float *loss, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+MOL_API mol_status mol_router_balance_grad(int32_t dtype, const void *logits, int64_t ld_logits,
+                                           const uint8_t *token_mask, const int32_t *counts,
+                                           const float *grad_loss, int32_t M,
+                                           int32_t num_experts, int32_t topk, int32_t scoring,
+                                           float alpha, void *grad_logits, int64_t ld_grad,
+                                           void *stream);
+
+/* ---------------------------------------------------------------------------------
  * 4-bit weights. A matrix of N rows of K weights is stored as uint8 [N, K / 2], two per byte:
  * byte b of a row holds k = 2b in its low half and k = 2b + 1 in its high half, each an
  * unsigned q in 0..15. Every group of G (32, 64 or 128) consecutive k's of a row has a scale and
@@ -405,6 +454,57 @@ MOL_API mol_status mol_moe_gemm_q4(int32_t dtype, const void *xin, int64_t ld_x,
                                    const int32_t *sorted_ids, const int32_t *expert_ids,
                                    const int32_t *num_post_padded, int32_t numel,
                                    int32_t block_m, void *out, int64_t ld_out, void *stream);
+
+/* ---------------------------------------------------------------------------------
+ * Microscaled 4-bit floats (MX4). A row of K values is stored as uint8 [K / 2], two per byte: byte
+ * b holds k = 2b in its low half and k = 2b + 1 in its high half, each a code of a sign bit (the
+ * highest) and one of the eight magnitudes 0, 1/2, 1, 3/2, 2, 3, 4, 6 in this order. Every 32 consecutive
+ * values share a scale byte s of uint8 [K / 32], which stands for 2^(s - 127); s = 255 makes the 32
+ * NaN. K is a multiple of 32. (The element and scale formats of the OCP Microscaling specification, MXFP4.)
+ *
+ * mol_mx4_quantize - rows to codes and scales. With m the largest magnitude of a block:
+ *   s = max(floor(log2 m) - 2, -127) + 127;  each value over 2^(s - 127) to the nearest magnitude, halves to
+ *   the even code, beyond 6 to 6. A block with a NaN or an infinity gets s = 255 and codes of zero.
+ *   activation    MOL_ACT_NONE: x [rows, K], the values;  MOL_ACT_SILU_MUL: x [rows, 2 K], gate
+ *                 columns first, value k = SiLU(x[k]) * x[K + k] (the rows of a layer's gate_up product,
+ *                 for its down product). Its codes are those of the value in 64 bits; a value beyond
+ *                 fp32's range counts as infinite.
+ *   x             rows of ld_x elements (dtype), aligned to its element
+ *   q             uint8 [rows, K / 2] out, 16-byte aligned;  scales  uint8 [rows, K / 32] out
+ * mol_mx4_dequantize - the values of codes and scales, x [rows, ld_x] (dtype) out: exact in both dtypes
+ *   up to s = 252, infinite where they pass fp32's range beyond.
+ * rows = 0 enqueues nothing. Errors: MOL_E_ARG, MOL_E_DTYPE, MOL_E_ALIGN, MOL_E_LIMIT (rows * K / 8
+ * past 2^31 - 4096).
+ *
+ * mol_moe_gemm_mx4 - mol_moe_gemm's base product over such weights:
+ *   out[p, n] = round( sum_k W[t, n, k] * xin[p / row_div, k] )
+ * for every pair p with a local base expert t in [0, E); other rows are untouched. Products and sums
+ * are fp32, rounded once. num_experts = 1 and ids of zero give the product with a single matrix.
+ *   dtype         MOL_F32 or MOL_BF16 of out, and of xin without x_scales
+ *   xin, x_scales x_scales NULL: rows of ld_x elements (dtype). Else rows of codes, ld_x / 2 bytes apart
+ *                 (ld_x a multiple of 32), with scales ld_x / 32 bytes apart
+ *   W             uint8 [E, N, K / 2], 16-byte aligned;  scales uint8 [E, N, K / 32]
+ *   others        as for mol_moe_gemm (rows of xin on 16-byte boundaries)
+ * For decode and prefill batches; blocks of any block_m are taken. Dense blocks run fastest at block_m
+ * = 128.
+ * Errors: MOL_E_ARG (K not a multiple of 32), MOL_E_LIMIT (one expert's weights 2 GiB or more, 4 GiB or more
+ * of x_scales, 2^24 work items or more), others as for mol_moe_gemm.
+ * ------------------------------------------------------------------------------- */
+enum { MOL_ACT_NONE = 0, MOL_ACT_SILU_MUL = 1 };
+
+MOL_API mol_status mol_mx4_quantize(int32_t dtype, int32_t activation, const void *x,
+                                    int64_t ld_x, int64_t rows, int32_t K, uint8_t *q,
+                                    uint8_t *scales, void *stream);
+MOL_API mol_status mol_mx4_dequantize(int32_t dtype, const uint8_t *q, const uint8_t *scales,
+                                      int64_t rows, int32_t K, void *x, int64_t ld_x,
+                                      void *stream);
+MOL_API mol_status mol_moe_gemm_mx4(int32_t dtype, const void *xin, int64_t ld_x,
+                                    const uint8_t *x_scales, int32_t row_div, const uint8_t *W,
+                                    const uint8_t *scales, int32_t K, int32_t N,
+                                    int32_t num_experts, const int32_t *sorted_ids,
+                                    const int32_t *expert_ids, const int32_t *num_post_padded,
+                                    int32_t numel, int32_t block_m, void *out, int64_t ld_out,
+                                    void *stream);
 
 /* ---------------------------------------------------------------------------------
  * mol_moe_layer - a whole layer for a few tokens, from the routed ids to the combined rows, with

@@ -22,6 +22,7 @@ MOL_F32, MOL_BF16 = 0, 1
 MOL_MAX_BUCKETS = 8192
 MOL_SCORE_SOFTMAX, MOL_SCORE_SIGMOID = 0, 1
 MOL_MAX_ROUTER_TOPK = 64
+MOL_ACT_NONE, MOL_ACT_SILU_MUL = 0, 1
 
 # every symbol include/mol.h declares, with (restype, argtypes)
 _P, _I32, _I64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
@@ -54,6 +55,15 @@ SIGNATURES = {
                                _P, _P, _P]),
     "mol_moe_gemm_q4": (_I32, [_I32, _P, _I64, _I32, _P, _P, _P, _I32, _I32, _I32, _I32, _P, _P,
                                _P, _I32, _I32, _P, _I64, _P]),
+    "mol_router_balance_workspace_bytes": (_I64, [_I32, _I32]),
+    "mol_router_balance": (_I32, [_I32, _P, _I64, _P, _P, _I32, _I32, _I32, _I32, _F32, _P, _P, _P,
+                                  _P, _SZ, _P]),
+    "mol_router_balance_grad": (_I32, [_I32, _P, _I64, _P, _P, _P, _I32, _I32, _I32, _I32, _F32,
+                                       _P, _I64, _P]),
+    "mol_mx4_quantize": (_I32, [_I32, _I32, _P, _I64, _I64, _I32, _P, _P, _P]),
+    "mol_mx4_dequantize": (_I32, [_I32, _P, _P, _I64, _I32, _P, _I64, _P]),
+    "mol_moe_gemm_mx4": (_I32, [_I32, _P, _I64, _P, _I32, _P, _P, _I32, _I32, _I32, _P, _P, _P,
+                                _I32, _I32, _P, _I64, _P]),
     "mol_moe_layer_workspace_bytes": (_I64, [_I32, _I32, _I32, _I32, _I32, _I32]),
     "mol_moe_layer": (_I32, [_P, _P, _P, _I64, _P, _P, _P, _I32, _I32, _P, _I64, _P, _SZ, _P]),
 }
@@ -459,6 +469,19 @@ def _q4(W, scales, zeros, name: str, dev):
     return N, 2 * half, 2 * half // scales.shape[2]
 
 
+def _routing(dev, E: int, numel: int, block_m: int, sorted_ids, expert_ids, num_post_padded):
+    """The aligned blocks of a batch are on dev, and as long as any routing of numel pairs can be."""
+    # the routing's bound on blocks, as mol_align_max_blocks has it (which the call checks again)
+    blocks = -(-(numel + min(numel, E + 1) * (block_m - 1)) // block_m) if block_m > 0 else 0
+    for t, name, least in ((sorted_ids, "sorted_ids", blocks * block_m),
+                           (expert_ids, "expert_ids", blocks),
+                           (num_post_padded, "num_post_padded", 1)):
+        if t.dtype is not torch.int32 or t.device != dev or not t.is_contiguous():
+            _on(dev, name, t, torch.int32, t.shape)
+        if t.numel() < least:
+            raise ValueError(f"{name} has {t.numel()} entries, fewer than the routing's {least}")
+
+
 def mol_moe_gemm_q4(xin, row_div: int, W, scales, sorted_ids, expert_ids, num_post_padded,
                     numel: int, block_m: int, out, zeros=None):
     """The base grouped GEMM of a stage into out [numel, N] over 4-bit weights W uint8
@@ -475,18 +498,190 @@ def mol_moe_gemm_q4(xin, row_div: int, W, scales, sorted_ids, expert_ids, num_po
         raise ValueError(f"xin has {xin.shape[0]} rows: {numel} pairs need "
                          f"{-(-numel // row_div)}")
     ld_out = _rows(out, "out", dev, dtype, (numel, N))
-    # the routing's bound on blocks, as mol_align_max_blocks has it (which the call checks again)
-    blocks = -(-(numel + min(numel, E + 1) * (block_m - 1)) // block_m) if block_m > 0 else 0
-    for t, name, least in ((sorted_ids, "sorted_ids", blocks * block_m),
-                           (expert_ids, "expert_ids", blocks),
-                           (num_post_padded, "num_post_padded", 1)):
-        if t.dtype is not torch.int32 or t.device != dev or not t.is_contiguous():
-            _on(dev, name, t, torch.int32, t.shape)
-        if t.numel() < least:
-            raise ValueError(f"{name} has {t.numel()} entries, fewer than the routing's {least}")
+    _routing(dev, E, numel, block_m, sorted_ids, expert_ids, num_post_padded)
     _call(dev, "mol_moe_gemm_q4", _dtype_code(scales), xin.data_ptr(), ld_x, row_div,
           W.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(), group, K,
           N, E, sorted_ids.data_ptr(), expert_ids.data_ptr(), num_post_padded.data_ptr(), numel,
+          block_m, out.data_ptr(), ld_out)
+    return out
+
+
+def mol_router_balance_workspace_bytes(M: int, num_experts: int) -> int:
+    _fit("mol_router_balance_workspace_bytes", M, num_experts)
+    v = lib().mol_router_balance_workspace_bytes(M, num_experts)
+    if v < 0:
+        raise MolError("mol_router_balance_workspace_bytes", -v)
+    return int(v)
+
+
+def new_router_balance_workspace(M: int, num_experts: int, device):
+    """A workspace for mol_router_balance at up to M tokens (its contents need no initialisation)."""
+    n = mol_router_balance_workspace_bytes(M, num_experts)
+    return torch.empty(max(256, n), dtype=torch.uint8, device=device)
+
+
+def _logits(fn: str, logits, topk: int, scoring: int, token_mask):
+    """(M, E, row stride, mask pointer) of a batch's logits."""
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be 2-d with contiguous rows")
+    M, E = logits.shape
+    _fit(fn, M, E, topk, scoring)
+    if token_mask is not None:
+        if token_mask.dtype is not torch.bool and token_mask.dtype is not torch.uint8:
+            raise TypeError(f"token_mask must be bool or uint8, got {token_mask.dtype}")
+        _on(logits.device, "token_mask", token_mask, token_mask.dtype, (M,))
+        token_mask = token_mask.data_ptr()
+    return M, E, logits.stride(0) if M > 1 else max(logits.stride(0), E), token_mask
+
+
+def mol_router_balance(logits, topk_ids, scoring: int = MOL_SCORE_SOFTMAX, alpha: float = 1.0,
+                       token_mask=None, counts=None, prob_sums=None, loss=None, workspace=None):
+    """The balance loss of a routed batch from its logits [M, E] (rows may be strided) and the ids
+    [M, topk] chosen over all experts: (loss float32 [1], counts int32 [E + 1] with the number of tokens
+    last, prob_sums float32 [E]). token_mask bool or uint8 [M]: 0 for tokens that do not count."""
+    dev = logits.device
+    if topk_ids.dim() != 2:
+        raise ValueError("topk_ids must be 2-d")
+    topk = topk_ids.shape[1]
+    M, E, ld, mask = _logits("mol_router_balance", logits, topk, scoring, token_mask)
+    _on(dev, "topk_ids", topk_ids, torch.int32, (M, topk))
+    if counts is None:
+        counts = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    else:
+        _on(dev, "counts", counts, torch.int32, (E + 1,))
+    if prob_sums is None:
+        prob_sums = torch.empty(E, dtype=torch.float32, device=dev)
+    else:
+        _on(dev, "prob_sums", prob_sums, torch.float32, (E,))
+    if loss is None:
+        loss = torch.empty(1, dtype=torch.float32, device=dev)
+    else:
+        _on(dev, "loss", loss, torch.float32, (1,))
+    if workspace is None:
+        workspace = new_router_balance_workspace(M, E, dev)
+    _on(dev, "workspace", workspace, torch.uint8, workspace.shape)
+    _call(dev, "mol_router_balance", _dtype_code(logits), logits.data_ptr(), ld, topk_ids.data_ptr(),
+          mask, M, E, topk, scoring, alpha, counts.data_ptr(), prob_sums.data_ptr(), loss.data_ptr(),
+          workspace.data_ptr(), workspace.numel())
+    return loss, counts, prob_sums
+
+
+def mol_router_balance_grad(logits, counts, topk: int, scoring: int = MOL_SCORE_SOFTMAX,
+                            alpha: float = 1.0, token_mask=None, grad_loss=None, out=None):
+    """The gradient of mol_router_balance's loss in the logits [M, E] (dtype of logits), from its counts (or
+    their sums over ranks); grad_loss float32 [1], the gradient that arrives at the loss (None: 1)."""
+    dev = logits.device
+    M, E, ld, mask = _logits("mol_router_balance_grad", logits, topk, scoring, token_mask)
+    _on(dev, "counts", counts, torch.int32, (E + 1,))
+    if grad_loss is not None:
+        _on(dev, "grad_loss", grad_loss, torch.float32, (1,))
+    if out is None:
+        out = torch.empty((M, E), dtype=logits.dtype, device=dev)
+    ld_out = _rows(out, "out", dev, logits.dtype, (M, E))
+    _call(dev, "mol_router_balance_grad", _dtype_code(logits), logits.data_ptr(), ld, mask,
+          counts.data_ptr(), None if grad_loss is None else grad_loss.data_ptr(), M, E, topk, scoring,
+          alpha, out.data_ptr(), ld_out)
+    return out
+
+
+def _as_rows(t: torch.Tensor, name: str):
+    """(rows, width, row stride) of a tensor of one row dimension or more, the last dimension contiguous."""
+    if t.dim() < 2:
+        raise ValueError(f"{name} must have rows: at least 2 dimensions")
+    width = t.shape[-1]
+    if t.dim() > 2 or t.is_contiguous():
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous, or 2-d with contiguous rows")
+        return t.numel() // width if width else 0, width, width
+    if t.stride(1) != 1 and width > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    rows = t.shape[0]
+    return rows, width, t.stride(0) if rows > 1 else max(t.stride(0), width)
+
+
+def mol_mx4_quantize(x, activation: int = MOL_ACT_NONE, q=None, scales=None):
+    """Rows [..., K] of bf16 or fp32 (strided rows if 2-d) as MX4: (q uint8 [..., K/2], scales uint8
+    [..., K/32]). MOL_ACT_SILU_MUL: rows [..., 2 K], gate columns first, as SiLU(gate) * up."""
+    rows, width, ld = _as_rows(x, "x")
+    if activation not in (MOL_ACT_NONE, MOL_ACT_SILU_MUL):
+        raise ValueError(f"unknown activation {activation}")
+    K = width // 2 if activation == MOL_ACT_SILU_MUL else width
+    if K < 1 or K % 32 or (activation == MOL_ACT_SILU_MUL and width % 2):
+        raise ValueError(f"rows of {width} are not whole blocks of 32 values")
+    _fit("mol_mx4_quantize", K)
+    dev, lead = x.device, x.shape[:-1]
+    if q is None:
+        q = torch.empty((*lead, K // 2), dtype=torch.uint8, device=dev)
+    else:
+        _on(dev, "q", q, torch.uint8, (*lead, K // 2))
+    if scales is None:
+        scales = torch.empty((*lead, K // 32), dtype=torch.uint8, device=dev)
+    else:
+        _on(dev, "scales", scales, torch.uint8, (*lead, K // 32))
+    _call(dev, "mol_mx4_quantize", _dtype_code(x), activation, x.data_ptr(), ld, rows, K, q.data_ptr(),
+          scales.data_ptr())
+    return q, scales
+
+
+def mol_mx4_dequantize(q, scales, dtype=torch.bfloat16, out=None):
+    """The values [..., K] of MX4 codes q uint8 [..., K/2] and scales uint8 [..., K/32], in dtype (that of
+    out, whose rows may be strided if 2-d)."""
+    dev = q.device
+    if q.dim() < 2:
+        raise ValueError("q must have rows: at least 2 dimensions")
+    lead, K = q.shape[:-1], 2 * q.shape[-1]
+    if K < 1 or K % 32:
+        raise ValueError(f"rows of {K} are not whole blocks of 32 values")
+    _fit("mol_mx4_dequantize", K)
+    _on(dev, "q", q, torch.uint8, q.shape)
+    _on(dev, "scales", scales, torch.uint8, (*lead, K // 32))
+    if out is None:
+        out = torch.empty((*lead, K), dtype=dtype, device=dev)
+    elif out.shape != (*lead, K) or out.device != dev:
+        raise ValueError(f"out must be {(*lead, K)} on {dev}, got {tuple(out.shape)} on {out.device}")
+    rows, _, ld = _as_rows(out, "out")
+    _call(dev, "mol_mx4_dequantize", _dtype_code(out), q.data_ptr(), scales.data_ptr(), rows, K,
+          out.data_ptr(), ld)
+    return out
+
+
+def mol_moe_gemm_mx4(xin, row_div: int, W, scales, sorted_ids, expert_ids, num_post_padded,
+                     numel: int, block_m: int, out, x_scales=None):
+    """The base grouped GEMM of a stage into out [numel, N] (bf16 or fp32) over MX4 weights W uint8
+    [E, N, K/2] with scales uint8 [E, N, K/32] (routing by base expert). xin: rows [., K] in the dtype of
+    out, or with x_scales uint8 [., K/32] rows of MX4 codes uint8 [., K/2]."""
+    _fit("mol_moe_gemm_mx4", row_div, numel, block_m)
+    dev = W.device
+    if W.dim() != 3:
+        raise ValueError("W must be [E, N, K/2]")
+    E, N, half = W.shape
+    K = 2 * half
+    _fit("mol_moe_gemm_mx4", E, N, K)
+    if K < 1 or K % 32:
+        raise ValueError(f"W: rows of {K} are not whole blocks of 32 values")
+    _on(dev, "W", W, torch.uint8, (E, N, half))
+    _on(dev, "scales", scales, torch.uint8, (E, N, K // 32))
+    if xin.dim() != 2:
+        raise ValueError("xin must be 2-d")
+    rows, dtype = xin.shape[0], out.dtype
+    if x_scales is None:
+        ld_x = _rows(xin, "xin", dev, dtype, (rows, K))
+    else:
+        ld_x = 2 * _rows(xin, "xin", dev, torch.uint8, (rows, half))
+        ld_s = _rows(x_scales, "x_scales", dev, torch.uint8, (rows, K // 32))
+        if rows > 1 and ld_s * 32 != ld_x:
+            raise ValueError(f"rows of xin are {ld_x} values apart, rows of x_scales {ld_s * 32}")
+        if rows == 1:
+            ld_x = K
+    if row_div < 1:
+        raise ValueError(f"row_div must be at least 1, got {row_div}")
+    if rows * row_div < numel:
+        raise ValueError(f"xin has {rows} rows: {numel} pairs need {-(-numel // row_div)}")
+    ld_out = _rows(out, "out", dev, dtype, (numel, N))
+    _routing(dev, E, numel, block_m, sorted_ids, expert_ids, num_post_padded)
+    _call(dev, "mol_moe_gemm_mx4", _dtype_code(out), xin.data_ptr(), ld_x,
+          None if x_scales is None else x_scales.data_ptr(), row_div, W.data_ptr(), scales.data_ptr(),
+          K, N, E, sorted_ids.data_ptr(), expert_ids.data_ptr(), num_post_padded.data_ptr(), numel,
           block_m, out.data_ptr(), ld_out)
     return out
 

@@ -799,6 +799,212 @@ MOL_API mol_status mol_moe_gemm_q4(int32_t dtype, const void* xin, int64_t ld_x,
   return hip_status(mol::launch_q4_gemm(a, bf16, (hipStream_t)stream));
 }
 
+// ---- microscaled 4-bit floats ----------------------------------------------------------
+
+namespace {
+
+// What quantise and dequantise share; vecs 0 with MOL_OK: nothing to do.
+mol_status mx4_args(int32_t dtype, const void* x, int64_t ld, int64_t width, int64_t rows, int32_t K,
+                    const void* q, const void* scales, mol::MxArgs& a) {
+  if (dtype != MOL_F32 && dtype != MOL_BF16) return MOL_E_DTYPE;
+  if (rows < 0 || K < 1 || K % mol::kMxValues || ld < width) return MOL_E_ARG;
+  if (rows > mol::kMxMaxVecs / (K / 8)) return MOL_E_LIMIT;
+  if (rows == 0) return MOL_OK;
+  if (!x || !q || !scales) return MOL_E_ARG;
+  const int esz = dtype == MOL_BF16 ? 2 : 4;
+  if (!aligned_to(x, esz) || !aligned16(q)) return MOL_E_ALIGN;
+  a.ld = ld;
+  a.K = K;
+  a.vpr = K / 8;
+  a.vecs = (int32_t)(rows * a.vpr);
+  a.vec = aligned16(x) && (ld * esz) % 16 == 0;
+  a.f_vpr = mol::make_fastdiv((uint32_t)a.vpr);
+  return MOL_OK;
+}
+
+}  // namespace
+
+MOL_API mol_status mol_mx4_quantize(int32_t dtype, int32_t activation, const void* x, int64_t ld_x,
+                                    int64_t rows, int32_t K, uint8_t* q, uint8_t* scales,
+                                    void* stream) {
+  if (activation != MOL_ACT_NONE && activation != MOL_ACT_SILU_MUL) return MOL_E_ARG;
+  const bool act = activation == MOL_ACT_SILU_MUL;
+  mol::MxArgs a{};
+  const mol_status st = mx4_args(dtype, x, ld_x, act ? 2 * (int64_t)K : K, rows, K, q, scales, a);
+  if (st != MOL_OK || a.vecs == 0) return st;
+  a.x = x;
+  a.q = q;
+  a.scales = scales;
+  return hip_status(mol::launch_mx4_quantize(a, dtype == MOL_BF16, act, (hipStream_t)stream));
+}
+
+MOL_API mol_status mol_mx4_dequantize(int32_t dtype, const uint8_t* q, const uint8_t* scales,
+                                      int64_t rows, int32_t K, void* x, int64_t ld_x, void* stream) {
+  mol::MxArgs a{};
+  const mol_status st = mx4_args(dtype, x, ld_x, K, rows, K, q, scales, a);
+  if (st != MOL_OK || a.vecs == 0) return st;
+  a.out = x;
+  a.q = const_cast<uint8_t*>(q);
+  a.scales = const_cast<uint8_t*>(scales);
+  return hip_status(mol::launch_mx4_dequantize(a, dtype == MOL_BF16, (hipStream_t)stream));
+}
+
+MOL_API mol_status mol_moe_gemm_mx4(int32_t dtype, const void* xin, int64_t ld_x,
+                                    const uint8_t* x_scales, int32_t row_div, const uint8_t* W,
+                                    const uint8_t* scales, int32_t K, int32_t N, int32_t num_experts,
+                                    const int32_t* sorted_ids, const int32_t* expert_ids,
+                                    const int32_t* num_post_padded, int32_t numel, int32_t block_m,
+                                    void* out, int64_t ld_out, void* stream) {
+  const StageCheck rc =
+      routing_check(sorted_ids, expert_ids, num_post_padded, numel, num_experts, block_m);
+  if (rc.st != MOL_OK) return rc.st;
+  if (dtype != MOL_F32 && dtype != MOL_BF16) return MOL_E_DTYPE;
+  if (K < 1 || K % mol::kMxValues || N < 1 || row_div < 1 || ld_x < K || ld_out < N) return MOL_E_ARG;
+  if (N * (int64_t)(K / 2) >= (int64_t(1) << 31)) return MOL_E_LIMIT;  // one expert's weights
+  if (numel == 0) return MOL_OK;
+  if (!xin || !W || !scales || !out) return MOL_E_ARG;
+  const bool bf16 = dtype == MOL_BF16;
+  const int esz = bf16 ? 2 : 4;
+  if (x_scales ? ld_x % mol::kMxValues != 0 : (ld_x * esz) % 16 != 0) return MOL_E_ALIGN;
+  if (!aligned16(xin) || !aligned16(W) || !aligned_to(out, esz)) return MOL_E_ALIGN;
+  mol::MxGemmArgs a{};
+  a.x = xin;
+  a.x_bytes = x_scales ? ld_x / 2 : ld_x * esz;
+  a.x_scales = x_scales;
+  a.ld_xs = ld_x / mol::kMxValues;
+  // (the kernels address the scales of x by 32-bit offsets)
+  if (x_scales && cdiv64(numel, row_div) > ((int64_t(1) << 32) - 1) / a.ld_xs) return MOL_E_LIMIT;
+  a.W = W;
+  a.scales = scales;
+  a.K = K;
+  a.N = N;
+  a.E = num_experts;
+  a.blocks = K / mol::kMxValues;
+  a.pairs_w = a.blocks % 2 == 0 && aligned_to(scales, 2);
+  a.pairs_x = a.blocks % 2 == 0 && a.ld_xs % 2 == 0 && aligned_to(x_scales, 2);
+  a.vec_out = ld_out % 4 == 0 && aligned_to(out, 4 * esz);
+  a.sorted = sorted_ids;
+  a.expert_ids = expert_ids;
+  a.npp = num_post_padded;
+  a.numel = numel;
+  a.BM = block_m;
+  a.max_blocks = (int32_t)rc.max_blocks;
+  a.out = out;
+  a.ld_out = ld_out;
+  a.f_rd = mol::make_fastdiv((uint32_t)row_div);
+  a.f_bm = mol::make_fastdiv((uint32_t)block_m);
+  // blocks that hold pairs: at most one partly filled per expert, beside the full ones
+  const int64_t filled = std::min<int64_t>(numel, (int64_t)num_experts + numel / block_m);
+  const int form = mol::mx_form(filled, numel, N);
+  if (rc.max_blocks * mol::mx_items(form, N, block_m) + 8 > kGridMax) return MOL_E_LIMIT;
+  return hip_status(mol::launch_mx4_gemm(a, bf16, form, (hipStream_t)stream));
+}
+
+// ---- balance loss --------------------------------------------------------------------
+
+namespace {
+
+struct BalanceWorkspace {
+  int64_t counts, done, bytes;  // offsets (the sums come first), and the whole
+};
+BalanceWorkspace balance_workspace(int64_t M, int32_t E) {
+  const int64_t groups = mol::balance_groups(M, E);
+  BalanceWorkspace w{};
+  if (groups == 1) return w;
+  w.counts = round256(groups * E * 4);
+  w.done = w.counts + round256(groups * (E + 1) * 4);
+  w.bytes = w.done + 256;
+  return w;
+}
+
+mol_status balance_check(int32_t dtype, int64_t ld, int32_t M, int32_t E, int32_t topk,
+                         int32_t scoring, float alpha) {
+  if (dtype != MOL_F32 && dtype != MOL_BF16) return MOL_E_DTYPE;
+  if (M < 0 || E < 1 || topk < 1 || ld < E || !std::isfinite(alpha)) return MOL_E_ARG;
+  if (scoring != MOL_SCORE_SOFTMAX && scoring != MOL_SCORE_SIGMOID) return MOL_E_ARG;
+  if ((int64_t)E + 1 > MOL_MAX_BUCKETS || topk > MOL_MAX_ROUTER_TOPK || (int64_t)M * topk > kI32Max)
+    return MOL_E_LIMIT;
+  return MOL_OK;
+}
+
+mol::BalanceArgs balance_args(const void* logits, int64_t ld, const uint8_t* mask, int32_t M, int32_t E,
+                              int32_t topk, int32_t scoring, float alpha, int esz) {
+  mol::BalanceArgs a{};
+  a.logits = logits;
+  a.ld = ld;
+  a.mask = mask;
+  a.M = M;
+  a.E = E;
+  a.topk = topk;
+  a.sigmoid = scoring == MOL_SCORE_SIGMOID;
+  a.vec = aligned16(logits) && (ld * esz) % 16 == 0;
+  a.alpha = alpha;
+  return a;
+}
+
+}  // namespace
+
+MOL_API int64_t mol_router_balance_workspace_bytes(int32_t M, int32_t num_experts) {
+  if (M < 0 || num_experts < 1) return -MOL_E_ARG;
+  if ((int64_t)num_experts + 1 > MOL_MAX_BUCKETS) return -MOL_E_LIMIT;
+  return balance_workspace(M, num_experts).bytes;
+}
+
+MOL_API mol_status mol_router_balance(int32_t dtype, const void* logits, int64_t ld_logits,
+                                      const int32_t* topk_ids, const uint8_t* token_mask, int32_t M,
+                                      int32_t num_experts, int32_t topk, int32_t scoring, float alpha,
+                                      int32_t* counts, float* prob_sums, float* loss,
+                                      void* workspace, size_t workspace_bytes, void* stream) {
+  const mol_status st = balance_check(dtype, ld_logits, M, num_experts, topk, scoring, alpha);
+  if (st != MOL_OK) return st;
+  if (!counts || !prob_sums || !loss || (M > 0 && (!logits || !topk_ids))) return MOL_E_ARG;
+  const int esz = dtype == MOL_BF16 ? 2 : 4;
+  if (!aligned_to(logits, esz) || !aligned_to(topk_ids, 4) || !aligned_to(counts, 4) ||
+      !aligned_to(prob_sums, 4) || !aligned_to(loss, 4))
+    return MOL_E_ALIGN;
+  const BalanceWorkspace ws = balance_workspace(M, num_experts);
+  if (ws.bytes && (!workspace || workspace_bytes < (size_t)ws.bytes)) return MOL_E_WORKSPACE;
+  if (ws.bytes && !aligned16(workspace)) return MOL_E_ALIGN;
+  mol::BalanceArgs a =
+      balance_args(logits, ld_logits, token_mask, M, num_experts, topk, scoring, alpha, esz);
+  a.ids = topk_ids;
+  a.counts = counts;
+  a.sums = prob_sums;
+  a.loss = loss;
+  a.groups = mol::balance_groups(M, num_experts);
+  if (ws.bytes) {
+    char* base = static_cast<char*>(workspace);
+    a.part_sums = reinterpret_cast<float*>(base);
+    a.part_counts = reinterpret_cast<int32_t*>(base + ws.counts);
+    a.done = reinterpret_cast<int32_t*>(base + ws.done);
+  }
+  return hip_status(mol::launch_balance(a, dtype == MOL_BF16, (hipStream_t)stream));
+}
+
+MOL_API mol_status mol_router_balance_grad(int32_t dtype, const void* logits, int64_t ld_logits,
+                                           const uint8_t* token_mask, const int32_t* counts,
+                                           const float* grad_loss, int32_t M, int32_t num_experts,
+                                           int32_t topk, int32_t scoring, float alpha,
+                                           void* grad_logits, int64_t ld_grad, void* stream) {
+  const mol_status st = balance_check(dtype, ld_logits, M, num_experts, topk, scoring, alpha);
+  if (st != MOL_OK) return st;
+  if (ld_grad < num_experts) return MOL_E_ARG;
+  if (M == 0) return MOL_OK;
+  if (!logits || !counts || !grad_logits) return MOL_E_ARG;
+  const int esz = dtype == MOL_BF16 ? 2 : 4;
+  if (!aligned_to(logits, esz) || !aligned_to(counts, 4) || !aligned_to(grad_loss, 4) ||
+      !aligned_to(grad_logits, esz))
+    return MOL_E_ALIGN;
+  mol::BalanceArgs a =
+      balance_args(logits, ld_logits, token_mask, M, num_experts, topk, scoring, alpha, esz);
+  a.vec_grad = aligned16(grad_logits) && (ld_grad * esz) % 16 == 0;
+  a.counts = const_cast<int32_t*>(counts);
+  a.up = grad_loss;
+  a.grad = grad_logits;
+  a.ld_grad = ld_grad;
+  return hip_status(mol::launch_balance_grad(a, dtype == MOL_BF16, (hipStream_t)stream));
+}
+
 // ---- whole layer ---------------------------------------------------------------------
 
 MOL_API int64_t mol_moe_layer_workspace_bytes(int32_t dtype, int32_t M, int32_t topk,

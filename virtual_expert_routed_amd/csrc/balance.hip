@@ -1,0 +1,292 @@
+// The balance loss of a routed batch, the experts' counts, and the gradient in the router's logits.
+//
+// Over the n tokens that count (not masked out, with at least one candidate logit), with c_e the
+// number of their top-k slots that hold expert e and p_me the scores of token m over its candidates
+// (softmax, or sigmoids over their sum):
+//   P_e = sum_m p_me,    loss = alpha E / (k n^2) sum_e c_e P_e
+//   d loss / d l_mj = p_mj q_mj (b_j - sum_e p_me b_e),    b_e = alpha / (k n^2) (E c_e - k n)
+// with q = 1 for softmax and 1 - sigmoid(l_mj) for sigmoid. b is the derivative in p_me less alpha / n,
+// which is the same for every expert and leaves the difference as it is (the p_me of a token add up
+// to 1): E c_e - k n is formed in whole numbers, so a nearly balanced batch loses nothing to cancellation.
+//
+// A row of logits is in the registers of LPR lanes, as in the router. The forward pass gives each
+// workgroup a strided set of rows; a thread adds up the scores of its own experts over its rows, the
+// workgroup adds its threads in a fixed order and writes one row of partial sums (and of counts, from
+// whole-number atomics in LDS). A second launch adds the rows, 64 experts a workgroup; the last
+// workgroup to finish forms the loss. Few tokens take one workgroup and one launch. No sum depends
+// on the order in which anything arrives: results are the same bit for bit.
+#include "router_row.h"
+
+namespace mol {
+namespace {
+
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
+// A row's scores before their sum is divided out, in place of its logits; m their largest logit.
+// Sigmoids are multiplied by exp(-min(m, 0)), which keeps the largest from underflowing.
+template <int VPL>
+__device__ __forceinline__ float scores(float (&v)[VPL], float m, bool sigmoid) {
+  float sum = 0.f;
+  const float shift = fminf(m, 0.f);
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    float w = 0.f;
+    if (v[i] != kMasked) {
+      if (!sigmoid) w = exp_below(v[i], m);
+      else w = v[i] > 0.f ? 1.f / (1.f + expf(-v[i])) : exp_below(v[i], shift) / (1.f + expf(v[i]));
+    }
+    v[i] = w;
+    sum += w;
+  }
+  return sum;
+}
+
+__device__ __forceinline__ float loss_of(double cp, int n, const BalanceArgs& a) {
+  if (n <= 0) return 0.f;
+  return (float)((double)a.alpha * a.E * cp / ((double)a.topk * n * n));
+}
+
+// sum over the workgroup's threads, in a fixed order, in thread 0
+__device__ __forceinline__ double block_sum(double v, double* lds) {
+  for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d, 64);
+  if ((threadIdx.x & 63) == 0) lds[wave_id()] = v;
+  __syncthreads();
+  return threadIdx.x == 0 ? (lds[0] + lds[1]) + (lds[2] + lds[3]) : 0.0;
+}
+
+template <bool BF16, int LPR, int VPL>
+__global__ void __launch_bounds__(kThreads) balance_kernel(BalanceArgs a) {
+  constexpr int ESZ = BF16 ? 2 : 4;
+  constexpr int RPW = kThreads / LPR;   // rows at a time
+  constexpr int W = LPR * VPL;          // experts of the registers, at least E
+  __shared__ float part[W];
+  __shared__ int hist[W + 1];           // counts, then the tokens that count
+  __shared__ double red[kThreads / 64];
+  const int tid = threadIdx.x, lane = tid & 63, lr = lane % LPR;
+  for (int e = tid; e <= W; e += kThreads) hist[e] = 0;
+  __syncthreads();
+  const int e0 = lr * VPL, n = min(max(a.E - e0, 0), VPL);
+  float acc[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) acc[i] = 0.f;
+  for (int64_t r0 = (int64_t)blockIdx.x * RPW; r0 < a.M; r0 += (int64_t)gridDim.x * RPW) {
+    const int64_t row = r0 + tid / LPR;
+    const bool in = row < a.M && (!a.mask || a.mask[row]);
+    float v[VPL];
+    load_row<BF16, VPL>((const char*)a.logits + (in ? row : 0) * a.ld * ESZ, e0, in ? n : 0, a.vec, v);
+    float m = kMasked;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) m = fmaxf(m, v[i]);
+    m = group_max<LPR>(m);
+    const float sum = group_sum<LPR>(scores<VPL>(v, m, a.sigmoid));
+    if (m != kMasked) {  // (the same in all lanes of a row)
+      const float inv = 1.f / sum;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
+      for (int j = lr; j < a.topk; j += LPR) {
+        const int e = a.ids[row * a.topk + j];
+        if ((unsigned)e < (unsigned)a.E) atomicAdd(&hist[e], 1);
+      }
+      if (lr == 0) atomicAdd(&hist[W], 1);
+    }
+  }
+  // the rows of a wave, then wave after wave
+  if constexpr (LPR < 64) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      acc[i] += __shfl_xor(acc[i], 16, 64);
+      acc[i] += __shfl_xor(acc[i], 32, 64);
+    }
+  }
+  for (int w = 0; w < kThreads / 64; ++w) {
+    if (w == wave_id() && lane < LPR) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) part[e0 + i] = w ? part[e0 + i] + acc[i] : acc[i];
+    }
+    __syncthreads();
+  }
+  const bool alone = gridDim.x == 1;
+  float* sums = alone ? a.sums : a.part_sums + (int64_t)blockIdx.x * a.E;
+  int* counts = alone ? a.counts : a.part_counts + (int64_t)blockIdx.x * (a.E + 1);
+  double cp = 0.0;
+  for (int e = tid; e < a.E; e += kThreads) {
+    const float p = part[e];
+    sums[e] = p;
+    counts[e] = hist[e];
+    cp += (double)hist[e] * p;
+  }
+  if (tid == 0) counts[a.E] = hist[W];
+  if (alone) {
+    cp = block_sum(cp, red);
+    if (tid == 0) *a.loss = loss_of(cp, hist[W], a);
+  } else if (blockIdx.x == 0 && tid == 0) {
+    *a.done = 0;
+  }
+}
+
+// Adds the workgroups' rows: 64 experts (one of them the count of tokens), four ranges of rows each.
+__global__ void __launch_bounds__(kThreads) balance_finish_kernel(BalanceArgs a) {
+  __shared__ double part[kThreads / 64][64];
+  __shared__ int count[kThreads / 64][64];
+  __shared__ double red[kThreads / 64];
+  __shared__ bool last;
+  const int tid = threadIdx.x, lane = tid & 63, w = wave_id();
+  const int e = blockIdx.x * 64 + lane;
+  const int per = (a.groups + 3) / 4, g1 = min((w + 1) * per, a.groups);
+  double p = 0.0;
+  int c = 0;
+  if (e <= a.E) {
+#pragma unroll 8
+    for (int g = w * per; g < g1; ++g) {
+      c += a.part_counts[(int64_t)g * (a.E + 1) + e];
+      if (e < a.E) p += (double)a.part_sums[(int64_t)g * a.E + e];
+    }
+  }
+  part[w][lane] = p;
+  count[w][lane] = c;
+  __syncthreads();
+  if (w == 0 && e <= a.E) {
+    c = (count[0][lane] + count[1][lane]) + (count[2][lane] + count[3][lane]);
+    __hip_atomic_store(&a.counts[e], c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (e < a.E)
+      __hip_atomic_store(&a.sums[e],
+                         (float)((part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane])),
+                         __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  // the workgroup that is the last to have stored its experts sees all of them
+  if (w == 0) {
+    __threadfence();
+    if (lane == 0)
+      last = __hip_atomic_fetch_add(a.done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+             (int)gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  double cp = 0.0;
+  for (int i = tid; i < a.E; i += kThreads)
+    cp += (double)__hip_atomic_load(&a.counts[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) *
+          __hip_atomic_load(&a.sums[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  cp = block_sum(cp, red);
+  if (tid == 0)
+    *a.loss = loss_of(cp, __hip_atomic_load(&a.counts[a.E], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT), a);
+}
+
+// No tokens: everything is zero.
+__global__ void __launch_bounds__(kThreads) balance_empty_kernel(BalanceArgs a) {
+  for (int e = threadIdx.x; e <= a.E; e += kThreads) {
+    a.counts[e] = 0;
+    if (e < a.E) a.sums[e] = 0.f;
+  }
+  if (threadIdx.x == 0) *a.loss = 0.f;
+}
+
+template <bool BF16, int LPR, int VPL>
+__global__ void __launch_bounds__(kThreads) balance_grad_kernel(BalanceArgs a) {
+  constexpr int ESZ = BF16 ? 2 : 4;
+  constexpr int RPW = kThreads / LPR;
+  constexpr int VE = 16 / ESZ;
+  const int tid = threadIdx.x, lr = tid % LPR;
+  const int e0 = lr * VPL, n = min(max(a.E - e0, 0), VPL);
+  const int tokens = a.counts[a.E];
+  const double unit = tokens > 0 ? (double)a.alpha / ((double)a.topk * tokens * tokens) *
+                                       (a.up ? (double)*a.up : 1.0)
+                                 : 0.0;
+  float b[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+    b[i] = i < n ? (float)((double)((int64_t)a.E * a.counts[e0 + i] - (int64_t)a.topk * tokens) * unit)
+                 : 0.f;
+  for (int64_t r0 = (int64_t)blockIdx.x * RPW; r0 < a.M; r0 += (int64_t)gridDim.x * RPW) {
+    const int64_t row = r0 + tid / LPR;
+    if (row >= a.M) return;  // (all of a row's lanes; no row of this workgroup comes after)
+    const bool in = tokens > 0 && (!a.mask || a.mask[row]);
+    float v[VPL], q[VPL];
+    load_row<BF16, VPL>((const char*)a.logits + row * a.ld * ESZ, e0, in ? n : 0, a.vec, v);
+    float m = kMasked;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      m = fmaxf(m, v[i]);
+      q[i] = a.sigmoid ? 1.f / (1.f + expf(v[i])) : 1.f;
+    }
+    m = group_max<LPR>(m);
+    const float sum = group_sum<LPR>(scores<VPL>(v, m, a.sigmoid));
+    const float inv = m != kMasked ? 1.f / sum : 0.f;
+    float mean = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      v[i] *= inv;
+      mean = fmaf(v[i], b[i], mean);
+    }
+    mean = group_sum<LPR>(mean);
+    char* dst = (char*)a.grad + row * a.ld_grad * ESZ;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) v[i] = v[i] == 0.f ? 0.f : v[i] * q[i] * (b[i] - mean);
+    if (VPL % VE == 0 && a.vec_grad && n == VPL) {
+#pragma unroll
+      for (int i = 0; i < VPL; i += VE) {
+        uint32_t u[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (BF16)
+            u[j] = f32_to_bf16_rne(v[i + 2 * j]) | ((uint32_t)f32_to_bf16_rne(v[i + 2 * j + 1]) << 16);
+          else
+            u[j] = __float_as_uint(v[i + j]);
+        }
+        *reinterpret_cast<uint4*>(dst + (int64_t)(e0 + i) * ESZ) = make_uint4(u[0], u[1], u[2], u[3]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        if (i >= n) continue;
+        if constexpr (BF16) ((uint16_t*)dst)[e0 + i] = f32_to_bf16_rne(v[i]);
+        else ((float*)dst)[e0 + i] = v[i];
+      }
+    }
+  }
+}
+
+template <bool BF16, int LPR, int VPL>
+hipError_t run(const BalanceArgs& a, bool grad, hipStream_t st) {
+  if (grad) {
+    const int64_t rows = kThreads / LPR, want = ((int64_t)a.M + rows - 1) / rows;
+    const int grid = (int)(want < kBalanceGradGroups ? want : kBalanceGradGroups);
+    hipLaunchKernelGGL((balance_grad_kernel<BF16, LPR, VPL>), dim3(grid), dim3(kThreads), 0, st, a);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((balance_kernel<BF16, LPR, VPL>), dim3(a.groups), dim3(kThreads), 0, st, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.groups == 1) return e;
+  hipLaunchKernelGGL(balance_finish_kernel, dim3(a.E / 64 + 1), dim3(kThreads), 0, st, a);
+  return hipGetLastError();
+}
+
+// 16 lanes a row up to 256 experts, else a wave; its lanes hold up to 128 experts.
+template <bool BF16>
+hipError_t dispatch(const BalanceArgs& a, bool grad, hipStream_t st) {
+  if (balance_narrow(a.E)) {
+    if (a.E <= 64) return run<BF16, 16, 4>(a, grad, st);
+    if (a.E <= 128) return run<BF16, 16, 8>(a, grad, st);
+    return run<BF16, 16, 16>(a, grad, st);
+  }
+  if (a.E <= 512) return run<BF16, 64, 8>(a, grad, st);
+  if (a.E <= 1024) return run<BF16, 64, 16>(a, grad, st);
+  if (a.E <= 2048) return run<BF16, 64, 32>(a, grad, st);
+  return run<BF16, 64, 128>(a, grad, st);
+}
+
+}  // namespace
+
+hipError_t launch_balance(const BalanceArgs& a, bool bf16, hipStream_t st) {
+  if (a.M == 0) {
+    hipLaunchKernelGGL(balance_empty_kernel, dim3(1), dim3(kThreads), 0, st, a);
+    return hipGetLastError();
+  }
+  return bf16 ? dispatch<true>(a, false, st) : dispatch<false>(a, false, st);
+}
+
+hipError_t launch_balance_grad(const BalanceArgs& a, bool bf16, hipStream_t st) {
+  return bf16 ? dispatch<true>(a, true, st) : dispatch<false>(a, true, st);
+}
+
+}  // namespace mol

@@ -203,6 +203,106 @@ struct RouterArgs {
 inline bool router_narrow(int32_t E, int32_t topk) { return topk <= 16 && E <= 256; }
 inline int router_rows(int32_t E, int32_t topk) { return router_narrow(E, topk) ? 16 : 4; }
 
+// The balance loss of a routed batch and its gradient.
+struct BalanceArgs {
+  const void* logits;      // [M, E], ld apart
+  int64_t ld;
+  const int32_t* ids;      // [M, topk]
+  const uint8_t* mask;     // [M] (0: the token does not count) or nullptr
+  int32_t M;
+  int32_t E;
+  int32_t topk;
+  bool sigmoid;
+  bool vec;                // rows of logits (of grad) start on 16-byte boundaries
+  bool vec_grad;
+  float alpha;
+  int32_t* counts;         // [E + 1]: the experts, then the tokens that count
+  float* sums;             // [E]
+  float* loss;             // [1]
+  int32_t groups;          // workgroups of the forward pass
+  float* part_sums;        // [groups, E]
+  int32_t* part_counts;    // [groups, E + 1]
+  int32_t* done;           // [1]
+  const float* up;         // gradient: of the loss, or nullptr (1)
+  void* grad;              // [M, E], ld_grad apart
+  int64_t ld_grad;
+};
+
+inline bool balance_narrow(int32_t E) { return E <= 256; }
+constexpr int kBalanceGradGroups = 2048;
+
+// Workgroups of the forward pass: one for up to four turns of its rows, else one for each 16 (narrow
+// rows) or 4, at most 512, and fewer where their partial sums would take more than 4 MiB.
+inline int32_t balance_groups(int64_t M, int32_t E) {
+  const int64_t rows = balance_narrow(E) ? 16 : 4;
+  if (M <= 4 * rows) return 1;
+  const int64_t most = (int64_t(1) << 20) / E < 512 ? (int64_t(1) << 20) / E : 512;
+  const int64_t want = (M + rows - 1) / rows;
+  return (int32_t)(want < most ? want : most);
+}
+
+// Rows to and from microscaled 4-bit floats.
+struct MxArgs {
+  const void* x;           // quantise: rows of K (with the activation 2 K) elements, ld apart
+  void* out;               // dequantise: [rows, K], ld apart
+  int64_t ld;
+  void* q;                 // [rows, K / 2] codes
+  uint8_t* scales;         // [rows, K / 32]
+  int32_t K;
+  int32_t vpr;             // vectors of eight values in a row
+  int32_t vecs;            // and in all rows
+  bool vec;                // rows of x or out start on 16-byte boundaries
+  FastDiv f_vpr;
+};
+constexpr int kMxValues = 32;  // under one scale
+constexpr int64_t kMxMaxVecs = (int64_t(1) << 31) - 4096;
+
+// The base grouped GEMM over microscaled 4-bit weights.
+struct MxGemmArgs {
+  const void* x;           // rows of dtype elements, or of codes
+  int64_t x_bytes;         // from one row of x to the next
+  const uint8_t* x_scales; // of rows of codes
+  int64_t ld_xs;           // from one row of them to the next
+  const uint8_t* W;        // [E, N, K / 2]
+  const uint8_t* scales;   // [E, N, K / 32]
+  int32_t K;
+  int32_t N;
+  int32_t E;
+  int32_t blocks;          // K / 32
+  bool pairs_w;            // scales of two neighbouring blocks are one aligned 16-bit load
+  bool pairs_x;
+  bool vec_out;            // four neighbouring outputs of a row are one aligned store
+  const int32_t* sorted;
+  const int32_t* expert_ids;
+  const int32_t* npp;
+  int32_t numel;
+  int32_t BM;
+  int32_t max_blocks;
+  void* out;               // [numel, ld_out]
+  int64_t ld_out;
+  FastDiv f_rd;
+  FastDiv f_bm;
+  // of the form, set at the launch
+  int32_t span;            // columns of a work item
+  int32_t items;           // work items per routing block: spans times tiles of weight rows
+  FastDiv f_items;
+  FastDiv f_tiles;
+};
+enum { kMxRowsBf16 = 0, kMxRowsF32 = 1, kMxRowsCodes = 2 };  // of x
+
+// The form of the product: 16 columns a pass over 16 weight rows whose k's four waves split, 16
+// columns over 64 rows, or as many columns as the registers hold.
+enum { kMxSplit = 0, kMxNarrow = 1, kMxWide = 2 };
+inline int mx_form(int64_t filled, int64_t pairs, int64_t N) {
+  if (pairs > 16 * filled) return kMxWide;
+  return filled * ((N + 63) / 64) < 384 ? kMxSplit : kMxNarrow;
+}
+// at most this many work items in a routing block of BM pairs
+inline int64_t mx_items(int form, int64_t N, int64_t BM) {
+  const int64_t rows = form == kMxSplit ? 16 : 64;
+  return (N + rows - 1) / rows * (form == kMxWide ? (BM + 31) / 32 : 1);
+}
+
 // The work items of a stream of weight rows: 64 rows times `tiles`, or 16 rows whose k's four waves
 // split. All read the same bytes.
 //  - 16 rows where 64 would make fewer than 384 items for the chip's 256 CUs. Queued calls over 4-bit
@@ -352,5 +452,10 @@ hipError_t launch_moe_layer_q64(const LayerArgs& a, bool bf16, hipStream_t strea
 hipError_t launch_moe_layer_q128(const LayerArgs& a, bool bf16, hipStream_t stream);
 hipError_t launch_moe_layer_direct(const LayerArgs& a, bool bf16, hipStream_t stream);
 hipError_t launch_router(const RouterArgs& a, bool bf16, hipStream_t stream);
+hipError_t launch_balance(const BalanceArgs& a, bool bf16, hipStream_t stream);
+hipError_t launch_balance_grad(const BalanceArgs& a, bool bf16, hipStream_t stream);
+hipError_t launch_mx4_quantize(const MxArgs& a, bool bf16, bool act, hipStream_t stream);
+hipError_t launch_mx4_gemm(const MxGemmArgs& a, bool bf16, int form, hipStream_t stream);
+hipError_t launch_mx4_dequantize(const MxArgs& a, bool bf16, hipStream_t stream);
 
 }  // namespace mol

@@ -1,0 +1,212 @@
+// Rows of numbers to microscaled 4-bit floats and back (mx4.h has the format).
+//
+// Per block of 32 values v, with m = max |v|:
+//   s    = max(floor(log2 m) - 2, -127) + 127      the scale's byte: m / 2^(s - 127) is in [4, 8)
+//   code = v / 2^(s - 127) to the nearest of the fifteen values, halves to the even code, beyond 6 to 6
+// A block that holds a NaN or an infinity gets s = 255 and codes of zero. With the activation, v is
+// SiLU(gate) * up of two halves of a row.
+//
+// The division is by a power of two and the rounding the hardware's, so codes of given values are
+// exact. Those of the activation are the ones of its value in 64 bits: the product is formed in fp32,
+// within 2^-19 of itself, and lanes whose codes or scale would be others 2^-18 to either side form it
+// again in 64 bits (about one lane in a thousand).
+//
+// Bound by bytes. A lane takes eight consecutive values (16 bytes of bf16), four lanes a block; a thread
+// has kVecs such vectors in flight.
+#include "mx4.h"
+#include "skinny.h"
+
+namespace mol {
+namespace {
+
+constexpr int kVecs = 4;                        // vectors of eight values a thread
+constexpr int kChunk = kThreads * kVecs;        // and a workgroup
+
+// Eight elements from a row: wide loads where rows are on 16-byte boundaries.
+template <bool BF16>
+__device__ __forceinline__ void load8(const char* row, int v, bool vec, float (&f)[8]) {
+  constexpr int ESZ = BF16 ? 2 : 4;
+  const char* p = row + (int64_t)v * (8 * ESZ);
+  if (vec) {
+    if constexpr (BF16) {
+      const uint4 w = ld16(p);
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[2 * i] = bf16_lo(u[i]);
+        f[2 * i + 1] = bf16_hi(u[i]);
+      }
+    } else {
+      const uint4 a = ld16(p), b = ld16(p + 16);
+      const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(u[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (BF16) f[i] = __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16);
+      else f[i] = ((const float*)p)[i];
+    }
+  }
+}
+
+// the largest over the four lanes of a block
+__device__ __forceinline__ uint32_t block_max(uint32_t m) {
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xf, 0xf, false));
+  return max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xf, 0xf, false));
+}
+
+// the scale's byte of a block whose largest |v| has these bits
+__device__ __forceinline__ uint32_t scale_of(uint32_t m) {
+  return m >= 0x7f800000u ? kMxNaN : (uint32_t)max((int)(m >> 23) - 2, 0);
+}
+
+// element j of eight, j not known at compile time
+__device__ __forceinline__ float pick(const float (&f)[8], int j) {
+  float v = f[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) v = i == j ? f[i] : v;
+  return v;
+}
+
+// SiLU(g) * u in 64 bits
+__device__ __forceinline__ double silu_mul64(float g, float u) {
+  return (double)g / (1.0 + exp(-(double)g)) * (double)u;
+}
+
+// A value in 64 bits over 2^(s - 127) as a code.
+__device__ __forceinline__ uint32_t encode64(double v, int s) {
+  const double y = ldexp(fabs(v), 127 - s);
+  const uint32_t c = (y > 0.25) + (y >= 0.75) + (y > 1.25) + (y >= 1.75) + (y > 2.5) + (y >= 3.5) + (y > 5.0);
+  return c | (__builtin_signbit(v) ? 8u : 0u);
+}
+
+template <bool BF16, bool ACT>
+__global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(MxArgs a) {
+  constexpr int ESZ = BF16 ? 2 : 4;
+  const int i0 = (int)blockIdx.x * kChunk + (int)threadIdx.x;
+  float f[kVecs][8], g[ACT ? kVecs : 1][8];
+#pragma unroll
+  for (int t = 0; t < kVecs; ++t) {
+    const int i = min(i0 + t * kThreads, a.vecs - 1);  // (a vector of eight values of some row)
+    const int row = fdiv(i, a.f_vpr), v = i - row * a.vpr;
+    const char* src = (const char*)a.x + (int64_t)row * a.ld * ESZ;
+    if constexpr (ACT) {
+      load8<BF16>(src, v, a.vec, g[t]);
+      load8<BF16>(src + (int64_t)a.K * ESZ, v, a.vec, f[t]);
+    } else {
+      load8<BF16>(src, v, a.vec, f[t]);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < kVecs; ++t) {
+    const int i = i0 + t * kThreads;
+    if (i >= a.vecs) break;  // (a block's four lanes go together)
+    float v[8];
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] = ACT ? silu(g[t][j]) * f[t][j] : f[t][j];
+      m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+    }
+    m = block_max(m);
+    uint32_t s = scale_of(m);
+    uint32_t w = mx_encode(v, mx_scale(s));
+    if constexpr (ACT) {
+      constexpr float kLess = 1.f - 0x1p-18f, kMore = 1.f + 0x1p-18f;
+      float lo[8], hi[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        lo[j] = v[j] * kLess;
+        hi[j] = v[j] * kMore;
+      }
+      const float mf = __uint_as_float(m), unit = mx_scale(s);
+      const bool other_scale = s != kMxNaN && scale_of(__float_as_uint(mf * kLess)) !=
+                                                  scale_of(__float_as_uint(mf * kMore));
+      const bool other_code = s != kMxNaN && mx_encode(lo, unit) != mx_encode(hi, unit);
+      if (other_scale) {  // (the same in a block's four lanes)
+        double d = 0.0;
+#pragma unroll 1
+        for (int j = 0; j < 8; ++j) d = fmax(d, fabs(silu_mul64(pick(g[t], j), pick(f[t], j))));
+        d = fmax(d, __shfl_xor(d, 1, 64));
+        d = fmax(d, __shfl_xor(d, 2, 64));
+        s = (uint32_t)max(ilogb(d) + 125, 0);
+      }
+      if (other_scale || other_code) {
+        w = 0;
+#pragma unroll 1
+        for (int j = 0; j < 8; ++j) w |= encode64(silu_mul64(pick(g[t], j), pick(f[t], j)), (int)s) << (4 * j);
+      }
+    }
+    if (s == kMxNaN) w = 0;
+    ((uint32_t*)a.q)[i] = w;
+    if ((threadIdx.x & 3) == 0) a.scales[i >> 2] = (uint8_t)s;
+  }
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads) mx4_dequantize_kernel(MxArgs a) {
+  constexpr int ESZ = BF16 ? 2 : 4;
+  const int i0 = (int)blockIdx.x * kChunk + (int)threadIdx.x;
+  uint32_t w[kVecs], s[kVecs];
+#pragma unroll
+  for (int t = 0; t < kVecs; ++t) {
+    const int i = min(i0 + t * kThreads, a.vecs - 1);
+    w[t] = ((const uint32_t*)a.q)[i];
+    s[t] = a.scales[i >> 2];
+  }
+#pragma unroll
+  for (int t = 0; t < kVecs; ++t) {
+    const int i = i0 + t * kThreads;
+    if (i >= a.vecs) break;
+    const int row = fdiv(i, a.f_vpr), v = i - row * a.vpr;
+    char* dst = (char*)a.out + (int64_t)row * a.ld * ESZ + (int64_t)v * (8 * ESZ);
+    const float unit = mx_scale(s[t]);
+    if constexpr (BF16) {
+      const uint4 b = mx_bf16(w[t], unit);
+      if (a.vec) {
+        *reinterpret_cast<uint4*>(dst) = b;
+      } else {
+        const uint32_t u[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ((uint16_t*)dst)[j] = (uint16_t)(u[j / 2] >> (16 * (j % 2)));
+      }
+    } else {
+      float f[8];
+      mx_f32(w[t], unit, f);
+      if (a.vec) {
+        reinterpret_cast<float4*>(dst)[0] = make_float4(f[0], f[1], f[2], f[3]);
+        reinterpret_cast<float4*>(dst)[1] = make_float4(f[4], f[5], f[6], f[7]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ((float*)dst)[j] = f[j];
+      }
+    }
+  }
+}
+
+int grid_of(const MxArgs& a) { return (int)(((int64_t)a.vecs + kChunk - 1) / kChunk); }
+
+}  // namespace
+
+hipError_t launch_mx4_quantize(const MxArgs& a, bool bf16, bool act, hipStream_t st) {
+  const dim3 grid(grid_of(a)), threads(kThreads);
+  if (bf16) {
+    if (act) hipLaunchKernelGGL((mx4_quantize_kernel<true, true>), grid, threads, 0, st, a);
+    else hipLaunchKernelGGL((mx4_quantize_kernel<true, false>), grid, threads, 0, st, a);
+  } else {
+    if (act) hipLaunchKernelGGL((mx4_quantize_kernel<false, true>), grid, threads, 0, st, a);
+    else hipLaunchKernelGGL((mx4_quantize_kernel<false, false>), grid, threads, 0, st, a);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_mx4_dequantize(const MxArgs& a, bool bf16, hipStream_t st) {
+  const dim3 grid(grid_of(a)), threads(kThreads);
+  if (bf16) hipLaunchKernelGGL((mx4_dequantize_kernel<true>), grid, threads, 0, st, a);
+  else hipLaunchKernelGGL((mx4_dequantize_kernel<false>), grid, threads, 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace mol

@@ -20,40 +20,14 @@
 // for 16384 tokens of 128 (5.2 MB, 0.7 TB/s), bound by issue: all of its 1024 workgroups are resident, and
 // on each selection almost every wave runs the rescan of VPL registers for one lane of 16. Calls queued one
 // after another take 6.6 to 7.1 us at each of these sizes: the host's time for a call.
-#include "delta_common.h"
+#include "router_row.h"
 
 namespace mol {
 namespace {
 
-constexpr float kMasked = -__builtin_inff();
-
-template <int CTRL>
-__device__ __forceinline__ float max_lane(float v) {
-  return fmaxf(v, from_lane<CTRL>(v));
-}
-
-// the maximum over each group of LPR consecutive lanes, in every lane of the group (the
-// butterfly of group_sum)
-template <int LPR>
-__device__ __forceinline__ float group_max(float v) {
-  v = max_lane<0xB1>(v);
-  v = max_lane<0x4E>(v);
-  v = max_lane<0x141>(v);
-  v = max_lane<0x140>(v);
-  if constexpr (LPR >= 64) {
-    v = fmaxf(v, __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(v), 0x401F)));
-    v = fmaxf(v, __shfl_xor(v, 32, 64));
-  }
-  return v;
-}
-
-// exp(l - m) for l <= m; 1 at l == m, infinite m included
-__device__ __forceinline__ float exp_below(float l, float m) { return l == m ? 1.f : expf(l - m); }
-
 template <bool BF16, int LPR, int VPL>
 __global__ void __launch_bounds__(kThreads) router_kernel(RouterArgs a) {
   constexpr int ESZ = BF16 ? 2 : 4;
-  constexpr int VE = 16 / ESZ;
   static_assert(LPR == 16 || LPR == 64, "a row is a lane group of 16 or a wave");
   const int lane = threadIdx.x & 63;
   const int lr = lane % LPR;
@@ -64,43 +38,11 @@ __global__ void __launch_bounds__(kThreads) router_kernel(RouterArgs a) {
   const int n = live ? min(max(a.E - e0, 0), VPL) : 0;  // experts of this lane
 
   float v[VPL];
-  if (VPL % VE == 0 && a.vec) {
-#pragma unroll
-    for (int i = 0; i < VPL; i += VE) {
-      if (i + VE <= n) {
-        const uint4 w = ld16(src + (int64_t)(e0 + i) * ESZ);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int j = 0; j < VE; ++j)
-          v[i + j] = !BF16 ? __uint_as_float(u[j % 4]) : j % 2 ? bf16_hi(u[j / 2]) : bf16_lo(u[j / 2]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < VE; ++j) {
-          float x = kMasked;
-          if (i + j < n) {
-            if constexpr (BF16) x = __uint_as_float((uint32_t)((const uint16_t*)src)[e0 + i + j] << 16);
-            else x = ((const float*)src)[e0 + i + j];
-          }
-          v[i + j] = x;
-        }
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      float x = kMasked;
-      if (i < n) {
-        if constexpr (BF16) x = __uint_as_float((uint32_t)((const uint16_t*)src)[e0 + i] << 16);
-        else x = ((const float*)src)[e0 + i];
-      }
-      v[i] = x;
-    }
-  }
+  load_row<BF16, VPL>(src, e0, n, a.vec, v);
   float bv = kMasked;  // this lane's best remaining logit, at register bi
   int bi = 0;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    if (v[i] != v[i]) v[i] = kMasked;
     if (v[i] > bv) { bv = v[i]; bi = i; }
   }
   const float m = group_max<LPR>(bv);  // -inf: no candidate in the row

@@ -487,8 +487,8 @@ MOL_API mol_status mol_moe_gemm_q4(int32_t dtype, const void *xin, int64_t ld_x,
  *   others        as for mol_moe_gemm (rows of xin on 16-byte boundaries)
  * For decode and prefill batches; blocks of any block_m are taken. Dense blocks run fastest at block_m
  * = 128.
- * Errors: MOL_E_ARG (K not a multiple of 32), MOL_E_LIMIT (one expert's weights 2 GiB or more, 4 GiB or more
- * of x_scales, 2^24 work items or more), others as for mol_moe_gemm.
+ * Errors: MOL_E_ARG (K not a multiple of 32), MOL_E_LIMIT (one expert's weights 2 GiB or more, 2^24
+ * work items or more), others as for mol_moe_gemm.
  * ------------------------------------------------------------------------------- */
 enum { MOL_ACT_NONE = 0, MOL_ACT_SILU_MUL = 1 };
 

@@ -62,7 +62,6 @@ def gemm(**kw):
     (dict(N=2**24, ld_out=2**24), mb.MOL_E_LIMIT),               # one expert's weights: 2 GiB
     (dict(N=2**23, ld_out=2**23, numel=2**20), mb.MOL_E_LIMIT),  # the grid
     (dict(N=2**22, ld_out=2**22, numel=2**14, E=1, block_m=1024), mb.MOL_E_LIMIT),
-    (dict(x_scales=FAKE, ld_x=2**31, numel=2**7, row_div=1), mb.MOL_E_LIMIT),  # 8 GiB of scales of x
     (dict(x=None), mb.MOL_E_ARG), (dict(W=None), mb.MOL_E_ARG), (dict(scales=None), mb.MOL_E_ARG),
     (dict(out=None), mb.MOL_E_ARG), (dict(sorted=None), mb.MOL_E_ARG),
     (dict(expert=None), mb.MOL_E_ARG), (dict(npp=None), mb.MOL_E_ARG),

@@ -872,17 +872,17 @@ MOL_API mol_status mol_moe_gemm_mx4(int32_t dtype, const void* xin, int64_t ld_x
   a.x_bytes = x_scales ? ld_x / 2 : ld_x * esz;
   a.x_scales = x_scales;
   a.ld_xs = ld_x / mol::kMxValues;
-  // (the kernels address the scales of x by 32-bit offsets)
-  if (x_scales && cdiv64(numel, row_div) > ((int64_t(1) << 32) - 1) / a.ld_xs) return MOL_E_LIMIT;
   a.W = W;
   a.scales = scales;
   a.K = K;
   a.N = N;
   a.E = num_experts;
   a.blocks = K / mol::kMxValues;
-  a.pairs_w = a.blocks % 2 == 0 && aligned_to(scales, 2);
-  a.pairs_x = a.blocks % 2 == 0 && a.ld_xs % 2 == 0 && aligned_to(x_scales, 2);
-  a.vec_out = ld_out % 4 == 0 && aligned_to(out, 4 * esz);
+  const int unit = x_scales ? 8 : 4;  // blocks whose scales the kernels take at once
+  a.whole_w = a.blocks % unit == 0 && aligned_to(scales, unit);
+  a.whole_x = a.blocks % unit == 0 && a.ld_xs % unit == 0 && aligned_to(x_scales, unit);
+  a.vec_out = (ld_out * esz) % 16 == 0 && aligned16(out);
+  a.vec8_out = (ld_out * esz) % 8 == 0 && aligned_to(out, 8);
   a.sorted = sorted_ids;
   a.expert_ids = expert_ids;
   a.npp = num_post_padded;

@@ -10,7 +10,7 @@
 // sums that the formula has them in.
 //
 // A work item is a span of columns of a routing block (a pass of the widest form, all of the block's of the
-// narrow ones) and kWaves times 16 FR weight rows; wave w has 16 FR of them as
+// narrow ones) and NW times 16 FR weight rows; wave w has 16 FR of them as
 // the A operand, straight from memory into registers: lane l holds row l % 16 and whole blocks of 32 k's,
 // which block of a step being free as long as x agrees. x goes through LDS for all four waves,
 // as it lies in memory: direct-to-LDS loads, whose lanes choose their 16 bytes of a row so that the
@@ -21,6 +21,8 @@
 // Of the result, lane l holds column (pair) l % 16 and rows 4 (l / 16) + i.
 #pragma once
 
+#include <type_traits>
+
 #include "mx4.h"
 
 namespace mol {
@@ -30,15 +32,14 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
-constexpr int kMxWaves = kThreads / 64;
-
 // What stands for k's past a row's end: x reads these zeros.
 __device__ const uint4 kMxZeros[1] = {{0u, 0u, 0u, 0u}};
 
 // Shape of a kernel. XF: the rows of x; TC columns a pass; FR times 16 weight rows a wave; SU units a
-// stage (and wave); KS: the waves share 16 FR rows and split the units.
-template <int XF, int TC, int FR, int SU, int KS>
+// stage (and wave); NW waves; KS: the waves share 16 FR rows and split the units (KS = NW), or 1.
+template <int XF, int TC, int FR, int SU, int NW, int KS>
 struct MxShape {
+  static constexpr int THREADS = 64 * NW;
   static constexpr int S = XF == kMxRowsCodes ? 2 : 1;  // blocks a lane has of a unit
   static constexpr int UB = 4 * S;                      // blocks of a unit (four quads)
   static constexpr int XB = UB * kMxValues * (XF == kMxRowsCodes ? 1 : XF == kMxRowsBf16 ? 4 : 8) / 2;
@@ -48,12 +49,17 @@ struct MxShape {
   static constexpr int STAGE = SU * KS;                 // units of a stage
   static constexpr int PARTS = TC * XB / 1024;          // direct-to-LDS loads of a unit
   static constexpr int COLS = 64 / CH;                  // columns of one such load
-  static constexpr int NP = PARTS > kMxWaves ? PARTS / kMxWaves : 1;  // a wave's parts
+  static constexpr int NP = PARTS > NW ? PARTS / NW : 1;  // a wave's parts
   static constexpr int BYTES = STAGE * TC * XB;         // of a buffer
-  static constexpr int ROWS = 16 * FR * (KS > 1 ? 1 : kMxWaves);  // of an item
+  static constexpr int ROWS = 16 * FR * (KS > 1 ? 1 : NW);  // of an item
+  // units whose scales are staged at a time: a whole row's up to 2048 k's (1024 beside many rows of bf16 or
+  // fp32, whose stages take the room)
+  static constexpr int XSU = 8 > STAGE || S == 2 ? 8 : STAGE;
+  using Scales = typename std::conditional<UB == 8, uint2, uint32_t>::type;  // of one row's unit
   static_assert(CH >= 8 && CH <= 64 && 64 % CH == 0, "a load covers whole columns");
-  static_assert(PARTS % kMxWaves == 0 || kMxWaves % PARTS == 0, "parts go round the waves");
-  static_assert(STAGE * PARTS % kMxWaves == 0, "every wave has as many loads");
+  static_assert(PARTS % NW == 0 || NW % PARTS == 0, "parts go round the waves");
+  static_assert(STAGE * PARTS % NW == 0, "every wave has as many loads");
+  static_assert(XSU % STAGE == 0, "scales of whole stages");
 };
 
 // The 16-byte place of chunk c of column col: an exclusive or with the column, so that 16 columns'
@@ -63,38 +69,393 @@ __device__ __forceinline__ int mx_place(int c, int col) {
   return CH == 8 ? c ^ ((col >> 1) & 7) : c ^ (col & 15);
 }
 
-template <bool OBF16>
-__device__ __forceinline__ void mx_store(const MxGemmArgs& a, int p, int n, const f32x4_t& v) {
+// v, opaque to the compiler, which would otherwise compute what follows from it ahead of a loop and keep
+// (and spill) it across.
+__device__ __forceinline__ int opaque(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// Direct-to-LDS load of 16 bytes a lane, lane i's to lds_wave_base + 16 i, hidden from the compiler's count
+// of loads in flight: it would wait for the next stage's before it reads this one's. Its arrival is waited
+// for by count (mx_wait).
+__device__ __forceinline__ void mx_dma16(const void* src, const char* lds_wave_base) {
+  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)lds_wave_base;
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+               :
+               : "v"(src), "s"(__builtin_amdgcn_readfirstlane(at))
+               : "memory", "m0");
+}
+// Waits until at most N of this wave's loads are in flight (the last N issued) and its LDS accesses are done.
+template <int N>
+__device__ __forceinline__ void mx_wait() {
+  static_assert(N < 64, "the counter's range");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(N) : "memory");
+}
+
+// V neighbouring outputs of row p from column n on, one store where they are aligned and all there.
+template <bool OBF16, int V>
+__device__ __forceinline__ void mx_store(const MxGemmArgs& a, int p, int n, const uint32_t (&w)[OBF16 ? V / 2 : V]) {
+  constexpr int D = OBF16 ? V / 2 : V;  // dwords: 2 or 4
   const int64_t at = (int64_t)p * a.ld_out + n;
-  if (a.vec_out && n + 4 <= a.N) {
-    if constexpr (OBF16) {
-      uint2 w;
-      w.x = f32_to_bf16_rne(v[0]) | ((uint32_t)f32_to_bf16_rne(v[1]) << 16);
-      w.y = f32_to_bf16_rne(v[2]) | ((uint32_t)f32_to_bf16_rne(v[3]) << 16);
-      *reinterpret_cast<uint2*>((uint16_t*)a.out + at) = w;
-    } else {
-      *reinterpret_cast<float4*>((float*)a.out + at) = make_float4(v[0], v[1], v[2], v[3]);
-    }
+  char* dst = (char*)a.out + at * (OBF16 ? 2 : 4);
+  if ((D == 2 ? a.vec8_out : a.vec_out) && n + V <= a.N) {
+    if constexpr (D == 2) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < V; ++i) {
       if (n + i >= a.N) continue;
-      if constexpr (OBF16) ((uint16_t*)a.out)[at + i] = f32_to_bf16_rne(v[i]);
-      else ((float*)a.out)[at + i] = v[i];
+      if constexpr (OBF16) ((uint16_t*)dst)[i] = (uint16_t)(w[i / 2] >> (16 * (i % 2)));
+      else ((uint32_t*)dst)[i] = w[i];
     }
   }
 }
 
-template <int XF, bool OBF16, int TC, int FR, int SU, int KS>
-__global__ void __launch_bounds__(kThreads, 2) mx4_gemm_kernel(MxGemmArgs a) {
-  using Sh = MxShape<XF, TC, FR, SU, KS>;
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  return f32_to_bf16_rne(lo) | ((uint32_t)f32_to_bf16_rne(hi) << 16);
+}
+
+// A lane's sums of column (pair) p, rows n0 + 16 f + 4 quad + i of tile f, F tiles. bf16 tiles go in twos: the
+// quads exchange halves, so that a lane has eight neighbouring rows, 16 bytes, and four lanes 64.
+template <bool OBF16, int F>
+__device__ __forceinline__ void mx_store_tiles(const MxGemmArgs& a, bool there, int p, int n0, int quad,
+                                               const f32x4_t (&acc)[F]) {
+  if constexpr (OBF16 && F % 2 == 0) {
+#pragma unroll
+    for (int f = 0; f < F; f += 2) {
+      const f32x4_t x = acc[f], y = acc[f + 1];
+      const auto lo = __builtin_amdgcn_permlane16_swap(pack_bf16(x[0], x[1]), pack_bf16(y[0], y[1]), false, false);
+      const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf16(x[2], x[3]), pack_bf16(y[2], y[3]), false, false);
+      const uint32_t w[4] = {lo[0], hi[0], lo[1], hi[1]};
+      const int n = n0 + f * 16 + (quad & 1) * 16 + (quad >> 1) * 8;
+      if (there && n < a.N) mx_store<true, 8>(a, p, n, w);
+    }
+  } else {
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      const int n = n0 + f * 16 + quad * 4;
+      const f32x4_t v = acc[f];
+      if (!there || n >= a.N) continue;
+      if constexpr (OBF16) {
+        const uint32_t w[2] = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+        mx_store<true, 4>(a, p, n, w);
+      } else {
+        const uint32_t w[4] = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+        mx_store<false, 4>(a, p, n, w);
+      }
+    }
+  }
+}
+
+// One pass: the products of an item's weight rows with the ncol real pairs of a block, ncol <= TC.
+template <int XF, bool OBF16, int TC, int FR, int SU, int NW, int KS>
+__device__ __forceinline__ void mx4_pass(const MxGemmArgs& a, char* lds,
+                                         typename MxShape<XF, TC, FR, SU, NW, KS>::Scales* wsc,
+                                         typename MxShape<XF, TC, FR, SU, NW, KS>::Scales* xsc,
+                                         const int* pair, int e, int n0, int ncol) {
+  using Sh = MxShape<XF, TC, FR, SU, NW, KS>;
+  using Scales = typename Sh::Scales;
   constexpr int S = Sh::S, T = Sh::T;
   constexpr bool CODES = XF == kMxRowsCodes;
-  __shared__ __attribute__((aligned(16))) char lds[2 * Sh::BYTES];
-  __shared__ int pair[TC];
+  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 15, quad = lane >> 4;
+  const int units = (a.blocks + Sh::UB - 1) / Sh::UB;
+  const int r0 = n0 + (KS > 1 ? 0 : wv * (16 * FR));
+  const int first = KS > 1 ? wv : 0;  // of this wave's units, which are KS apart
 
-  // the items of the live blocks, a contiguous range for each of the eight XCDs (workgroups go round
-  // them): neighbouring items share an expert's weights and a block's rows in its L2
+  // this lane's weight rows
+  const int64_t wbytes = (int64_t)a.N * (a.K / 2);
+  const __amdgpu_buffer_rsrc_t w_rsrc = expert_rsrc(a.W + e * wbytes, wbytes);
+  uint32_t w_off[FR];
+#pragma unroll
+  for (int f = 0; f < FR; ++f)  // (rows past the last: it again, not stored)
+    w_off[f] = (uint32_t)min(r0 + f * 16 + col, a.N - 1) * (uint32_t)(a.K / 2);
+  // block s of the lane's in unit u
+  auto load_w = [&](int f, int u, int s, int quad) __attribute__((always_inline)) {
+    const int b = u * Sh::UB + quad * S + s;
+    return buf16(w_rsrc, b < a.blocks ? w_off[f] + (uint32_t)b * 16u : kOutOfRange);
+  };
+  // The scales of units [u0, u0 + XSU) of R rows, row r's from row(r) on, zeros (2^-127) past a row's end,
+  // where the codes are zeros; all of a row's unit at once where that is one aligned load.
+  auto stage_scales = [&](Scales* to, int R, int u0, bool whole, auto row) __attribute__((always_inline)) {
+    const int n = min(Sh::XSU, units - u0) * R;
+#pragma unroll 1
+    for (int i = opaque(tid); i < n; i += Sh::THREADS) {
+      const int u = i / R, b = (u0 + u) * Sh::UB;
+      const uint8_t* src = row(i - u * R) + b;
+      if (whole) {
+        to[i] = *reinterpret_cast<const Scales*>(src);
+      } else {
+        uint64_t v = 0;
+#pragma unroll 1
+        for (int k = 0; k < Sh::UB && b + k < a.blocks; ++k) v |= (uint64_t)src[k] << (8 * k);
+        __builtin_memcpy(&to[i], &v, sizeof(Scales));
+      }
+    }
+  };
+
+  // this lane's places of x: its column's row in each of the wave's parts of a unit
+  const char* x_row[Sh::NP];
+#pragma unroll
+  for (int i = 0; i < Sh::NP; ++i) {
+    const int part = (i * NW + wv) % Sh::PARTS;
+    const int c = part * Sh::COLS + lane / Sh::CH;
+    const int p = pair[min(c, ncol - 1)];  // (columns that are not there: the last one again)
+    x_row[i] = (const char*)a.x + (int64_t)fdiv(p, a.f_rd) * a.x_bytes;
+  }
+  const int row_chunks = a.blocks * (Sh::CH / Sh::UB);
+  auto stage_x = [&](int u0, char* buf) __attribute__((always_inline)) {
+    const int ln = opaque(lane);
+#pragma unroll
+    for (int i = 0; i < Sh::STAGE * Sh::PARTS / NW; ++i) {
+      const int id = i * NW + wv, u = id / Sh::PARTS, part = id % Sh::PARTS;
+      if (part * Sh::COLS >= ncol) continue;
+      const int at = (u0 + u) * Sh::CH + mx_place<Sh::CH>(ln % Sh::CH, part * Sh::COLS + ln / Sh::CH);
+      const void* src = at < row_chunks ? (const void*)(x_row[i % Sh::NP] + (int64_t)at * 16)
+                                        : (const void*)kMxZeros;
+      mx_dma16(src, buf + u * (TC * Sh::XB) + part * 1024);
+    }
+  };
+  uint4 w[SU][FR][S];
+  f32x4_t acc[T][FR];
+#pragma unroll
+  for (int t = 0; t < T; ++t)
+#pragma unroll
+    for (int f = 0; f < FR; ++f) acc[t][f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  stage_x(0, lds);
+#pragma unroll
+  for (int i = 0; i < SU; ++i) {
+    const int u = first + i * KS;
+#pragma unroll
+    for (int f = 0; f < FR; ++f) {
+#pragma unroll
+      for (int s = 0; s < S; ++s) w[i][f][s] = load_w(f, u, s, quad);
+    }
+  }
+
+  constexpr int kLoads = SU * FR * S;  // of weights in a stage, all issued after its x
+  int buf = 0;
+  for (int u0 = 0; u0 < units; u0 += Sh::STAGE, buf ^= 1) {
+    if (u0 % Sh::XSU == 0) {  // scales for this stage and those after it
+      if (u0 > 0) __syncthreads();
+      stage_scales(wsc, Sh::ROWS, u0, a.whole_w, [&](int r) {
+        return a.scales + ((int64_t)e * a.N + min(n0 + r, a.N - 1)) * a.blocks;
+      });
+      if constexpr (CODES)
+        stage_scales(xsc, TC, u0, a.whole_x, [&](int c) {
+          return a.x_scales + (int64_t)fdiv(pair[min(c, ncol - 1)], a.f_rd) * a.ld_xs;
+        });
+    }
+    // this wave's part of the stage of x has arrived, then everyone's, and the other buffer is free
+    if (u0 == 0) mx_wait<0>();  // (the stores of an earlier pass count too)
+    else mx_wait<kLoads>();
+    __builtin_amdgcn_s_barrier();
+    if (u0 + Sh::STAGE < units) stage_x(u0 + Sh::STAGE, lds + (buf ^ 1) * Sh::BYTES);
+#pragma unroll
+    for (int i = 0; i < SU; ++i) {
+      const int u = first + i * KS;  // of the stage
+      if (u0 + u >= units) break;
+      const char* xu = lds + buf * Sh::BYTES + u * (TC * Sh::XB);
+      const int us = (u0 + u) % Sh::XSU, next = u0 + u + Sh::STAGE;
+      const int ln = opaque(lane), col = ln & 15, quad = ln >> 4;
+      // chunk c of column t * 16 + col (whose place goes by col alone)
+      auto x_at = [&](int t, int c) __attribute__((always_inline)) {
+        return *reinterpret_cast<const uint4*>(xu + col * Sh::XB + mx_place<Sh::CH>(c, col) * 16 +
+                                               t * (16 * Sh::XB));
+      };
+      // scales of a lane's blocks, one a byte: of weight row f * 16 + col, of column t * 16 + col
+      auto scale_w = [&](int f) __attribute__((always_inline)) {
+        const Scales* p = wsc + us * Sh::ROWS + (r0 - n0) + f * 16 + col;
+        if constexpr (S == 2) return (uint32_t)reinterpret_cast<const uint16_t*>(p)[quad];
+        else return (uint32_t)reinterpret_cast<const uint8_t*>(p)[quad];
+      };
+      auto scale_x = [&](int t) __attribute__((always_inline)) {
+        return (uint32_t)reinterpret_cast<const uint16_t*>(xsc + us * TC + t * 16 + col)[quad];
+      };
+      uint32_t ws[FR];
+#pragma unroll
+      for (int f = 0; f < FR; ++f) ws[f] = scale_w(f);
+      if constexpr (CODES) {
+        // fragments of x are read kAhead steps before their products, and no earlier: left to itself
+        // the compiler reads all of them first and runs out of registers
+        constexpr int Q = S * T, kAhead = T > 1 ? 2 : 1, B = kAhead + 1;
+        uint4 xq[B];
+        uint32_t xsq[B];
+        auto read = [&](int q) __attribute__((always_inline)) {
+          xq[q % B] = x_at(q % T, quad * S + q / T);
+          xsq[q % B] = scale_x(q % T);
+        };
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) read(q);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          const int s = q / T, t = q % T;
+          if (q + kAhead < Q) read(q + kAhead);
+          if (t == 0 || t * 16 < ncol) {
+            const uint4 x = xq[q % B];
+            const i32x8_t xv = {(int)x.x, (int)x.y, (int)x.z, (int)x.w, 0, 0, 0, 0};
+#pragma unroll
+            for (int f = 0; f < FR; ++f) {
+              const uint4 v = w[i][f][s];
+              const i32x8_t wv8 = {(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
+              acc[t][f] = s == 0 ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                                       wv8, xv, acc[t][f], 4, 4, 0, (int)ws[f], 0, (int)xsq[q % B])
+                                 : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                                       wv8, xv, acc[t][f], 4, 4, 1, (int)ws[f], 1, (int)xsq[q % B]);
+            }
+          }
+          if (t == T - 1) {
+#pragma unroll
+            for (int f = 0; f < FR; ++f) w[i][f][s] = load_w(f, next, s, quad);
+          }
+          if constexpr (T > 1) __builtin_amdgcn_sched_barrier(0);
+        }
+      } else {
+        float unit[FR];
+#pragma unroll
+        for (int f = 0; f < FR; ++f) unit[f] = mx_scale(ws[f]);
+        constexpr int H = XF == kMxRowsBf16 ? 1 : 2;  // 16-byte vectors of x beside a dword of codes
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {                 // a dword of codes: eight k's
+          uint4 wb[FR];
+          float wf[FR][8];
+#pragma unroll
+          for (int f = 0; f < FR; ++f) {
+            const uint4 v = w[i][f][0];
+            const uint32_t c = j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
+            if constexpr (XF == kMxRowsBf16) wb[f] = mx_bf16(c, unit[f]);
+            else mx_f32(c, unit[f], wf[f]);
+          }
+#pragma unroll
+          for (int t = 0; t < T; ++t) {
+            uint4 x[H];
+#pragma unroll
+            for (int h = 0; h < H; ++h) x[h] = x_at(t, quad * Sh::LC + j * H + h);
+            if (t > 0 && t * 16 >= ncol) continue;
+            if constexpr (XF == kMxRowsBf16) {
+#pragma unroll
+              for (int f = 0; f < FR; ++f)
+                acc[t][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    __builtin_bit_cast(bf16x8_t, wb[f]), __builtin_bit_cast(bf16x8_t, x[0]), acc[t][f],
+                    0, 0, 0);
+            } else {
+#pragma unroll
+              for (int h = 0; h < H; ++h) {
+                const uint32_t xe[4] = {x[h].x, x[h].y, x[h].z, x[h].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                  for (int f = 0; f < FR; ++f)
+                    acc[t][f] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                        wf[f][h * 4 + k], __uint_as_float(xe[k]), acc[t][f], 0, 0, 0);
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int f = 0; f < FR; ++f) w[i][f][0] = load_w(f, next, 0, quad);
+      }
+    }
+  }
+
+  if constexpr (KS > 1) {  // the waves' sums of one tile
+    __syncthreads();
+    f32x4_t* red = reinterpret_cast<f32x4_t*>(lds);
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+#pragma unroll
+      for (int f = 0; f < FR; ++f) red[((t * FR + f) * NW + wv) * 64 + lane] = acc[t][f];
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+#pragma unroll
+      for (int f = 0; f < FR; ++f) {
+        if ((t * FR + f) % NW != wv) continue;
+        const f32x4_t* r = red + (t * FR + f) * NW * 64 + lane;
+        const f32x4_t v = (r[0] + r[64]) + (r[128] + r[192]);  // (NW = 4)
+        const int c = t * 16 + col;
+        const f32x4_t one[1] = {v};
+        mx_store_tiles<OBF16, 1>(a, c < ncol, pair[c], r0 + f * 16, quad, one);
+      }
+  } else {
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      if (t > 0 && t * 16 >= ncol) break;
+      const int c = t * 16 + col;
+      mx_store_tiles<OBF16, FR>(a, c < ncol, pair[c], r0, quad, acc[t]);
+    }
+  }
+}
+
+// Bytes of LDS: two buffers of x, the scales of the item's rows and of the columns.
+template <int XF, int TC, int FR, int SU, int NW, int KS>
+struct MxLds {
+  using Sh = MxShape<XF, TC, FR, SU, NW, KS>;
+  char x[2 * Sh::BYTES] __attribute__((aligned(16)));
+  typename Sh::Scales ws[Sh::XSU * Sh::ROWS];
+  typename Sh::Scales xs[XF == kMxRowsCodes ? Sh::XSU * TC : 1];
+  int pair[TC];
+};
+
+// The columns of a pass into LDS, p this thread's entry of the block; how many are real pairs, which are
+// a prefix of the block.
+template <int TC>
+__device__ __forceinline__ int put_pairs(int* pair, int p, int numel) {
+  if (threadIdx.x < TC) pair[threadIdx.x] = p;
+  __syncthreads();
+  const int lane = threadIdx.x & 63;
+  int ncol = 0;
+#pragma unroll
+  for (int j = 0; j < TC; j += 64)
+    ncol += __popcll(__builtin_amdgcn_ballot_w64(j + lane < TC && real_pair(pair[min(j + lane, TC - 1)], numel)));
+  return ncol;
+}
+
+// A few columns a block: an item is a block and 64 weight rows (16 with split k's), whose passes of up to
+// TC columns take the buffers in the shape of the columns there are.
+template <int XF, bool OBF16, int TC, int SU, int KS>
+__global__ void __launch_bounds__(256, 4) mx4_narrow_kernel(MxGemmArgs a) {
+  __shared__ MxLds<XF, TC, 1, SU, 4, KS> lds;
+  const int blk = fdiv((int)blockIdx.x, a.f_items);
+  const int n0 = ((int)blockIdx.x - blk * a.items) * (KS > 1 ? 16 : 64);
+  const int32_t* sorted = a.sorted + (int64_t)blk * a.BM;
+  const int tid = threadIdx.x;
+  const int npp = *a.npp;
+  const int er = a.expert_ids[blk];
+  // the first entries with the routing reads (their index stays inside the block)
+  int p = tid < TC && tid < a.BM ? sorted[tid] : a.numel;
+  const int nb = npp < 0 ? 0 : fdiv(npp, a.f_bm);
+  if (blk >= nb || (unsigned)er >= (unsigned)a.E) return;
+  const int e = __builtin_amdgcn_readfirstlane(er);
+  for (int j0 = 0; j0 < a.BM; j0 += TC) {
+    if (j0 > 0) {
+      p = tid < TC && j0 + tid < a.BM ? sorted[j0 + tid] : a.numel;
+      __syncthreads();  // the last pass is done with LDS
+    }
+    const int ncol = put_pairs<TC>(lds.pair, p, a.numel);
+    if (ncol == 0) return;
+    if constexpr (TC > 16) {
+      if (ncol <= 16)
+        mx4_pass<XF, OBF16, 16, 1, SU * (TC / 16), 4, KS>(a, lds.x, lds.ws, lds.xs, lds.pair, e, n0, ncol);
+      else if (TC > 32 && ncol <= 32)
+        mx4_pass<XF, OBF16, 32, 1, SU * (TC / 32), 4, KS>(a, lds.x, lds.ws, lds.xs, lds.pair, e, n0, ncol);
+      else
+        mx4_pass<XF, OBF16, TC, 1, SU, 4, KS>(a, lds.x, lds.ws, lds.xs, lds.pair, e, n0, ncol);
+    } else {
+      mx4_pass<XF, OBF16, TC, 1, SU, 4, KS>(a, lds.x, lds.ws, lds.xs, lds.pair, e, n0, ncol);
+    }
+    if (ncol < TC) return;
+  }
+}
+
+// Many columns a block: an item is a span of TC columns of a block and 16 FR NW weight rows. The
+// items of the live blocks are a contiguous range for each of the eight XCDs (workgroups go round them):
+// neighbouring items share an expert's weights and a block's rows in its L2.
+template <int XF, bool OBF16, int TC, int FR, int SU, int NW>
+__global__ void __launch_bounds__(64 * NW, 4) mx4_wide_kernel(MxGemmArgs a) {
+  using Sh = MxShape<XF, TC, FR, SU, NW, 1>;
+  __shared__ MxLds<XF, TC, FR, SU, NW, 1> lds;
   const int npp = *a.npp;
   const int nb = npp < 0 ? 0 : min(fdiv(npp, a.f_bm), a.max_blocks);
   const int per_xcd = (int)(((int64_t)nb * a.items + 7) >> 3);
@@ -104,276 +465,38 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_gemm_kernel(MxGemmArgs a) {
   if (local >= per_xcd || blk >= nb) return;
   const int er = a.expert_ids[blk];
   if ((unsigned)er >= (unsigned)a.E) return;
-  const int e = __builtin_amdgcn_readfirstlane(er);
   const int in_blk = item - blk * a.items;
-  const int span0 = fdiv(in_blk, a.f_tiles);  // of the block's spans of columns
-  const int n0 = (in_blk - span0 * (int)a.f_tiles.d) * Sh::ROWS;
-
-  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int col = lane & 15, quad = lane >> 4;
-  const int units = (a.blocks + Sh::UB - 1) / Sh::UB;
-  const int r0 = n0 + (KS > 1 ? 0 : wv * (16 * FR));
-  const int first = KS > 1 ? wv : 0;  // of this wave's units, which are KS apart
-
-  // this lane's weight rows and their scales
-  const int64_t wbytes = (int64_t)a.N * (a.K / 2), sbytes = (int64_t)a.N * a.blocks;
-  const __amdgpu_buffer_rsrc_t w_rsrc = expert_rsrc(a.W + e * wbytes, wbytes);
-  const __amdgpu_buffer_rsrc_t s_rsrc = expert_rsrc(a.scales + e * sbytes, sbytes);
-  uint32_t w_off[FR], s_off[FR];
-#pragma unroll
-  for (int f = 0; f < FR; ++f) {
-    const int n = min(r0 + f * 16 + col, a.N - 1);  // (rows past the last: it again, not stored)
-    w_off[f] = (uint32_t)n * (uint32_t)(a.K / 2);
-    s_off[f] = (uint32_t)n * (uint32_t)a.blocks;
-  }
-  // the first of a lane's blocks of unit u
-  auto block_of = [&](int u) __attribute__((always_inline)) { return u * Sh::UB + quad * S; };
-  auto load_w = [&](int f, int u, int s) __attribute__((always_inline)) {
-    const int b = block_of(u) + s;
-    return buf16(w_rsrc, b < a.blocks ? w_off[f] + (uint32_t)b * 16u : kOutOfRange);
-  };
-  // the scales of a lane's blocks of a unit, one a byte; 1 past the row (where the codes are zeros)
-  auto load_ws = [&](int f, int u) __attribute__((always_inline)) {
-    const int b = block_of(u);
-    uint32_t v;
-    if constexpr (S == 2) {
-      if (a.pairs_w) {
-        v = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
-            s_rsrc, b < a.blocks ? s_off[f] + (uint32_t)b : kOutOfRange, 0, 0);
-        return b < a.blocks ? v : 0x7f7fu;
-      }
-      const uint32_t lo = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
-          s_rsrc, b < a.blocks ? s_off[f] + (uint32_t)b : kOutOfRange, 0, 0);
-      const uint32_t hi = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
-          s_rsrc, b + 1 < a.blocks ? s_off[f] + (uint32_t)b + 1u : kOutOfRange, 0, 0);
-      return (b < a.blocks ? lo : 0x7fu) | (b + 1 < a.blocks ? hi : 0x7fu) << 8;
-    } else {
-      v = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
-          s_rsrc, b < a.blocks ? s_off[f] + (uint32_t)b : kOutOfRange, 0, 0);
-      return b < a.blocks ? v : 0x7fu;
-    }
-  };
-
-  const int32_t* sorted = a.sorted + (int64_t)blk * a.BM;
-  const int j_begin = span0 * a.span, j_end = min(a.BM, j_begin + a.span);
-  for (int j0 = j_begin; j0 < j_end; j0 += TC) {
-    if (j0 > j_begin) __syncthreads();  // the last pass is done with pair and LDS
-    for (int j = tid; j < TC; j += kThreads) pair[j] = j0 + j < a.BM ? sorted[j0 + j] : a.numel;
-    __syncthreads();
-    // the real pairs are a prefix of the block
-    int ncol = 0;
-#pragma unroll
-    for (int j = 0; j < TC; j += 64)
-      ncol += __popcll(__builtin_amdgcn_ballot_w64(j + lane < TC && real_pair(pair[min(j + lane, TC - 1)], a.numel)));
-    if (ncol == 0) return;
-
-    // this lane's places of x: its column's row in each of the wave's parts of a unit
-    const char* x_row[Sh::NP];
-    int x_chunk[Sh::NP];
-#pragma unroll
-    for (int i = 0; i < Sh::NP; ++i) {
-      const int part = (i * kMxWaves + wv) % Sh::PARTS;
-      const int c = part * Sh::COLS + lane / Sh::CH;
-      const int p = pair[min(c, ncol - 1)];  // (columns that are not there: the last one again)
-      x_row[i] = (const char*)a.x + (int64_t)fdiv(p, a.f_rd) * a.x_bytes;
-      x_chunk[i] = mx_place<Sh::CH>(lane % Sh::CH, c);
-    }
-    const int row_chunks = a.blocks * (Sh::CH / Sh::UB);
-    auto stage_x = [&](int u0, char* buf) __attribute__((always_inline)) {
-#pragma unroll
-      for (int i = 0; i < Sh::STAGE * Sh::PARTS / kMxWaves; ++i) {
-        const int id = i * kMxWaves + wv, u = id / Sh::PARTS, part = id % Sh::PARTS;
-        if (part * Sh::COLS >= ncol) continue;
-        const int at = (u0 + u) * Sh::CH + x_chunk[i % Sh::NP];
-        const void* src = at < row_chunks ? (const void*)(x_row[i % Sh::NP] + (int64_t)at * 16)
-                                          : (const void*)kMxZeros;
-        lds_dma16(src, buf + u * (TC * Sh::XB) + part * 1024);
-      }
-    };
-    // rows of codes: the scales of column t * 16 + col
-    uint32_t xs_off[CODES ? T : 1];
-    if constexpr (CODES) {
-#pragma unroll
-      for (int t = 0; t < T; ++t)
-        xs_off[t] = (uint32_t)fdiv(pair[min(t * 16 + col, ncol - 1)], a.f_rd) * (uint32_t)a.ld_xs;
-    }
-    auto load_xs = [&](int t, int u) __attribute__((always_inline)) {
-      const int b = block_of(u);
-      const uint8_t* src = a.x_scales + (size_t)(xs_off[CODES ? t : 0] + (uint32_t)min(b, a.blocks - 1));
-      uint32_t v;
-      if (a.pairs_x) {
-        v = *(const uint16_t*)(b < a.blocks ? src : a.x_scales);
-        return b < a.blocks ? v : 0x7f7fu;
-      }
-      const uint32_t lo = src[0], hi = src[b + 1 < a.blocks ? 1 : 0];
-      return (b < a.blocks ? lo : 0x7fu) | (b + 1 < a.blocks ? hi : 0x7fu) << 8;
-    };
-
-    uint4 w[SU][FR][S];
-    uint32_t ws[SU][FR], xs[SU][CODES ? T : 1];
-    f32x4_t acc[T][FR];
-#pragma unroll
-    for (int t = 0; t < T; ++t)
-#pragma unroll
-      for (int f = 0; f < FR; ++f) acc[t][f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    stage_x(0, lds);
-#pragma unroll
-    for (int i = 0; i < SU; ++i) {
-      const int u = first + i * KS;
-#pragma unroll
-      for (int f = 0; f < FR; ++f) {
-#pragma unroll
-        for (int s = 0; s < S; ++s) w[i][f][s] = load_w(f, u, s);
-        ws[i][f] = load_ws(f, u);
-      }
-      if constexpr (CODES) {
-#pragma unroll
-        for (int t = 0; t < T; ++t) xs[i][t] = load_xs(t, u);
-      }
-    }
-
-    int buf = 0;
-    for (int u0 = 0; u0 < units; u0 += Sh::STAGE, buf ^= 1) {
-      __builtin_amdgcn_s_waitcnt(0);  // this wave's part of the stage of x has arrived,
-      __syncthreads();                // everyone's, and the other buffer is no longer read
-      if (u0 + Sh::STAGE < units) stage_x(u0 + Sh::STAGE, lds + (buf ^ 1) * Sh::BYTES);
-#pragma unroll
-      for (int i = 0; i < SU; ++i) {
-        const int u = first + i * KS;  // of the stage
-        if (u0 + u >= units) break;
-        const char* xu = lds + buf * Sh::BYTES + u * (TC * Sh::XB);
-        auto x_at = [&](int t, int c) __attribute__((always_inline)) {  // chunk c of column t * 16 + col
-          const int cc = t * 16 + col;
-          return *reinterpret_cast<const uint4*>(xu + cc * Sh::XB + mx_place<Sh::CH>(c, cc) * 16);
-        };
-        if constexpr (CODES) {
-#pragma unroll
-          for (int s = 0; s < S; ++s) {
-#pragma unroll
-            for (int t = 0; t < T; ++t) {
-              if (t > 0 && t * 16 >= ncol) break;
-              const uint4 x = x_at(t, quad * S + s);
-              const i32x8_t xv = {(int)x.x, (int)x.y, (int)x.z, (int)x.w, 0, 0, 0, 0};
-#pragma unroll
-              for (int f = 0; f < FR; ++f) {
-                const uint4 v = w[i][f][s];
-                const i32x8_t wv8 = {(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
-                acc[t][f] = s == 0 ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                                         wv8, xv, acc[t][f], 4, 4, 0, (int)ws[i][f], 0, (int)xs[i][t])
-                                   : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                                         wv8, xv, acc[t][f], 4, 4, 1, (int)ws[i][f], 1, (int)xs[i][t]);
-              }
-            }
-          }
-        } else {
-          float unit[FR];
-#pragma unroll
-          for (int f = 0; f < FR; ++f) unit[f] = mx_scale(ws[i][f]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {  // a dword of codes: eight k's
-            if constexpr (XF == kMxRowsBf16) {
-              uint4 wb[FR];
-#pragma unroll
-              for (int f = 0; f < FR; ++f) {
-                const uint4 v = w[i][f][0];
-                wb[f] = mx_bf16(j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w, unit[f]);
-              }
-#pragma unroll
-              for (int t = 0; t < T; ++t) {
-                if (t > 0 && t * 16 >= ncol) break;
-                const bf16x8_t x = __builtin_bit_cast(bf16x8_t, x_at(t, quad * Sh::LC + j));
-#pragma unroll
-                for (int f = 0; f < FR; ++f)
-                  acc[t][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                      __builtin_bit_cast(bf16x8_t, wb[f]), x, acc[t][f], 0, 0, 0);
-              }
-            } else {
-              float wf[FR][8];
-#pragma unroll
-              for (int f = 0; f < FR; ++f) {
-                const uint4 v = w[i][f][0];
-                mx_f32(j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w, unit[f], wf[f]);
-              }
-#pragma unroll
-              for (int t = 0; t < T; ++t) {
-                if (t > 0 && t * 16 >= ncol) break;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const uint4 x = x_at(t, quad * Sh::LC + j * 2 + h);
-                  const uint32_t xe[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                  for (int k = 0; k < 4; ++k)
-#pragma unroll
-                    for (int f = 0; f < FR; ++f)
-                      acc[t][f] = __builtin_amdgcn_mfma_f32_16x16x4f32(
-                          wf[f][h * 4 + k], __uint_as_float(xe[k]), acc[t][f], 0, 0, 0);
-                }
-              }
-            }
-          }
-        }
-        const int next = u0 + u + Sh::STAGE;
-#pragma unroll
-        for (int f = 0; f < FR; ++f) {
-#pragma unroll
-          for (int s = 0; s < S; ++s) w[i][f][s] = load_w(f, next, s);
-          ws[i][f] = load_ws(f, next);
-        }
-        if constexpr (CODES) {
-#pragma unroll
-          for (int t = 0; t < T; ++t) xs[i][t] = load_xs(t, next);
-        }
-      }
-    }
-
-    if constexpr (KS > 1) {  // the waves' sums of one tile
-      __syncthreads();
-      f32x4_t* red = reinterpret_cast<f32x4_t*>(lds);
-#pragma unroll
-      for (int t = 0; t < T; ++t)
-#pragma unroll
-        for (int f = 0; f < FR; ++f) red[((t * FR + f) * kMxWaves + wv) * 64 + lane] = acc[t][f];
-      __syncthreads();
-#pragma unroll
-      for (int t = 0; t < T; ++t)
-#pragma unroll
-        for (int f = 0; f < FR; ++f) {
-          if ((t * FR + f) % kMxWaves != wv) continue;
-          const f32x4_t* r = red + (t * FR + f) * kMxWaves * 64 + lane;
-          const f32x4_t v = (r[0] + r[64]) + (r[128] + r[192]);
-          const int c = t * 16 + col;
-          const int n = r0 + f * 16 + quad * 4;
-          if (c < ncol && n < a.N) mx_store<OBF16>(a, pair[c], n, v);
-        }
-    } else {
-#pragma unroll
-      for (int t = 0; t < T; ++t) {
-        const int c = t * 16 + col;
-        if (c >= ncol) continue;
-        const int p = pair[c];
-#pragma unroll
-        for (int f = 0; f < FR; ++f) {
-          const int n = r0 + f * 16 + quad * 4;
-          if (n < a.N) mx_store<OBF16>(a, p, n, acc[t][f]);
-        }
-      }
-    }
-    if (ncol < TC) return;
-  }
+  const int span = fdiv(in_blk, a.f_tiles);  // of the block's spans of columns
+  const int n0 = (in_blk - span * (int)a.f_tiles.d) * Sh::ROWS;
+  const int j = span * TC + (int)threadIdx.x;
+  const int p = threadIdx.x < TC && j < a.BM ? a.sorted[(int64_t)blk * a.BM + j] : a.numel;
+  const int ncol = put_pairs<TC>(lds.pair, p, a.numel);
+  if (ncol == 0) return;
+  mx4_pass<XF, OBF16, TC, FR, SU, NW, 1>(a, lds.x, lds.ws, lds.xs, lds.pair,
+                                         __builtin_amdgcn_readfirstlane(er), n0, ncol);
 }
 
-template <int XF, bool OBF16, int TC, int FR, int SU, int KS>
-hipError_t mx4_launch(MxGemmArgs a, bool wide, hipStream_t st) {
-  using Sh = MxShape<XF, TC, FR, SU, KS>;
-  static_assert(KS == 1 || TC / 16 * FR * kMxWaves * 1024 <= 2 * Sh::BYTES, "room for the waves' sums");
+template <int XF, bool OBF16, int TC, int SU, int KS>
+hipError_t mx4_narrow(MxGemmArgs a, hipStream_t st) {
+  static_assert(KS == 1 || (KS == 4 && 4096 * TC / 16 <= 2 * MxShape<XF, TC, 1, SU, 4, KS>::BYTES),
+                "room for the waves' sums");
+  a.items = (a.N + (KS > 1 ? 15 : 63)) / (KS > 1 ? 16 : 64);
+  a.f_items = make_fastdiv((uint32_t)a.items);
+  hipLaunchKernelGGL((mx4_narrow_kernel<XF, OBF16, TC, SU, KS>), dim3((unsigned)(a.max_blocks * a.items)),
+                     dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
+template <int XF, bool OBF16, int TC, int FR, int SU, int NW>
+hipError_t mx4_wide(MxGemmArgs a, hipStream_t st) {
+  using Sh = MxShape<XF, TC, FR, SU, NW, 1>;
   const int32_t tiles = (a.N + Sh::ROWS - 1) / Sh::ROWS;
   a.f_tiles = make_fastdiv((uint32_t)tiles);
-  a.span = wide ? TC : a.BM;
-  a.items = tiles * ((a.BM + a.span - 1) / a.span);
+  a.items = tiles * ((a.BM + TC - 1) / TC);
   a.f_items = make_fastdiv((uint32_t)a.items);
   // (a range for each XCD, rounded up)
   const int64_t grid = ((int64_t)a.max_blocks * a.items + 7) / 8 * 8;
-  hipLaunchKernelGGL((mx4_gemm_kernel<XF, OBF16, TC, FR, SU, KS>), dim3((unsigned)grid), dim3(kThreads), 0,
+  hipLaunchKernelGGL((mx4_wide_kernel<XF, OBF16, TC, FR, SU, NW>), dim3((unsigned)grid), dim3(64 * NW), 0,
                      st, a);
   return hipGetLastError();
 }

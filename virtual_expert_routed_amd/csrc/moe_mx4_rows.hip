@@ -9,15 +9,15 @@ hipError_t launch_mx4_gemm(const MxGemmArgs& a, bool bf16, int form, hipStream_t
   if (a.x_scales) return launch_mx4_gemm_codes(a, bf16, form, st);
   if (bf16) {
     switch (form) {
-      case kMxSplit: return mx4_launch<kMxRowsBf16, true, 16, 1, 2, 4>(a, false, st);
-      case kMxNarrow: return mx4_launch<kMxRowsBf16, true, 16, 1, 4, 1>(a, false, st);
-      default: return mx4_launch<kMxRowsBf16, true, 128, 4, 1, 1>(a, true, st);
+      case kMxSplit: return mx4_narrow<kMxRowsBf16, true, 16, 2, 4>(a, st);
+      case kMxNarrow: return mx4_narrow<kMxRowsBf16, true, 64, 1, 1>(a, st);
+      default: return mx4_wide<kMxRowsBf16, true, 128, 2, 1, 8>(a, st);
     }
   }
   switch (form) {
-    case kMxSplit: return mx4_launch<kMxRowsF32, false, 16, 1, 1, 4>(a, false, st);
-    case kMxNarrow: return mx4_launch<kMxRowsF32, false, 16, 1, 2, 1>(a, false, st);
-    default: return mx4_launch<kMxRowsF32, false, 32, 1, 1, 1>(a, true, st);
+    case kMxSplit: return mx4_narrow<kMxRowsF32, false, 16, 1, 4>(a, st);
+    case kMxNarrow: return mx4_narrow<kMxRowsF32, false, 32, 1, 1>(a, st);
+    default: return mx4_wide<kMxRowsF32, false, 32, 1, 1, 4>(a, st);
   }
 }
 

@@ -269,9 +269,10 @@ struct MxGemmArgs {
   int32_t N;
   int32_t E;
   int32_t blocks;          // K / 32
-  bool pairs_w;            // scales of two neighbouring blocks are one aligned 16-bit load
-  bool pairs_x;
-  bool vec_out;            // four neighbouring outputs of a row are one aligned store
+  bool whole_w;            // a row's scales of eight (codes) or four blocks from a multiple on: one aligned load
+  bool whole_x;
+  bool vec_out;            // 16 bytes of neighbouring outputs are one aligned store; 8 bytes
+  bool vec8_out;
   const int32_t* sorted;
   const int32_t* expert_ids;
   const int32_t* npp;
@@ -283,7 +284,6 @@ struct MxGemmArgs {
   FastDiv f_rd;
   FastDiv f_bm;
   // of the form, set at the launch
-  int32_t span;            // columns of a work item
   int32_t items;           // work items per routing block: spans times tiles of weight rows
   FastDiv f_items;
   FastDiv f_tiles;

@@ -398,8 +398,8 @@ MOL_API mol_status mol_router_topk(int32_t dtype, const void *logits, int64_t ld
  *   prob_sums     float32 [num_experts] out: P_e;   loss  float32 [1] out
  *   workspace     device scratch of mol_router_balance_workspace_bytes(), 16-byte aligned (NULL when
  *                 that is 0); needs no initial contents. Calls that may overlap must not share it.
- * Results do not depend on timing: bit-for-bit reproducible. M = 0 writes zeros. Sums are fp32 in parts
- * of at most M / 512 + 1 tokens, joined in 64 bits.
+ * Bit-for-bit reproducible: no sum depends on timing. M = 0 writes zeros. A workgroup's sums are fp32, the
+ * sums over workgroups are formed in 64 bits.
  *
  * mol_router_balance_grad - grad_logits [M, ld_grad] (dtype) out, every element of [M, num_experts]:
  *   counts        int32 [num_experts + 1] of mol_router_balance, or their sums over the ranks that
@@ -474,7 +474,7 @@ MOL_API mol_status mol_moe_gemm_q4(int32_t dtype, const void *xin, int64_t ld_x,
  * mol_mx4_dequantize - the values of codes and scales, x [rows, ld_x] (dtype) out: exact in both dtypes
  *   up to s = 252, infinite where they pass fp32's range beyond.
  * rows = 0 enqueues nothing. Errors: MOL_E_ARG, MOL_E_DTYPE, MOL_E_ALIGN, MOL_E_LIMIT (rows * K / 8
- * past 2^31 - 4096).
+ * past 2^30 - 4096).
  *
  * mol_moe_gemm_mx4 - mol_moe_gemm's base product over such weights:
  *   out[p, n] = round( sum_k W[t, n, k] * xin[p / row_div, k] )

@@ -20,7 +20,7 @@ def quantize(**kw):
     (dict(act=2), mb.MOL_E_ARG), (dict(act=-1), mb.MOL_E_ARG),
     (dict(rows=-1), mb.MOL_E_ARG), (dict(K=0), mb.MOL_E_ARG), (dict(K=-32), mb.MOL_E_ARG), (dict(K=48), mb.MOL_E_ARG),
     (dict(ld=63), mb.MOL_E_ARG), (dict(act=1), mb.MOL_E_ARG), (dict(act=1, ld=127), mb.MOL_E_ARG),
-    (dict(rows=2**31), mb.MOL_E_LIMIT), (dict(rows=2**62), mb.MOL_E_LIMIT), (dict(rows=2**28 - 511), mb.MOL_E_LIMIT),
+    (dict(rows=2**31), mb.MOL_E_LIMIT), (dict(rows=2**62), mb.MOL_E_LIMIT), (dict(rows=2**27 - 511), mb.MOL_E_LIMIT),
     (dict(x=None), mb.MOL_E_ARG), (dict(q=None), mb.MOL_E_ARG), (dict(scales=None), mb.MOL_E_ARG),
     (dict(x=FAKE + 1), mb.MOL_E_ALIGN), (dict(dtype=0, x=FAKE + 2), mb.MOL_E_ALIGN), (dict(q=FAKE + 8), mb.MOL_E_ALIGN),
     (dict(rows=0, x=None, q=None, scales=None), mb.MOL_OK),
@@ -122,7 +122,7 @@ def test_balance_workspace_bytes():
     f = mb.lib().mol_router_balance_workspace_bytes
     assert f(0, 8) == 0 and f(16, 128) == 0
     for E in (1, 100, 257, 8191):
-        sizes = [f(m, E) for m in (0, 1, 16, 17, 64, 65, 300, 5000, 2**20, 2**31 - 1)]
+        sizes = [f(m, E) for m in (0, 1, 16, 17, 64, 65, 300, 1023, 1024, 1025, 1100, 5000, 2**20, 2**31 - 1)]
         assert sizes == sorted(sizes)  # a workspace for M tokens serves fewer
         assert 0 < sizes[-1] < 9 << 20
     assert f(-1, 8) == -mb.MOL_E_ARG and f(1, 0) == -mb.MOL_E_ARG and f(1, 8192) == -mb.MOL_E_LIMIT

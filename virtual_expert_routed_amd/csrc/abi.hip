@@ -907,8 +907,7 @@ namespace {
 struct BalanceWorkspace {
   int64_t counts, done, bytes;  // offsets (the sums come first), and the whole
 };
-BalanceWorkspace balance_workspace(int64_t M, int32_t E) {
-  const int64_t groups = mol::balance_groups(M, E);
+BalanceWorkspace balance_workspace(int64_t groups, int32_t E) {
   BalanceWorkspace w{};
   if (groups == 1) return w;
   w.counts = round256(groups * E * 4);
@@ -947,7 +946,7 @@ mol::BalanceArgs balance_args(const void* logits, int64_t ld, const uint8_t* mas
 MOL_API int64_t mol_router_balance_workspace_bytes(int32_t M, int32_t num_experts) {
   if (M < 0 || num_experts < 1) return -MOL_E_ARG;
   if ((int64_t)num_experts + 1 > MOL_MAX_BUCKETS) return -MOL_E_LIMIT;
-  return balance_workspace(M, num_experts).bytes;
+  return balance_workspace(mol::balance_groups_up_to(M, num_experts), num_experts).bytes;
 }
 
 MOL_API mol_status mol_router_balance(int32_t dtype, const void* logits, int64_t ld_logits,
@@ -962,7 +961,8 @@ MOL_API mol_status mol_router_balance(int32_t dtype, const void* logits, int64_t
   if (!aligned_to(logits, esz) || !aligned_to(topk_ids, 4) || !aligned_to(counts, 4) ||
       !aligned_to(prob_sums, 4) || !aligned_to(loss, 4))
     return MOL_E_ALIGN;
-  const BalanceWorkspace ws = balance_workspace(M, num_experts);
+  const int32_t groups = mol::balance_groups(M, num_experts);
+  const BalanceWorkspace ws = balance_workspace(groups, num_experts);
   if (ws.bytes && (!workspace || workspace_bytes < (size_t)ws.bytes)) return MOL_E_WORKSPACE;
   if (ws.bytes && !aligned16(workspace)) return MOL_E_ALIGN;
   mol::BalanceArgs a =
@@ -971,7 +971,7 @@ MOL_API mol_status mol_router_balance(int32_t dtype, const void* logits, int64_t
   a.counts = counts;
   a.sums = prob_sums;
   a.loss = loss;
-  a.groups = mol::balance_groups(M, num_experts);
+  a.groups = groups;
   if (ws.bytes) {
     char* base = static_cast<char*>(workspace);
     a.part_sums = reinterpret_cast<float*>(base);

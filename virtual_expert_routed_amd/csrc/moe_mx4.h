@@ -112,10 +112,6 @@ __device__ __forceinline__ void mx_store(const MxGemmArgs& a, int p, int n, cons
   }
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  return f32_to_bf16_rne(lo) | ((uint32_t)f32_to_bf16_rne(hi) << 16);
-}
-
 // A lane's sums of column (pair) p, rows n0 + 16 f + 4 quad + i of tile f, F tiles. bf16 tiles go in twos: the
 // quads exchange halves, so that a lane has eight neighbouring rows, 16 bytes, and four lanes 64.
 template <bool OBF16, int F>
@@ -125,8 +121,8 @@ __device__ __forceinline__ void mx_store_tiles(const MxGemmArgs& a, bool there, 
 #pragma unroll
     for (int f = 0; f < F; f += 2) {
       const f32x4_t x = acc[f], y = acc[f + 1];
-      const auto lo = __builtin_amdgcn_permlane16_swap(pack_bf16(x[0], x[1]), pack_bf16(y[0], y[1]), false, false);
-      const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf16(x[2], x[3]), pack_bf16(y[2], y[3]), false, false);
+      const auto lo = __builtin_amdgcn_permlane16_swap(bf16_pair(x[0], x[1]), bf16_pair(y[0], y[1]), false, false);
+      const auto hi = __builtin_amdgcn_permlane16_swap(bf16_pair(x[2], x[3]), bf16_pair(y[2], y[3]), false, false);
       const uint32_t w[4] = {lo[0], hi[0], lo[1], hi[1]};
       const int n = n0 + f * 16 + (quad & 1) * 16 + (quad >> 1) * 8;
       if (there && n < a.N) mx_store<true, 8>(a, p, n, w);
@@ -138,7 +134,7 @@ __device__ __forceinline__ void mx_store_tiles(const MxGemmArgs& a, bool there, 
       const f32x4_t v = acc[f];
       if (!there || n >= a.N) continue;
       if constexpr (OBF16) {
-        const uint32_t w[2] = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+        const uint32_t w[2] = {bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
         mx_store<true, 4>(a, p, n, w);
       } else {
         const uint32_t w[4] = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};

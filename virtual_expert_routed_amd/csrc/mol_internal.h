@@ -228,17 +228,24 @@ struct BalanceArgs {
   int64_t ld_grad;
 };
 
-inline bool balance_narrow(int32_t E) { return E <= 256; }
+// Rows of 16 lanes, four a wave, instead of a wave each.
+inline bool balance_narrow(int64_t M, int32_t E) { return E <= 256 && M > 1024; }
 constexpr int kBalanceGradGroups = 2048;
 
-// Workgroups of the forward pass: one for up to four turns of its rows, else one for each 16 (narrow
-// rows) or 4, at most 512, and fewer where their partial sums would take more than 4 MiB.
+// Workgroups of the forward pass: one for up to four turns of its rows, else one for each turn, at most
+// 512, and fewer where their partial sums would take more than 4 MiB.
+constexpr int kBalanceGroups = 512;
 inline int32_t balance_groups(int64_t M, int32_t E) {
-  const int64_t rows = balance_narrow(E) ? 16 : 4;
+  const int64_t rows = balance_narrow(M, E) ? 16 : 4;
   if (M <= 4 * rows) return 1;
-  const int64_t most = (int64_t(1) << 20) / E < 512 ? (int64_t(1) << 20) / E : 512;
+  const int64_t most = (int64_t(1) << 20) / E < kBalanceGroups ? (int64_t(1) << 20) / E : kBalanceGroups;
   const int64_t want = (M + rows - 1) / rows;
   return (int32_t)(want < most ? want : most);
+}
+// the most for any number of tokens up to M (the smallest rows take the most workgroups)
+inline int32_t balance_groups_up_to(int64_t M, int32_t E) {
+  const int32_t at = balance_groups(M, E), before = balance_groups(M < 1024 ? M : 1024, E);
+  return at > before ? at : before;
 }
 
 // Rows to and from microscaled 4-bit floats.
@@ -255,7 +262,7 @@ struct MxArgs {
   FastDiv f_vpr;
 };
 constexpr int kMxValues = 32;  // under one scale
-constexpr int64_t kMxMaxVecs = (int64_t(1) << 31) - 4096;
+constexpr int64_t kMxMaxVecs = (int64_t(1) << 30) - 4096;  // (fp32 counts them in fours)
 
 // The base grouped GEMM over microscaled 4-bit weights.
 struct MxGemmArgs {
@@ -456,6 +463,6 @@ hipError_t launch_balance(const BalanceArgs& a, bool bf16, hipStream_t stream);
 hipError_t launch_balance_grad(const BalanceArgs& a, bool bf16, hipStream_t stream);
 hipError_t launch_mx4_quantize(const MxArgs& a, bool bf16, bool act, hipStream_t stream);
 hipError_t launch_mx4_gemm(const MxGemmArgs& a, bool bf16, int form, hipStream_t stream);
-hipError_t launch_mx4_dequantize(const MxArgs& a, bool bf16, hipStream_t stream);
+hipError_t launch_mx4_dequantize(MxArgs a, bool bf16, hipStream_t stream);
 
 }  // namespace mol

@@ -62,14 +62,6 @@ __device__ __forceinline__ uint32_t scale_of(uint32_t m) {
   return m >= 0x7f800000u ? kMxNaN : (uint32_t)max((int)(m >> 23) - 2, 0);
 }
 
-// element j of eight, j not known at compile time
-__device__ __forceinline__ float pick(const float (&f)[8], int j) {
-  float v = f[0];
-#pragma unroll
-  for (int i = 1; i < 8; ++i) v = i == j ? f[i] : v;
-  return v;
-}
-
 // SiLU(g) * u in 64 bits
 __device__ __forceinline__ double silu_mul64(float g, float u) {
   return (double)g / (1.0 + exp(-(double)g)) * (double)u;
@@ -80,6 +72,32 @@ __device__ __forceinline__ uint32_t encode64(double v, int s) {
   const double y = ldexp(fabs(v), 127 - s);
   const uint32_t c = (y > 0.25) + (y >= 0.75) + (y > 1.25) + (y >= 1.75) + (y > 2.5) + (y >= 3.5) + (y > 5.0);
   return c | (__builtin_signbit(v) ? 8u : 0u);
+}
+
+// The codes of vector i once more, from values in 64 bits, and the scale if `scale` (then in a block's four
+// lanes together). Reads its values again: kept, they would take registers from every lane.
+template <bool BF16>
+__device__ __forceinline__ void codes64(const MxArgs& a, int i, bool scale, uint32_t& w, uint32_t& s) {
+  const int row = fdiv(i, a.f_vpr), k0 = (i - row * a.vpr) * 8;
+  auto value = [&](int j) {
+    const int64_t at = (int64_t)row * a.ld + k0 + j;
+    if constexpr (BF16)
+      return silu_mul64(__uint_as_float((uint32_t)((const uint16_t*)a.x)[at] << 16),
+                        __uint_as_float((uint32_t)((const uint16_t*)a.x)[at + a.K] << 16));
+    else
+      return silu_mul64(((const float*)a.x)[at], ((const float*)a.x)[at + a.K]);
+  };
+  if (scale) {
+    double d = 0.0;
+#pragma unroll 1
+    for (int j = 0; j < 8; ++j) d = fmax(d, fabs(value(j)));
+    d = fmax(d, __shfl_xor(d, 1, 64));
+    d = fmax(d, __shfl_xor(d, 2, 64));
+    s = (uint32_t)max(ilogb(d) + 125, 0);
+  }
+  w = 0;
+#pragma unroll 1
+  for (int j = 0; j < 8; ++j) w |= encode64(value(j), (int)s) << (4 * j);
 }
 
 template <bool BF16, bool ACT>
@@ -124,20 +142,8 @@ __global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(MxArgs a) {
       const float mf = __uint_as_float(m), unit = mx_scale(s);
       const bool other_scale = s != kMxNaN && scale_of(__float_as_uint(mf * kLess)) !=
                                                   scale_of(__float_as_uint(mf * kMore));
-      const bool other_code = s != kMxNaN && mx_encode(lo, unit) != mx_encode(hi, unit);
-      if (other_scale) {  // (the same in a block's four lanes)
-        double d = 0.0;
-#pragma unroll 1
-        for (int j = 0; j < 8; ++j) d = fmax(d, fabs(silu_mul64(pick(g[t], j), pick(f[t], j))));
-        d = fmax(d, __shfl_xor(d, 1, 64));
-        d = fmax(d, __shfl_xor(d, 2, 64));
-        s = (uint32_t)max(ilogb(d) + 125, 0);
-      }
-      if (other_scale || other_code) {
-        w = 0;
-#pragma unroll 1
-        for (int j = 0; j < 8; ++j) w |= encode64(silu_mul64(pick(g[t], j), pick(f[t], j)), (int)s) << (4 * j);
-      }
+      if (other_scale || (s != kMxNaN && mx_encode(lo, unit) != mx_encode(hi, unit)))
+        codes64<BF16>(a, i, other_scale, w, s);
     }
     if (s == kMxNaN) w = 0;
     ((uint32_t*)a.q)[i] = w;
@@ -145,42 +151,41 @@ __global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(MxArgs a) {
   }
 }
 
+// A lane writes 16 bytes, so that a wave's are neighbours: eight values in bf16, four in fp32.
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads) mx4_dequantize_kernel(MxArgs a) {
-  constexpr int ESZ = BF16 ? 2 : 4;
+  constexpr int V = BF16 ? 8 : 4;  // values a lane
   const int i0 = (int)blockIdx.x * kChunk + (int)threadIdx.x;
   uint32_t w[kVecs], s[kVecs];
 #pragma unroll
   for (int t = 0; t < kVecs; ++t) {
     const int i = min(i0 + t * kThreads, a.vecs - 1);
-    w[t] = ((const uint32_t*)a.q)[i];
-    s[t] = a.scales[i >> 2];
+    w[t] = BF16 ? ((const uint32_t*)a.q)[i] : ((const uint16_t*)a.q)[i];
+    s[t] = a.scales[i / (kMxValues / V)];
   }
 #pragma unroll
   for (int t = 0; t < kVecs; ++t) {
     const int i = i0 + t * kThreads;
     if (i >= a.vecs) break;
     const int row = fdiv(i, a.f_vpr), v = i - row * a.vpr;
-    char* dst = (char*)a.out + (int64_t)row * a.ld * ESZ + (int64_t)v * (8 * ESZ);
+    char* dst = (char*)a.out + (int64_t)row * a.ld * (16 / V) + (int64_t)v * 16;
     const float unit = mx_scale(s[t]);
+    uint4 b;
     if constexpr (BF16) {
-      const uint4 b = mx_bf16(w[t], unit);
-      if (a.vec) {
-        *reinterpret_cast<uint4*>(dst) = b;
-      } else {
-        const uint32_t u[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ((uint16_t*)dst)[j] = (uint16_t)(u[j / 2] >> (16 * (j % 2)));
-      }
+      b = mx_bf16(w[t], unit);
     } else {
-      float f[8];
-      mx_f32(w[t], unit, f);
-      if (a.vec) {
-        reinterpret_cast<float4*>(dst)[0] = make_float4(f[0], f[1], f[2], f[3]);
-        reinterpret_cast<float4*>(dst)[1] = make_float4(f[4], f[5], f[6], f[7]);
-      } else {
+      const f32x2_t x = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[t], unit, 0);
+      const f32x2_t y = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[t], unit, 1);
+      b = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x), __float_as_uint(y.y));
+    }
+    if (a.vec) {
+      *reinterpret_cast<uint4*>(dst) = b;
+    } else {
+      const uint32_t u[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ((float*)dst)[j] = f[j];
+      for (int j = 0; j < V; ++j) {
+        if constexpr (BF16) ((uint16_t*)dst)[j] = (uint16_t)(u[j / 2] >> (16 * (j % 2)));
+        else ((uint32_t*)dst)[j] = u[j];
       }
     }
   }
@@ -202,7 +207,12 @@ hipError_t launch_mx4_quantize(const MxArgs& a, bool bf16, bool act, hipStream_t
   return hipGetLastError();
 }
 
-hipError_t launch_mx4_dequantize(const MxArgs& a, bool bf16, hipStream_t st) {
+hipError_t launch_mx4_dequantize(MxArgs a, bool bf16, hipStream_t st) {
+  if (!bf16) {  // vectors of four
+    a.vpr *= 2;
+    a.vecs *= 2;
+    a.f_vpr = make_fastdiv((uint32_t)a.vpr);
+  }
   const dim3 grid(grid_of(a)), threads(kThreads);
   if (bf16) hipLaunchKernelGGL((mx4_dequantize_kernel<true>), grid, threads, 0, st, a);
   else hipLaunchKernelGGL((mx4_dequantize_kernel<false>), grid, threads, 0, st, a);

@@ -84,7 +84,7 @@ __device__ __forceinline__ void mx_dma16(const void* src, const char* lds_wave_b
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
                :
                : "v"(src), "s"(__builtin_amdgcn_readfirstlane(at))
-               : "memory", "m0");
+               : "memory");
 }
 // Waits until at most N of this wave's loads are in flight (the last N issued) and its LDS accesses are done.
 template <int N>
@@ -101,7 +101,7 @@ __device__ __forceinline__ void mx_store(const MxGemmArgs& a, int p, int n, cons
   char* dst = (char*)a.out + at * (OBF16 ? 2 : 4);
   if ((D == 2 ? a.vec8_out : a.vec_out) && n + V <= a.N) {
     if constexpr (D == 2) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-    else *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    else st16_nt(dst, make_uint4(w[0], w[1], w[2], w[3]));
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -144,12 +144,19 @@ __device__ __forceinline__ void mx_store_tiles(const MxGemmArgs& a, bool there, 
   }
 }
 
+// The columns of a pass in LDS: pairs, and the first bytes of their rows of x (row 0's for those that are not there).
+template <int TC>
+struct MxCols {
+  int64_t row[TC];
+  int pair[TC];
+};
+
 // One pass: the products of an item's weight rows with the ncol real pairs of a block, ncol <= TC.
-template <int XF, bool OBF16, int TC, int FR, int SU, int NW, int KS>
+template <int XF, bool OBF16, int TC, int FR, int SU, int NW, int KS, int TCL>
 __device__ __forceinline__ void mx4_pass(const MxGemmArgs& a, char* lds,
                                          typename MxShape<XF, TC, FR, SU, NW, KS>::Scales* wsc,
                                          typename MxShape<XF, TC, FR, SU, NW, KS>::Scales* xsc,
-                                         const int* pair, int e, int n0, int ncol) {
+                                         const MxCols<TCL>& cols, int e, int n0, int ncol) {
   using Sh = MxShape<XF, TC, FR, SU, NW, KS>;
   using Scales = typename Sh::Scales;
   constexpr int S = Sh::S, T = Sh::T;
@@ -191,15 +198,6 @@ __device__ __forceinline__ void mx4_pass(const MxGemmArgs& a, char* lds,
     }
   };
 
-  // this lane's places of x: its column's row in each of the wave's parts of a unit
-  const char* x_row[Sh::NP];
-#pragma unroll
-  for (int i = 0; i < Sh::NP; ++i) {
-    const int part = (i * NW + wv) % Sh::PARTS;
-    const int c = part * Sh::COLS + lane / Sh::CH;
-    const int p = pair[min(c, ncol - 1)];  // (columns that are not there: the last one again)
-    x_row[i] = (const char*)a.x + (int64_t)fdiv(p, a.f_rd) * a.x_bytes;
-  }
   const int row_chunks = a.blocks * (Sh::CH / Sh::UB);
   auto stage_x = [&](int u0, char* buf) __attribute__((always_inline)) {
     const int ln = opaque(lane);
@@ -207,8 +205,9 @@ __device__ __forceinline__ void mx4_pass(const MxGemmArgs& a, char* lds,
     for (int i = 0; i < Sh::STAGE * Sh::PARTS / NW; ++i) {
       const int id = i * NW + wv, u = id / Sh::PARTS, part = id % Sh::PARTS;
       if (part * Sh::COLS >= ncol) continue;
-      const int at = (u0 + u) * Sh::CH + mx_place<Sh::CH>(ln % Sh::CH, part * Sh::COLS + ln / Sh::CH);
-      const void* src = at < row_chunks ? (const void*)(x_row[i % Sh::NP] + (int64_t)at * 16)
+      const int c = part * Sh::COLS + ln / Sh::CH;  // a lane's column, and its chunk of the row
+      const int at = (u0 + u) * Sh::CH + mx_place<Sh::CH>(ln % Sh::CH, c);
+      const void* src = at < row_chunks ? (const void*)((const char*)a.x + cols.row[c] + (int64_t)at * 16)
                                         : (const void*)kMxZeros;
       mx_dma16(src, buf + u * (TC * Sh::XB) + part * 1024);
     }
@@ -240,7 +239,7 @@ __device__ __forceinline__ void mx4_pass(const MxGemmArgs& a, char* lds,
       });
       if constexpr (CODES)
         stage_scales(xsc, TC, u0, a.whole_x, [&](int c) {
-          return a.x_scales + (int64_t)fdiv(pair[min(c, ncol - 1)], a.f_rd) * a.ld_xs;
+          return a.x_scales + (int64_t)fdiv(cols.pair[min(c, ncol - 1)], a.f_rd) * a.ld_xs;
         });
     }
     // this wave's part of the stage of x has arrived, then everyone's, and the other buffer is free
@@ -372,14 +371,14 @@ __device__ __forceinline__ void mx4_pass(const MxGemmArgs& a, char* lds,
         const f32x4_t v = (r[0] + r[64]) + (r[128] + r[192]);  // (NW = 4)
         const int c = t * 16 + col;
         const f32x4_t one[1] = {v};
-        mx_store_tiles<OBF16, 1>(a, c < ncol, pair[c], r0 + f * 16, quad, one);
+        mx_store_tiles<OBF16, 1>(a, c < ncol, cols.pair[c], r0 + f * 16, quad, one);
       }
   } else {
 #pragma unroll
     for (int t = 0; t < T; ++t) {
       if (t > 0 && t * 16 >= ncol) break;
       const int c = t * 16 + col;
-      mx_store_tiles<OBF16, FR>(a, c < ncol, pair[c], r0, quad, acc[t]);
+      mx_store_tiles<OBF16, FR>(a, c < ncol, cols.pair[c], r0, quad, acc[t]);
     }
   }
 }
@@ -391,20 +390,23 @@ struct MxLds {
   char x[2 * Sh::BYTES] __attribute__((aligned(16)));
   typename Sh::Scales ws[Sh::XSU * Sh::ROWS];
   typename Sh::Scales xs[XF == kMxRowsCodes ? Sh::XSU * TC : 1];
-  int pair[TC];
+  MxCols<TC> cols;
 };
 
 // The columns of a pass into LDS, p this thread's entry of the block; how many are real pairs, which are
 // a prefix of the block.
 template <int TC>
-__device__ __forceinline__ int put_pairs(int* pair, int p, int numel) {
-  if (threadIdx.x < TC) pair[threadIdx.x] = p;
+__device__ __forceinline__ int put_pairs(MxCols<TC>& cols, int p, const MxGemmArgs& a) {
+  if (threadIdx.x < TC) {
+    cols.pair[threadIdx.x] = p;
+    cols.row[threadIdx.x] = real_pair(p, a.numel) ? (int64_t)fdiv(p, a.f_rd) * a.x_bytes : 0;
+  }
   __syncthreads();
   const int lane = threadIdx.x & 63;
   int ncol = 0;
 #pragma unroll
   for (int j = 0; j < TC; j += 64)
-    ncol += __popcll(__builtin_amdgcn_ballot_w64(j + lane < TC && real_pair(pair[min(j + lane, TC - 1)], numel)));
+    ncol += __popcll(__builtin_amdgcn_ballot_w64(j + lane < TC && real_pair(cols.pair[min(j + lane, TC - 1)], a.numel)));
   return ncol;
 }
 
@@ -429,17 +431,17 @@ __global__ void __launch_bounds__(256, 4) mx4_narrow_kernel(MxGemmArgs a) {
       p = tid < TC && j0 + tid < a.BM ? sorted[j0 + tid] : a.numel;
       __syncthreads();  // the last pass is done with LDS
     }
-    const int ncol = put_pairs<TC>(lds.pair, p, a.numel);
+    const int ncol = put_pairs<TC>(lds.cols, p, a);
     if (ncol == 0) return;
     if constexpr (TC > 16) {
       if (ncol <= 16)
-        mx4_pass<XF, OBF16, 16, 1, SU * (TC / 16), 4, KS>(a, lds.x, lds.ws, lds.xs, lds.pair, e, n0, ncol);
+        mx4_pass<XF, OBF16, 16, 1, SU * (TC / 16), 4, KS>(a, lds.x, lds.ws, lds.xs, lds.cols, e, n0, ncol);
       else if (TC > 32 && ncol <= 32)
-        mx4_pass<XF, OBF16, 32, 1, SU * (TC / 32), 4, KS>(a, lds.x, lds.ws, lds.xs, lds.pair, e, n0, ncol);
+        mx4_pass<XF, OBF16, 32, 1, SU * (TC / 32), 4, KS>(a, lds.x, lds.ws, lds.xs, lds.cols, e, n0, ncol);
       else
-        mx4_pass<XF, OBF16, TC, 1, SU, 4, KS>(a, lds.x, lds.ws, lds.xs, lds.pair, e, n0, ncol);
+        mx4_pass<XF, OBF16, TC, 1, SU, 4, KS>(a, lds.x, lds.ws, lds.xs, lds.cols, e, n0, ncol);
     } else {
-      mx4_pass<XF, OBF16, TC, 1, SU, 4, KS>(a, lds.x, lds.ws, lds.xs, lds.pair, e, n0, ncol);
+      mx4_pass<XF, OBF16, TC, 1, SU, 4, KS>(a, lds.x, lds.ws, lds.xs, lds.cols, e, n0, ncol);
     }
     if (ncol < TC) return;
   }
@@ -466,9 +468,9 @@ __global__ void __launch_bounds__(64 * NW, 4) mx4_wide_kernel(MxGemmArgs a) {
   const int n0 = (in_blk - span * (int)a.f_tiles.d) * Sh::ROWS;
   const int j = span * TC + (int)threadIdx.x;
   const int p = threadIdx.x < TC && j < a.BM ? a.sorted[(int64_t)blk * a.BM + j] : a.numel;
-  const int ncol = put_pairs<TC>(lds.pair, p, a.numel);
+  const int ncol = put_pairs<TC>(lds.cols, p, a);
   if (ncol == 0) return;
-  mx4_pass<XF, OBF16, TC, FR, SU, NW, 1>(a, lds.x, lds.ws, lds.xs, lds.pair,
+  mx4_pass<XF, OBF16, TC, FR, SU, NW, 1>(a, lds.x, lds.ws, lds.xs, lds.cols,
                                          __builtin_amdgcn_readfirstlane(er), n0, ncol);
 }
 

@@ -291,7 +291,8 @@ struct MxGemmArgs {
   FastDiv f_rd;
   FastDiv f_bm;
   // of the form, set at the launch
-  int32_t items;           // work items per routing block: spans times tiles of weight rows
+  int32_t items;           // work items per routing block: spans times tiles (runs of tiles) of weight rows
+  int32_t run;             // tiles of a run
   FastDiv f_items;
   FastDiv f_tiles;
 };
@@ -299,7 +300,7 @@ enum { kMxRowsBf16 = 0, kMxRowsF32 = 1, kMxRowsCodes = 2 };  // of x
 
 // The form of the product: 16 columns a pass over 16 weight rows whose k's four waves split, 16
 // columns over 64 rows, or as many columns as the registers hold.
-enum { kMxSplit = 0, kMxNarrow = 1, kMxWide = 2 };
+enum { kMxSplit = 0, kMxNarrow = 1, kMxWide = 2, kMxTiles = 3 };
 inline int mx_form(int64_t filled, int64_t pairs, int64_t N) {
   if (pairs > 16 * filled) return kMxWide;
   return filled * ((N + 63) / 64) < 384 ? kMxSplit : kMxNarrow;
@@ -307,7 +308,7 @@ inline int mx_form(int64_t filled, int64_t pairs, int64_t N) {
 // at most this many work items in a routing block of BM pairs
 inline int64_t mx_items(int form, int64_t N, int64_t BM) {
   const int64_t rows = form == kMxSplit ? 16 : 64;
-  return (N + rows - 1) / rows * (form == kMxWide ? (BM + 31) / 32 : 1);
+  return (N + rows - 1) / rows * (form >= kMxWide ? (BM + 31) / 32 : 1);
 }
 
 // The work items of a stream of weight rows: 64 rows times `tiles`, or 16 rows whose k's four waves

@@ -398,6 +398,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _call(dev, fn: str, *args) -> None:
     """The entry point on dev's current stream, with dev current for the launch."""
     if dev.type != "cuda":
@@ -405,11 +408,12 @@ def _call(dev, fn: str, *args) -> None:
     f = _fns.get(fn)
     if f is None:
         f = _fns[fn] = getattr(lib(), fn)
-    if dev.index == torch.cuda.current_device():
-        status = f(*args, _raw_stream(dev.index))
+    index = dev.index
+    if index == _device():
+        status = f(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            status = f(*args, _raw_stream(dev.index))
+            status = f(*args, _raw_stream(index))
     if status != MOL_OK:
         raise MolError(fn, status)
 
@@ -586,38 +590,44 @@ def mol_router_balance_grad(logits, counts, topk: int, scoring: int = MOL_SCORE_
 
 def _as_rows(t: torch.Tensor, name: str):
     """(rows, width, row stride) of a tensor of one row dimension or more, the last dimension contiguous."""
+    if t.dim() == 2:
+        (rows, width), (ld, step) = t.shape, t.stride()
+        if step != 1 and width > 1:
+            raise ValueError(f"{name} must have contiguous rows")
+        return rows, width, ld if rows > 1 else max(ld, width)
     if t.dim() < 2:
         raise ValueError(f"{name} must have rows: at least 2 dimensions")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, or 2-d with contiguous rows")
     width = t.shape[-1]
-    if t.dim() > 2 or t.is_contiguous():
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous, or 2-d with contiguous rows")
-        return t.numel() // width if width else 0, width, width
-    if t.stride(1) != 1 and width > 1:
-        raise ValueError(f"{name} must have contiguous rows")
-    rows = t.shape[0]
-    return rows, width, t.stride(0) if rows > 1 else max(t.stride(0), width)
+    return t.numel() // width if width else 0, width, width
 
 
 def mol_mx4_quantize(x, activation: int = MOL_ACT_NONE, q=None, scales=None):
     """Rows [..., K] of bf16 or fp32 (strided rows if 2-d) as MX4: (q uint8 [..., K/2], scales uint8
     [..., K/32]). MOL_ACT_SILU_MUL: rows [..., 2 K], gate columns first, as SiLU(gate) * up."""
     rows, width, ld = _as_rows(x, "x")
-    if activation not in (MOL_ACT_NONE, MOL_ACT_SILU_MUL):
+    if activation == MOL_ACT_NONE:
+        K = width
+    elif activation == MOL_ACT_SILU_MUL:
+        K = width // 2
+    else:
         raise ValueError(f"unknown activation {activation}")
-    K = width // 2 if activation == MOL_ACT_SILU_MUL else width
-    if K < 1 or K % 32 or (activation == MOL_ACT_SILU_MUL and width % 2):
+    if K < 1 or K % 32 or (K != width and width % 2):
         raise ValueError(f"rows of {width} are not whole blocks of 32 values")
-    _fit("mol_mx4_quantize", K)
-    dev, lead = x.device, x.shape[:-1]
+    if K > 0x7fffffff:
+        raise ValueError(f"mol_mx4_quantize: {K} does not fit 32 bits")
+    dev = x.device
+    lead = (rows,) if x.dim() == 2 else x.shape[:-1]
+    codes_shape, scales_shape = (*lead, K // 2), (*lead, K // 32)
     if q is None:
-        q = torch.empty((*lead, K // 2), dtype=torch.uint8, device=dev)
+        q = torch.empty(codes_shape, dtype=torch.uint8, device=dev)
     else:
-        _on(dev, "q", q, torch.uint8, (*lead, K // 2))
+        _on(dev, "q", q, torch.uint8, codes_shape)
     if scales is None:
-        scales = torch.empty((*lead, K // 32), dtype=torch.uint8, device=dev)
+        scales = torch.empty(scales_shape, dtype=torch.uint8, device=dev)
     else:
-        _on(dev, "scales", scales, torch.uint8, (*lead, K // 32))
+        _on(dev, "scales", scales, torch.uint8, scales_shape)
     _call(dev, "mol_mx4_quantize", _dtype_code(x), activation, x.data_ptr(), ld, rows, K, q.data_ptr(),
           scales.data_ptr())
     return q, scales
@@ -626,14 +636,15 @@ def mol_mx4_quantize(x, activation: int = MOL_ACT_NONE, q=None, scales=None):
 def mol_mx4_dequantize(q, scales, dtype=torch.bfloat16, out=None):
     """The values [..., K] of MX4 codes q uint8 [..., K/2] and scales uint8 [..., K/32], in dtype (that of
     out, whose rows may be strided if 2-d)."""
-    dev = q.device
-    if q.dim() < 2:
+    dev, shape = q.device, q.shape
+    if len(shape) < 2:
         raise ValueError("q must have rows: at least 2 dimensions")
-    lead, K = q.shape[:-1], 2 * q.shape[-1]
+    lead, K = shape[:-1], 2 * shape[-1]
     if K < 1 or K % 32:
         raise ValueError(f"rows of {K} are not whole blocks of 32 values")
-    _fit("mol_mx4_dequantize", K)
-    _on(dev, "q", q, torch.uint8, q.shape)
+    if K > 0x7fffffff:
+        raise ValueError(f"mol_mx4_dequantize: {K} does not fit 32 bits")
+    _on(dev, "q", q, torch.uint8, shape)
     _on(dev, "scales", scales, torch.uint8, (*lead, K // 32))
     if out is None:
         out = torch.empty((*lead, K), dtype=dtype, device=dev)

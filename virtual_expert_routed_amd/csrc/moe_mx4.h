@@ -52,9 +52,8 @@ struct MxShape {
   static constexpr int NP = PARTS > NW ? PARTS / NW : 1;  // a wave's parts
   static constexpr int BYTES = STAGE * TC * XB;         // of a buffer
   static constexpr int ROWS = 16 * FR * (KS > 1 ? 1 : NW);  // of an item
-  // units whose scales are staged at a time: a whole row's up to 2048 k's (1024 beside many rows of bf16 or
-  // fp32, whose stages take the room)
-  static constexpr int XSU = 8 > STAGE || S == 2 ? 8 : STAGE;
+  // units whose scales are staged at a time: those of 2048 k's (1024 beside bf16 or fp32 rows)
+  static constexpr int XSU = 8;
   using Scales = typename std::conditional<UB == 8, uint2, uint32_t>::type;  // of one row's unit
   static_assert(CH >= 8 && CH <= 64 && 64 % CH == 0, "a load covers whole columns");
   static_assert(PARTS % NW == 0 || NW % PARTS == 0, "parts go round the waves");
@@ -433,15 +432,16 @@ __global__ void __launch_bounds__(256, 4) mx4_narrow_kernel(MxGemmArgs a) {
     }
     const int ncol = put_pairs<TC>(lds.cols, p, a);
     if (ncol == 0) return;
+    auto pass = [&](auto tc) __attribute__((always_inline)) {
+      constexpr int C = decltype(tc)::value;
+      mx4_pass<XF, OBF16, C, 1, SU * (TC / C), 4, KS>(a, lds.x, lds.ws, lds.xs, lds.cols, e, n0, ncol);
+    };
     if constexpr (TC > 16) {
-      if (ncol <= 16)
-        mx4_pass<XF, OBF16, 16, 1, SU * (TC / 16), 4, KS>(a, lds.x, lds.ws, lds.xs, lds.cols, e, n0, ncol);
-      else if (TC > 32 && ncol <= 32)
-        mx4_pass<XF, OBF16, 32, 1, SU * (TC / 32), 4, KS>(a, lds.x, lds.ws, lds.xs, lds.cols, e, n0, ncol);
-      else
-        mx4_pass<XF, OBF16, TC, 1, SU, 4, KS>(a, lds.x, lds.ws, lds.xs, lds.cols, e, n0, ncol);
+      if (ncol <= 16) pass(std::integral_constant<int, 16>{});
+      else if (TC > 32 && ncol <= 32) pass(std::integral_constant<int, 32>{});
+      else pass(std::integral_constant<int, TC>{});
     } else {
-      mx4_pass<XF, OBF16, TC, 1, SU, 4, KS>(a, lds.x, lds.ws, lds.xs, lds.cols, e, n0, ncol);
+      pass(std::integral_constant<int, TC>{});
     }
     if (ncol < TC) return;
   }

@@ -298,17 +298,19 @@ struct MxGemmArgs {
 };
 enum { kMxRowsBf16 = 0, kMxRowsF32 = 1, kMxRowsCodes = 2 };  // of x
 
-// The form of the product: 16 columns a pass over 16 weight rows whose k's four waves split, 16
-// columns over 64 rows, or as many columns as the registers hold.
-enum { kMxSplit = 0, kMxNarrow = 1, kMxWide = 2, kMxTiles = 3 };
-inline int mx_form(int64_t filled, int64_t pairs, int64_t N) {
-  if (pairs > 16 * filled) return kMxWide;
-  return filled * ((N + 63) / 64) < 384 ? kMxSplit : kMxNarrow;
+// The form of the product: passes of 32 columns over 16 weight rows whose k's four waves split (fp32 rows), passes
+// of up to 64 columns (fp32 rows 32) over 64 rows, or spans of 128 columns over 256 rows (fp32 rows 32 over 64).
+enum { kMxSplit = 0, kMxNarrow = 1, kMxWide = 2 };
+inline int mx_form(int64_t filled, int64_t pairs, int64_t N, int64_t BM, int rows) {
+  if (pairs > 32 * filled &&
+      (rows == kMxRowsF32 || filled * ((BM + 127) / 128) * ((N + 255) / 256) >= 200))
+    return kMxWide;
+  return rows == kMxRowsF32 && filled * ((N + 63) / 64) < 256 ? kMxSplit : kMxNarrow;
 }
 // at most this many work items in a routing block of BM pairs
 inline int64_t mx_items(int form, int64_t N, int64_t BM) {
   const int64_t rows = form == kMxSplit ? 16 : 64;
-  return (N + rows - 1) / rows * (form >= kMxWide ? (BM + 31) / 32 : 1);
+  return (N + rows - 1) / rows * (form == kMxWide ? (BM + 31) / 32 : 1);
 }
 
 // The work items of a stream of weight rows: 64 rows times `tiles`, or 16 rows whose k's four waves

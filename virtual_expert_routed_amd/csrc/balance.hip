@@ -64,24 +64,31 @@ __device__ __forceinline__ float loss_of(double cp, int n, const BalanceArgs& a)
   return (float)((double)a.alpha * a.E * cp / ((double)a.topk * n * n));
 }
 
-// sum over the workgroup's threads, in a fixed order, in thread 0
+// sum over the workgroup's waves, in a fixed order, in thread 0
+template <int WAVES>
 __device__ __forceinline__ double block_sum(double v, double* lds) {
   for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d, 64);
   if ((threadIdx.x & 63) == 0) lds[wave_id()] = v;
   __syncthreads();
-  return threadIdx.x == 0 ? (lds[0] + lds[1]) + (lds[2] + lds[3]) : 0.0;
+  v = 0.0;
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) v += lds[i];
+  }
+  return v;
 }
 
 template <bool BF16, int LPR, int VPL>
-__global__ void __launch_bounds__(kThreads) balance_kernel(BalanceArgs a) {
+__global__ void __launch_bounds__(VPL <= 16 ? 1024 : 256) balance_kernel(BalanceArgs a) {
   constexpr int ESZ = BF16 ? 2 : 4;
-  constexpr int RPW = kThreads / LPR;   // rows at a time
+  constexpr int NT = VPL <= 16 ? 1024 : 256;  // balance_threads()
+  constexpr int RPW = NT / LPR;         // rows at a time
   constexpr int W = LPR * VPL;          // experts of the registers, at least E
   __shared__ float part[W];
   __shared__ int hist[W + 1];           // counts, then the tokens that count
-  __shared__ double red[kThreads / 64];
+  __shared__ double red[NT / 64];
   const int tid = threadIdx.x, lane = tid & 63, lr = lane % LPR;
-  for (int e = tid; e <= W; e += kThreads) hist[e] = 0;
+  for (int e = tid; e <= W; e += NT) hist[e] = 0;
   __syncthreads();
   const int e0 = lr * VPL, n = min(max(a.E - e0, 0), VPL);
   float acc[VPL];
@@ -126,7 +133,7 @@ __global__ void __launch_bounds__(kThreads) balance_kernel(BalanceArgs a) {
       acc[i] += __shfl_xor(acc[i], 32, 64);
     }
   }
-  for (int w = 0; w < kThreads / 64; ++w) {
+  for (int w = 0; w < NT / 64; ++w) {
     if (w == wave_id() && lane < LPR) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) part[e0 + i] = w ? part[e0 + i] + acc[i] : acc[i];
@@ -137,7 +144,7 @@ __global__ void __launch_bounds__(kThreads) balance_kernel(BalanceArgs a) {
   float* sums = alone ? a.sums : a.part_sums + (int64_t)blockIdx.x * a.E;
   int* counts = alone ? a.counts : a.part_counts + (int64_t)blockIdx.x * (a.E + 1);
   double cp = 0.0;
-  for (int e = tid; e < a.E; e += kThreads) {
+  for (int e = tid; e < a.E; e += NT) {
     const float p = part[e];
     sums[e] = p;
     counts[e] = hist[e];
@@ -145,7 +152,7 @@ __global__ void __launch_bounds__(kThreads) balance_kernel(BalanceArgs a) {
   }
   if (tid == 0) counts[a.E] = hist[W];
   if (alone) {
-    cp = block_sum(cp, red);
+    cp = block_sum<NT / 64>(cp, red);
     if (tid == 0) *a.loss = loss_of(cp, hist[W], a);
   } else if (blockIdx.x == 0 && tid == 0) {
     *a.done = 0;
@@ -207,7 +214,7 @@ __global__ void __launch_bounds__(kThreads) balance_finish_kernel(BalanceArgs a)
   for (int i = tid; i < a.E; i += kThreads)
     cp += (double)__hip_atomic_load(&a.counts[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) *
           __hip_atomic_load(&a.sums[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  cp = block_sum(cp, red);
+  cp = block_sum<kThreads / 64>(cp, red);
   if (tid == 0)
     *a.loss = loss_of(cp, __hip_atomic_load(&a.counts[a.E], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT), a);
 }
@@ -292,7 +299,7 @@ hipError_t run(const BalanceArgs& a, bool grad, hipStream_t st) {
     hipLaunchKernelGGL((balance_grad_kernel<BF16, LPR, VPL>), dim3(grid), dim3(kThreads), 0, st, a);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL((balance_kernel<BF16, LPR, VPL>), dim3(a.groups), dim3(kThreads), 0, st, a);
+  hipLaunchKernelGGL((balance_kernel<BF16, LPR, VPL>), dim3(a.groups), dim3(VPL <= 16 ? 1024 : 256), 0, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.groups == 1) return e;
   hipLaunchKernelGGL(balance_finish_kernel, dim3(a.E / 8 + 1), dim3(kThreads), 0, st, a);

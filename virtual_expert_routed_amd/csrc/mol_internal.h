@@ -230,13 +230,18 @@ struct BalanceArgs {
 
 // Rows of 16 lanes, four a wave, instead of a wave each.
 inline bool balance_narrow(int64_t M, int32_t E) { return E <= 256 && M > 1024; }
-constexpr int kBalanceGradGroups = 2048;
 
-// Workgroups of the forward pass: one for up to four turns of its rows, else one for each turn, at most
-// 512, and fewer where their partial sums would take more than 4 MiB.
-constexpr int kBalanceGroups = 512;
+// Threads of a workgroup of the forward pass (a lane holds the scores of up to 16 experts, or of 32 and 128),
+// and the rows that it takes at a time.
+inline int balance_threads(int32_t E) { return E <= 1024 ? 1024 : 256; }
+inline int64_t balance_rows(int64_t M, int32_t E) { return balance_threads(E) / (balance_narrow(M, E) ? 16 : 64); }
+
+// Workgroups of the forward pass: one for up to four turns of its rows, which needs no second launch (a turn takes
+// 1.5 us, the second launch 5); else one for each turn, at most 256, and fewer where their partial sums would take more than 4 MiB.
+constexpr int kBalanceGroups = 256;
+constexpr int kBalanceGradGroups = 2048;
 inline int32_t balance_groups(int64_t M, int32_t E) {
-  const int64_t rows = balance_narrow(M, E) ? 16 : 4;
+  const int64_t rows = balance_rows(M, E);
   if (M <= 4 * rows) return 1;
   const int64_t most = (int64_t(1) << 20) / E < kBalanceGroups ? (int64_t(1) << 20) / E : kBalanceGroups;
   const int64_t want = (M + rows - 1) / rows;

@@ -62,6 +62,22 @@ __device__ __forceinline__ uint32_t scale_of(uint32_t m) {
   return m >= 0x7f800000u ? kMxNaN : (uint32_t)max((int)(m >> 23) - 2, 0);
 }
 
+// v = SiLU(g) * u within 2^-19 of itself. Up to |g| = 32 the hardware's exp2 and reciprocal do: the exponent's argument
+// is rounded at 46 (2^-19.5 in all).
+__device__ __forceinline__ void silu_mul8(const float (&g)[8], const float (&u)[8], float (&v)[8]) {
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(g[j]));
+  if (m < 32.f) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      v[j] = g[j] * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(g[j] * -1.44269502f)) * u[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = silu(g[j]) * u[j];
+  }
+}
+
 // SiLU(g) * u in 64 bits
 __device__ __forceinline__ double silu_mul64(float g, float u) {
   return (double)g / (1.0 + exp(-(double)g)) * (double)u;
@@ -122,16 +138,19 @@ __global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(MxArgs a) {
     const int i = i0 + t * kThreads;
     if (i >= a.vecs) break;  // (a block's four lanes go together)
     float v[8];
+    if constexpr (ACT) silu_mul8(g[t], f[t], v);
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      v[j] = ACT ? silu(g[t][j]) * f[t][j] : f[t][j];
+      if constexpr (!ACT) v[j] = f[t][j];
       m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
     }
     m = block_max(m);
     uint32_t s = scale_of(m);
-    uint32_t w = mx_encode(v, mx_scale(s));
-    if constexpr (ACT) {
+    uint32_t w;
+    if constexpr (!ACT) {
+      w = mx_encode(v, mx_scale(s));
+    } else {
       constexpr float kLess = 1.f - 0x1p-18f, kMore = 1.f + 0x1p-18f;
       float lo[8], hi[8];
 #pragma unroll
@@ -142,7 +161,8 @@ __global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(MxArgs a) {
       const float mf = __uint_as_float(m), unit = mx_scale(s);
       const bool other_scale = s != kMxNaN && scale_of(__float_as_uint(mf * kLess)) !=
                                                   scale_of(__float_as_uint(mf * kMore));
-      if (other_scale || (s != kMxNaN && mx_encode(lo, unit) != mx_encode(hi, unit)))
+      w = mx_encode(lo, unit);  // (the same as v's, or formed again)
+      if (other_scale || (s != kMxNaN && w != mx_encode(hi, unit)))
         codes64<BF16>(a, i, other_scale, w, s);
     }
     if (s == kMxNaN) w = 0;
@@ -179,7 +199,7 @@ __global__ void __launch_bounds__(kThreads) mx4_dequantize_kernel(MxArgs a) {
       b = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x), __float_as_uint(y.y));
     }
     if (a.vec) {
-      *reinterpret_cast<uint4*>(dst) = b;
+      st16_nt(dst, b);
     } else {
       const uint32_t u[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll

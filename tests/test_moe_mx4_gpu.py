@@ -6,6 +6,7 @@ the output type of the value."""
 import pytest
 import torch
 
+from tests import mx4_cases as mc
 from tests import mx4_defs as d
 from virtual_expert_routed_amd import binding as mb
 
@@ -87,6 +88,14 @@ def test_few_pairs(x, dtype, M, E, topk, K, N, per_pair):
 def test_many_pairs(x, dtype, M, E, topk, K, N, block):
     Case(M, E, topk, K, N, x, dtype, block=block, skew=True).check()
     Case(M, E, topk, K, N, x, dtype, block=block, per_pair=True, seed=1).check()
+
+
+@pytest.mark.parametrize("x,M,E,topk,K,N,block,form", mc.FORMS)
+@pytest.mark.parametrize("per_pair", [False, True])
+def test_every_form(x, M, E, topk, K, N, block, form, per_pair):
+    for dtype in (torch.bfloat16, torch.float32) if x == "codes" else ({"bf16": torch.bfloat16, "f32": torch.float32}[x],):
+        Case(M, E, topk, K, N, "codes" if x == "codes" else "rows", dtype, block=block, per_pair=per_pair,
+             pad_out=8 if per_pair else 0).check()
 
 
 @FORMS
@@ -243,3 +252,53 @@ def test_weights_past_32_bits():
             ref, mag = w @ xv[p], w.abs() @ xv[p].abs()
             assert bool(((out[p, rows].double() - ref).abs() <= (K + 1) * 2.0 ** -24 * mag * 2 + 2.0 ** -8 * ref.abs()).all())
             assert int((out[p] != 0).sum()) <= 5
+
+
+@FORMS
+def test_wide_form_of_strided_rows_with_nan_and_infinity(x, dtype):
+    """The widest form: rows of x and of out apart from each other, NaN blocks of weights and rows, infinite rows, and
+    a graph's replay."""
+    c = Case(1000, 2, 1, 224, 6401, x, dtype, block=128, pad_out=7)
+    c.s[0, 3, 6], c.s[1, 0, 0], c.s[1, 6400, 2] = 255, 255, 255
+    c.s[0, 20], c.s[1, 21] = 0, 200
+    if c.xs is None:
+        wide = torch.full((1000, 224 + 24), float("nan"), dtype=dtype, device="cuda")
+        wide[:, 8:232] = c.x
+        c.x = wide[:, 8:232]
+        c.x[3, 5], c.x[4, 223], c.x[5, 100] = float("inf"), -float("inf"), float("nan")
+        xv = c.x.double()
+    else:
+        wide, ws = (torch.full((1000, n), 255, dtype=torch.uint8, device="cuda") for n in (160, 10))
+        wide[:, 16:128], ws[:, 2:9] = c.x, c.xs
+        c.x, c.xs = wide[:, 16:128], ws[:, 2:9]
+        c.xs[2, 1], c.xs[3], c.xs[4] = 255, 20, 160
+        xv = value(c.x.contiguous(), c.xs.contiguous())
+    wv = value(c.W.view(-1, 112), c.s.view(-1, 7)).view(2, 6401, 224)
+    first = c.run().clone()
+    flat = c.ids.reshape(-1)
+    for e in range(2):
+        p = (flat == e).nonzero().reshape(-1)
+        odd = ~xv[p].isfinite().all(dim=1)
+        for q in p[odd].tolist():  # term by term: a product of matrices may meet infinities in another order
+            ref = (wv[e] * xv[q]).sum(dim=1)
+            assert torch.equal(first[q].isnan(), ref.isnan()) and torch.equal(first[q].isinf(), ref.isinf())
+            assert torch.equal(first[q].double()[ref.isinf()], ref[ref.isinf()])
+        p = p[~odd]
+        w0 = torch.nan_to_num(wv[e])
+        ref, mag = xv[p] @ w0.t(), xv[p].abs() @ w0.abs().t()
+        nan = wv[e].isnan().any(dim=1)
+        got = first[p].double()
+        assert bool(got[:, nan].isnan().all())
+        tiny = 225 * 2.0 ** -149 + torch.finfo(dtype).smallest_normal * HALF[dtype] * 2
+        err = (got - ref).abs() - (225 * 2.0 ** -24 * mag * (1 + HALF[dtype]) + HALF[dtype] * ref.abs() + tiny)
+        assert bool((err[:, ~nan] <= 0).all())
+    assert bool((first[(flat < 0) | (flat >= 2)] == 7.0).all())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.run()
+    for _ in range(3):
+        c.out.fill_(7.0)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(c.out.nan_to_num(123.0), first.nan_to_num(123.0))

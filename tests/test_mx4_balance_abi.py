@@ -61,7 +61,8 @@ def gemm(**kw):
     (dict(E=8192), mb.MOL_E_LIMIT), (dict(block_m=1025), mb.MOL_E_LIMIT),
     (dict(N=2**24, ld_out=2**24), mb.MOL_E_LIMIT),               # one expert's weights: 2 GiB
     (dict(N=2**23, ld_out=2**23, numel=2**20), mb.MOL_E_LIMIT),  # the grid
-    (dict(N=2**22, ld_out=2**22, numel=2**14, E=1, block_m=1024), mb.MOL_E_LIMIT),
+    (dict(N=2**22, ld_out=2**22, numel=2**17, E=1, block_m=1024), mb.MOL_E_LIMIT),  # 2^32 threads in groups of 512
+    (dict(dtype=0, K=32, ld_x=32, N=2**20, ld_out=2**20, numel=2**20, E=1, block_m=32), mb.MOL_E_LIMIT),
     (dict(x=None), mb.MOL_E_ARG), (dict(W=None), mb.MOL_E_ARG), (dict(scales=None), mb.MOL_E_ARG),
     (dict(out=None), mb.MOL_E_ARG), (dict(sorted=None), mb.MOL_E_ARG),
     (dict(expert=None), mb.MOL_E_ARG), (dict(npp=None), mb.MOL_E_ARG),

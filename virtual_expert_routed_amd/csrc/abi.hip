@@ -895,8 +895,9 @@ MOL_API mol_status mol_moe_gemm_mx4(int32_t dtype, const void* xin, int64_t ld_x
   a.f_bm = mol::make_fastdiv((uint32_t)block_m);
   // blocks that hold pairs: at most one partly filled per expert, beside the full ones
   const int64_t filled = std::min<int64_t>(numel, (int64_t)num_experts + numel / block_m);
-  const int form = mol::mx_form(filled, numel, N, block_m, x_scales ? mol::kMxRowsCodes : bf16 ? mol::kMxRowsBf16 : mol::kMxRowsF32);
-  if (rc.max_blocks * mol::mx_items(form, N, block_m) + 8 > kGridMax) return MOL_E_LIMIT;
+  const int rows = x_scales ? mol::kMxRowsCodes : bf16 ? mol::kMxRowsBf16 : mol::kMxRowsF32;
+  const int form = mol::mx_form(filled, numel, N, block_m, rows);
+  if (rc.max_blocks * mol::mx_items(form, N, block_m, rows) + 16 > kGridMax) return MOL_E_LIMIT;
   return hip_status(mol::launch_mx4_gemm(a, bf16, form, (hipStream_t)stream));
 }
 

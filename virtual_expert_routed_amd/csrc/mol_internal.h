@@ -312,10 +312,11 @@ inline int mx_form(int64_t filled, int64_t pairs, int64_t N, int64_t BM, int row
     return kMxWide;
   return rows == kMxRowsF32 && filled * ((N + 63) / 64) < 256 ? kMxSplit : kMxNarrow;
 }
-// at most this many work items in a routing block of BM pairs
-inline int64_t mx_items(int form, int64_t N, int64_t BM) {
-  const int64_t rows = form == kMxSplit ? 16 : 64;
-  return (N + rows - 1) / rows * (form == kMxWide ? (BM + 31) / 32 : 1);
+// A routing block's work items, in workgroups of 256 threads.
+inline int64_t mx_items(int form, int64_t N, int64_t BM, int rows) {
+  if (form != kMxWide) return form == kMxSplit ? (N + 15) / 16 : (N + 63) / 64;
+  if (rows == kMxRowsF32) return (N + 63) / 64 * ((BM + 31) / 32);
+  return 2 * ((N + 255) / 256) * ((BM + 127) / 128);
 }
 
 // The work items of a stream of weight rows: 64 rows times `tiles`, or 16 rows whose k's four waves

@@ -20,6 +20,12 @@ FORMS = [
     ("codes", 1000, 2, 1, 288, 6461, 48, WIDE), ("codes", 900, 3, 1, 768, 6420, 200, WIDE),
     ("codes", 700, 2, 1, 2080, 7401, 128, WIDE), ("codes", 700, 2, 1, 4672, 6430, 1024, WIDE),
     ("codes", 3000, 60, 2, 352, 300, 128, WIDE),
+    # wide over small blocks, two, four and eight of one expert together, the last of them partly filled; chains of
+    # them past a wave's lanes; not over the smallest, nor for fp32 rows
+    ("codes", 1000, 2, 1, 160, 6401, 64, WIDE), ("codes", 1500, 3, 1, 288, 4400, 32, WIDE),
+    ("codes", 1000, 3, 1, 64, 5500, 16, WIDE), ("codes", 500, 2, 1, 64, 9000, 1, NARROW),
+    ("bf16", 1500, 3, 1, 160, 4400, 64, WIDE), ("bf16", 9000, 1, 1, 96, 700, 16, WIDE),
+    ("f32", 700, 2, 1, 96, 130, 16, SPLIT),
     ("bf16", 1000, 2, 1, 32, 6401, 128, WIDE), ("bf16", 1000, 2, 1, 256, 6400, 128, WIDE),
     ("bf16", 1000, 2, 1, 288, 6461, 48, WIDE), ("bf16", 700, 2, 1, 2208, 6430, 1024, WIDE),
     ("bf16", 3000, 60, 2, 352, 300, 128, WIDE),

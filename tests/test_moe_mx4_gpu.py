@@ -98,6 +98,32 @@ def test_every_form(x, M, E, topk, K, N, block, form, per_pair):
              pad_out=8 if per_pair else 0).check()
 
 
+@pytest.mark.parametrize("x,dtype", [("codes", torch.bfloat16), ("rows", torch.bfloat16)], ids=["codes", "bf16"])
+@pytest.mark.parametrize("block", [16, 32, 64])
+def test_small_blocks_in_any_order(x, dtype, block):
+    """Blocks of an expert that are partly filled, empty or apart from each other, of the widest form."""
+    c = Case(1200, 3, 1, 160, 4400, x, dtype, block=block)
+    c.ids[torch.rand(1200, 1, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda") < 0.5] = -1
+    ahead, behind = [], []
+    for e in range(3):
+        pairs = (c.ids.reshape(-1) == e).nonzero().reshape(-1).tolist()
+        mine = []
+        for size in (block, block, 3, block, 0, block - 1) + (block,) * 99:
+            if pairs:
+                mine.append((pairs[:size] + [c.numel] * (block - size))[:block])
+                pairs = pairs[size:]
+        mine[-1] += [c.numel] * (block - len(mine[-1]))
+        ahead += [(b, e) for b in mine[:5]]
+        behind += [(b, e) for b in mine[5:]]
+    blocks = ahead + behind
+    srt, ids, npp = c.routing
+    assert len(blocks) <= ids.numel()
+    srt[:len(blocks) * block] = torch.tensor([b for b, _ in blocks], dtype=torch.int32).reshape(-1)
+    ids[:len(blocks)] = torch.tensor([e for _, e in blocks], dtype=torch.int32)
+    npp.fill_(len(blocks) * block)
+    c.check()
+
+
 @FORMS
 @pytest.mark.parametrize("block", [1, 16, 48, 64, 128, 256])
 def test_blocks(x, dtype, block):

@@ -11,9 +11,9 @@ SRC = r'''
 #include <algorithm>
 #include "mol_internal.h"
 int main() {
-  long long filled, pairs, N, BM, rows;
-  while (std::scanf("%lld %lld %lld %lld %lld", &filled, &pairs, &N, &BM, &rows) == 5)
-    std::printf("%d\n", mol::mx_form(filled, pairs, N, BM, (int)rows));
+  long long pairs, E, N, BM, rows;
+  while (std::scanf("%lld %lld %lld %lld %lld", &pairs, &E, &N, &BM, &rows) == 5)
+    std::printf("%d\n", mol::mx_form(pairs, E, N, BM, (int)rows));
 }
 '''
 
@@ -25,9 +25,7 @@ def test_the_cases_take_the_forms_they_name(tmp_path):
                     os.path.join(conftest.ROOT, "virtual_expert_routed_amd", "csrc"), str(src), "-o", str(exe)], check=True)
     asked = []
     for x, M, E, topk, K, N, block_m, form in mc.FORMS:
-        pairs = M * topk
-        filled = min(pairs, E + pairs // block_m)  # as mol_moe_gemm_mx4 counts them
-        asked.append((filled, pairs, N, block_m, {"bf16": 0, "f32": 1, "codes": 2}[x]))
+        asked.append((M * topk, E, N, block_m, {"bf16": 0, "f32": 1, "codes": 2}[x]))
     r = subprocess.run([str(exe)], input="\n".join(" ".join(map(str, a)) for a in asked), text=True, capture_output=True,
                        check=True)
     got = [int(ln) for ln in r.stdout.splitlines()]

@@ -893,11 +893,9 @@ MOL_API mol_status mol_moe_gemm_mx4(int32_t dtype, const void* xin, int64_t ld_x
   a.ld_out = ld_out;
   a.f_rd = mol::make_fastdiv((uint32_t)row_div);
   a.f_bm = mol::make_fastdiv((uint32_t)block_m);
-  // blocks that hold pairs: at most one partly filled per expert, beside the full ones
-  const int64_t filled = std::min<int64_t>(numel, (int64_t)num_experts + numel / block_m);
   const int rows = x_scales ? mol::kMxRowsCodes : bf16 ? mol::kMxRowsBf16 : mol::kMxRowsF32;
-  const int form = mol::mx_form(filled, numel, N, block_m, rows);
-  if (rc.max_blocks * mol::mx_items(form, N, block_m, rows) + 16 > kGridMax) return MOL_E_LIMIT;
+  const int form = mol::mx_form(numel, num_experts, N, block_m, rows);
+  if (mol::mx_grid(form, rc.max_blocks, N, block_m, rows) > kGridMax) return MOL_E_LIMIT;
   return hip_status(mol::launch_mx4_gemm(a, bf16, form, (hipStream_t)stream));
 }
 

@@ -447,27 +447,53 @@ __global__ void __launch_bounds__(256, 4) mx4_narrow_kernel(MxGemmArgs a) {
   }
 }
 
-// Many columns a block: an item is a span of TC columns of a block and 16 FR NW weight rows. The
-// items of the live blocks are a contiguous range for each of the eight XCDs (workgroups go round them):
-// neighbouring items share an expert's weights and a block's rows in its L2.
+// Many columns an expert: an item is a span of TC columns of a block, or up to a.merge smaller blocks of one expert
+// that together have TC, and 16 FR NW weight rows. The items of the live blocks are a contiguous range for
+// each of the eight XCDs (workgroups go round them): neighbouring items share an expert's weights and a block's
+// rows in its L2.
 template <int XF, bool OBF16, int TC, int FR, int SU, int NW>
 __global__ void __launch_bounds__(64 * NW, 4) mx4_wide_kernel(MxGemmArgs a) {
   using Sh = MxShape<XF, TC, FR, SU, NW, 1>;
   __shared__ MxLds<XF, TC, FR, SU, NW, 1> lds;
   const int npp = *a.npp;
   const int nb = npp < 0 ? 0 : min(fdiv(npp, a.f_bm), a.max_blocks);
-  const int per_xcd = (int)(((int64_t)nb * a.items + 7) >> 3);
+  // of the items of a.merge neighbouring blocks an XCD has those of the first one for its whole range, then the
+  // second's: those that lead (below) lie together more often than not, and their workgroups on all compute units
+  const int per_xcd = (int)((((int64_t)nb + a.merge - 1) / a.merge * a.items + 7) >> 3);
   const int local = (int)blockIdx.x >> 3;
-  const int item = ((int)blockIdx.x & 7) * per_xcd + local;
-  const int blk = fdiv(item, a.f_items);
-  if (local >= per_xcd || blk >= nb) return;
+  const int turn = a.merge > 1 ? (int)((uint32_t)local / (uint32_t)max(per_xcd, 1)) : 0;
+  const int item = ((int)blockIdx.x & 7) * per_xcd + local - turn * per_xcd;
+  const int group = fdiv(item, a.f_items);
+  const int blk = group * a.merge + turn;
+  if (local >= per_xcd * a.merge || blk >= nb) return;
   const int er = a.expert_ids[blk];
   if ((unsigned)er >= (unsigned)a.E) return;
-  const int in_blk = item - blk * a.items;
+  int width = a.BM;  // columns of the item's blocks
+  if (a.merge > 1) {
+    // A full block and the next one go together where they are one expert's: of a chain of such blocks every
+    // a.merge-th, from its first on, leads an item, and its followers leave theirs to it.
+    const int lane = threadIdx.x & 63;
+    auto joins = [&](int i) __attribute__((always_inline)) {  // block i with block i + 1, 0 <= i < nb - 1
+      return a.expert_ids[i] == er && a.expert_ids[i + 1] == er &&
+             real_pair(a.sorted[(int64_t)i * a.BM + a.BM - 1], a.numel);
+    };
+    int place = 0;
+    for (int at = blk; at > 0; at -= 64) {
+      const int i = at - 1 - lane;
+      const uint64_t ends = __builtin_amdgcn_ballot_w64(i < 0 || !joins(i));
+      place += ends ? __builtin_ctzll(ends) : 64;
+      if (ends) break;
+    }
+    if (place % a.merge) return;
+    const int i = blk + lane;
+    const uint64_t ends = __builtin_amdgcn_ballot_w64(lane >= a.merge - 1 || i >= nb - 1 || !joins(i));
+    width += __builtin_ctzll(ends) * a.BM;  // (a.merge <= 8)
+  }
+  const int in_blk = item - group * a.items;
   const int span = fdiv(in_blk, a.f_tiles);  // of the block's spans of columns
   const int n0 = (in_blk - span * (int)a.f_tiles.d) * Sh::ROWS;
   const int j = span * TC + (int)threadIdx.x;
-  const int p = threadIdx.x < TC && j < a.BM ? a.sorted[(int64_t)blk * a.BM + j] : a.numel;
+  const int p = threadIdx.x < TC && j < width ? a.sorted[(int64_t)blk * a.BM + j] : a.numel;
   const int ncol = put_pairs<TC>(lds.cols, p, a);
   if (ncol == 0) return;
   mx4_pass<XF, OBF16, TC, FR, SU, NW, 1>(a, lds.x, lds.ws, lds.xs, lds.cols,
@@ -491,9 +517,10 @@ hipError_t mx4_wide(MxGemmArgs a, hipStream_t st) {
   const int32_t tiles = (a.N + Sh::ROWS - 1) / Sh::ROWS;
   a.f_tiles = make_fastdiv((uint32_t)tiles);
   a.items = tiles * ((a.BM + TC - 1) / TC);
+  a.merge = mx_merge(a.BM, TC);
   a.f_items = make_fastdiv((uint32_t)a.items);
   // (a range for each XCD, rounded up)
-  const int64_t grid = ((int64_t)a.max_blocks * a.items + 7) / 8 * 8;
+  const int64_t grid = ((int64_t)(a.max_blocks + a.merge - 1) / a.merge * a.items + 7) / 8 * 8 * a.merge;
   hipLaunchKernelGGL((mx4_wide_kernel<XF, OBF16, TC, FR, SU, NW>), dim3((unsigned)grid), dim3(64 * NW), 0,
                      st, a);
   return hipGetLastError();

@@ -296,8 +296,8 @@ struct MxGemmArgs {
   FastDiv f_rd;
   FastDiv f_bm;
   // of the form, set at the launch
-  int32_t items;           // work items per routing block: spans times tiles (runs of tiles) of weight rows
-  int32_t run;             // tiles of a run
+  int32_t items;           // work items per routing block: spans times tiles of weight rows
+  int32_t merge;           // blocks of one expert that an item takes together
   FastDiv f_items;
   FastDiv f_tiles;
 };
@@ -306,17 +306,24 @@ enum { kMxRowsBf16 = 0, kMxRowsF32 = 1, kMxRowsCodes = 2 };  // of x
 // The form of the product: passes of 32 columns over 16 weight rows whose k's four waves split (fp32 rows), passes
 // of up to 64 columns (fp32 rows 32) over 64 rows, or spans of 128 columns over 256 rows (fp32 rows 32 over 64).
 enum { kMxSplit = 0, kMxNarrow = 1, kMxWide = 2 };
-inline int mx_form(int64_t filled, int64_t pairs, int64_t N, int64_t BM, int rows) {
-  if (pairs > 32 * filled &&
-      (rows == kMxRowsF32 || filled * ((BM + 127) / 128) * ((N + 255) / 256) >= 200))
+// Blocks of BM pairs that hold some: at most one partly filled for each of E experts, beside the full ones.
+inline int64_t mx_filled(int64_t pairs, int64_t E, int64_t BM) { return pairs < E + pairs / BM ? pairs : E + pairs / BM; }
+// Blocks of BM pairs that an item of the widest form, of TC columns, takes together.
+inline int mx_merge(int64_t BM, int TC) { return BM >= 16 && BM < TC && TC % BM == 0 ? (int)(TC / BM) : 1; }
+inline int mx_form(int64_t pairs, int64_t E, int64_t N, int64_t BM, int rows) {
+  const int64_t filled = mx_filled(pairs, E, BM);
+  const int64_t wide = rows != kMxRowsF32 && mx_merge(BM, 128) > 1 ? mx_filled(pairs, E, 128) : filled;
+  if (pairs > 32 * wide &&
+      (rows == kMxRowsF32 || wide * ((BM + 127) / 128) * ((N + 255) / 256) >= 200))
     return kMxWide;
   return rows == kMxRowsF32 && filled * ((N + 63) / 64) < 256 ? kMxSplit : kMxNarrow;
 }
-// A routing block's work items, in workgroups of 256 threads.
-inline int64_t mx_items(int form, int64_t N, int64_t BM, int rows) {
-  if (form != kMxWide) return form == kMxSplit ? (N + 15) / 16 : (N + 63) / 64;
-  if (rows == kMxRowsF32) return (N + 63) / 64 * ((BM + 31) / 32);
-  return 2 * ((N + 255) / 256) * ((BM + 127) / 128);
+// The launch for up to B routing blocks, in workgroups of 256 threads (a wide one over codes or bf16 rows has 512).
+inline int64_t mx_grid(int form, int64_t B, int64_t N, int64_t BM, int rows) {
+  if (form != kMxWide) return B * (form == kMxSplit ? (N + 15) / 16 : (N + 63) / 64);
+  const int TC = rows == kMxRowsF32 ? 32 : 128, ROWS = rows == kMxRowsF32 ? 64 : 256, merge = mx_merge(BM, TC);
+  const int64_t items = (N + ROWS - 1) / ROWS * ((BM + TC - 1) / TC);
+  return ((B + merge - 1) / merge * items + 7) / 8 * 8 * merge * (rows == kMxRowsF32 ? 1 : 2);
 }
 
 // The work items of a stream of weight rows: 64 rows times `tiles`, or 16 rows whose k's four waves

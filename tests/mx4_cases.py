@@ -24,6 +24,7 @@ FORMS = [
     # them past a wave's lanes; not over the smallest, nor for fp32 rows
     ("codes", 1000, 2, 1, 160, 6401, 64, WIDE), ("codes", 1500, 3, 1, 288, 4400, 32, WIDE),
     ("codes", 1000, 3, 1, 64, 5500, 16, WIDE), ("codes", 500, 2, 1, 64, 9000, 1, NARROW),
+    ("codes", 1000, 3, 1, 96, 2500, 16, WIDE), ("codes", 500, 60, 4, 64, 1000, 16, WIDE),
     ("bf16", 1500, 3, 1, 160, 4400, 64, WIDE), ("bf16", 9000, 1, 1, 96, 700, 16, WIDE),
     ("f32", 700, 2, 1, 96, 130, 16, SPLIT),
     ("bf16", 1000, 2, 1, 32, 6401, 128, WIDE), ("bf16", 1000, 2, 1, 256, 6400, 128, WIDE),

@@ -9,14 +9,28 @@
 // exact, scale included. Products and sums are fp32, so infinities and NaN of x reach exactly the
 // sums that the formula has them in.
 //
-// A work item is a span of columns of a routing block (a pass of the widest form, all of the block's of the
-// narrow ones) and NW times 16 FR weight rows; wave w has 16 FR of them as
-// the A operand, straight from memory into registers: lane l holds row l % 16 and whole blocks of 32 k's,
-// which block of a step being free as long as x agrees. x goes through LDS for all four waves,
-// as it lies in memory: direct-to-LDS loads, whose lanes choose their 16 bytes of a row so that the
-// reads of a fragment (16 columns at one place of their rows) spread over the banks. Stages of x
-// alternate between two buffers, the next one loading while one is at work; a weight register is filled
-// again as soon as it has been used.
+// A work item is a span of columns of a routing block (of the wide form; all of the block's of the narrow ones)
+// and NW times 16 FR weight rows; wave w has 16 FR of them as the A operand, straight from memory into
+// registers: lane l holds row l % 16 and whole blocks of 32 k's, which block of a step being free as long as
+// x agrees. x goes through LDS for all waves, as it lies in memory: direct-to-LDS loads, whose lanes choose
+// their 16 bytes of a row so that the reads of a fragment (16 columns at one place of their rows) spread over
+// the banks. Stages of x alternate between two buffers, the next one loading while one is at work; a weight
+// register is filled again as soon as it has been used. A row's scales come by 2048 k's (1024 beside bf16
+// and fp32 rows) through LDS: a scale byte a lane loaded from memory beside its codes took as many look-ups
+// of the L1 as the codes.
+//
+// Kernel times (rocprofv3) and what bounds them, K 2048 and N 1536 (gate_up) or K 768 and N 2048 (down), top 8 of
+// 128 experts, a copy's 4.94 TB/s:
+//   1 token, codes, gate_up                   8.4 us  13.4 MB in 2.7 us: the launch, the routing, then one load's latency after another
+//   23 tokens, codes, down                   17.4 us  83 MB of weights, 97 % of the copy's rate
+//   128 tokens, zipf, bf16 rows, gate_up     42.9 us  200 MB, 95 %
+//   4096 tokens, codes, gate_up             112 us    1.8 PFLOP/s: look-ups of the L1 for W (the bytes alone: 64)
+//   4096 tokens, bf16 rows, down            131 us    0.79 PFLOP/s of bf16, 71 % of the library's square product
+//   16384 tokens, codes, down               275 us    1.5 PFLOP/s; a third of it the stores of 537 MB
+// W as the A operand costs 64 lines of the L1 a load (16 rows of 64 bytes apart). Both operands through LDS, three
+// stages deep, took as long (129 and 308 us for 4096 gate_up and 16384 down where this took 130 and 307),
+// so the form with fewer barriers stayed; workgroups that stay and take item after item 155 and 363; 256 columns
+// an item 138 and 306 against 113 and 275.
 //
 // Of the result, lane l holds column (pair) l % 16 and rows 4 (l / 16) + i.
 #pragma once
@@ -49,7 +63,6 @@ struct MxShape {
   static constexpr int STAGE = SU * KS;                 // units of a stage
   static constexpr int PARTS = TC * XB / 1024;          // direct-to-LDS loads of a unit
   static constexpr int COLS = 64 / CH;                  // columns of one such load
-  static constexpr int NP = PARTS > NW ? PARTS / NW : 1;  // a wave's parts
   static constexpr int BYTES = STAGE * TC * XB;         // of a buffer
   static constexpr int ROWS = 16 * FR * (KS > 1 ? 1 : NW);  // of an item
   // units whose scales are staged at a time: those of 2048 k's (1024 beside bf16 or fp32 rows)

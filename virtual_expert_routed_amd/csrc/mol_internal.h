@@ -303,20 +303,34 @@ struct MxGemmArgs {
 };
 enum { kMxRowsBf16 = 0, kMxRowsF32 = 1, kMxRowsCodes = 2 };  // of x
 
-// The form of the product: passes of 32 columns over 16 weight rows whose k's four waves split (fp32 rows), passes
-// of up to 64 columns (fp32 rows 32) over 64 rows, or spans of 128 columns over 256 rows (fp32 rows 32 over 64).
+// The form of the product:
+//  - split: passes of 16 columns over 16 weight rows, whose k's four waves share out (fp32 rows)
+//  - narrow: passes of up to 64 columns (fp32 rows 32) over 64 weight rows
+//  - wide: 128 columns over 256 weight rows (fp32 rows 32 over 64), a work item each
 enum { kMxSplit = 0, kMxNarrow = 1, kMxWide = 2 };
 // Blocks of BM pairs that hold some: at most one partly filled for each of E experts, beside the full ones.
 inline int64_t mx_filled(int64_t pairs, int64_t E, int64_t BM) { return pairs < E + pairs / BM ? pairs : E + pairs / BM; }
-// Blocks of BM pairs that an item of the widest form, of TC columns, takes together.
+// Blocks of BM pairs that an item of the wide form, of TC columns, takes together. (4096 tokens, top 8 of 128
+// experts, K 2048, N 1536, codes and bf16 rows: blocks of 64 one by one 155 and 277 us, together 119 and 235;
+// blocks of 16 447 and 596, together 135 and 253.)
 inline int mx_merge(int64_t BM, int TC) { return BM >= 16 && BM < TC && TC % BM == 0 ? (int)(TC / BM) : 1; }
+// Wide where a pass of the narrow form would have many columns or read an expert's weights many times, and where
+// there are work items for the chip; of the narrow ones split for few items. Queued calls, us (K 2048, N 1536, experts
+// 128 top 8 unless said):
+//   narrow and wide  codes, blocks of 64: 512 tokens 42 and 49, 1024 60 and 53, 4096 192 and 119; of 16: 256 tokens 45
+//     and 47, 512 73 and 56.  bf16 rows, blocks of 64: 512 tokens 72 and 77, 768 98 and 85, 4096 401 and 235
+//   one expert of N 2048 (8 items a span): blocks of 64, codes: 1024 tokens 12.5 and 18.4 (72 items), 4096 32 and 29
+//     (264); of 16: 1024 23 and 18, 2048 42 and 20 (136); bf16 rows, blocks of 64: 2048 34 and 46 (136), 4096 63 and 61
+//   narrow and split, fp32 rows: one token of one expert (32 items) 17.3 and 10.5, of 8 of 128 experts (192) 19.3 and
+//     19.0, 256 items 12.6 and 13.4.  (bf16 rows, split against narrow: one token of one expert 11.1 and 9.5.)
 inline int mx_form(int64_t pairs, int64_t E, int64_t N, int64_t BM, int rows) {
   const int64_t filled = mx_filled(pairs, E, BM);
-  const int64_t wide = rows != kMxRowsF32 && mx_merge(BM, 128) > 1 ? mx_filled(pairs, E, 128) : filled;
-  if (pairs > 32 * wide &&
-      (rows == kMxRowsF32 || wide * ((BM + 127) / 128) * ((N + 255) / 256) >= 200))
-    return kMxWide;
-  return rows == kMxRowsF32 && filled * ((N + 63) / 64) < 256 ? kMxSplit : kMxNarrow;
+  if (rows == kMxRowsF32)
+    return pairs > 32 * filled ? kMxWide : filled * ((N + 63) / 64) < 256 ? kMxSplit : kMxNarrow;
+  const int64_t spans = mx_merge(BM, 128) > 1 ? mx_filled(pairs, E, 128) : filled * ((BM + 127) / 128);
+  const int64_t taken = mx_merge(BM, 128) > 1 ? spans : filled;  // blocks, or runs of blocks taken together
+  const int64_t items = spans * ((N + 255) / 256), least = rows == kMxRowsCodes && filled >= 4 * spans ? 100 : 200;
+  return (pairs > 32 * taken || filled >= 2 * taken) && items >= least ? kMxWide : kMxNarrow;
 }
 // The launch for up to B routing blocks, in workgroups of 256 threads (a wide one over codes or bf16 rows has 512).
 inline int64_t mx_grid(int form, int64_t B, int64_t N, int64_t BM, int rows) {

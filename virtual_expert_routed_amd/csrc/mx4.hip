@@ -8,11 +8,14 @@
 //
 // The division is by a power of two and the rounding the hardware's, so codes of given values are
 // exact. Those of the activation are the ones of its value in 64 bits: the product is formed in fp32,
-// within 2^-19 of itself, and lanes whose codes or scale would be others 2^-18 to either side form it
+// within 2^-18.5 of itself, and lanes whose codes or scale would be others 2^-18 to either side form it
 // again in 64 bits (about one lane in a thousand).
 //
 // Bound by bytes. A lane takes eight consecutive values (16 bytes of bf16), four lanes a block; a thread
-// has kVecs such vectors in flight.
+// has kVecs such vectors in flight. Kernel times (rocprofv3): 196608 rows of 2048 in fp32 (1.6 GB, to codes and
+// back) 339 and 328 us, 5.4 and 5.6 TB/s; the activation of 32768 bf16 rows of 2 x 768 28 us (4.0 TB/s: eight
+// exponentials, reciprocals and two encodings a lane beside the bytes), back to bf16 10 us (6.3 TB/s); 23 rows of
+// 2048 3 us each way, a launch.
 #include "mx4.h"
 #include "skinny.h"
 
@@ -62,7 +65,7 @@ __device__ __forceinline__ uint32_t scale_of(uint32_t m) {
   return m >= 0x7f800000u ? kMxNaN : (uint32_t)max((int)(m >> 23) - 2, 0);
 }
 
-// v = SiLU(g) * u within 2^-19 of itself. Up to |g| = 32 the hardware's exp2 and reciprocal do: the exponent's argument
+// v = SiLU(g) * u within 2^-18.5 of itself. Up to |g| = 32 the hardware's exp2 and reciprocal do: the exponent's argument
 // is rounded at 46 (2^-19.5 in all).
 __device__ __forceinline__ void silu_mul8(const float (&g)[8], const float (&u)[8], float (&v)[8]) {
   float m = 0.f;

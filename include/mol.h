@@ -405,7 +405,7 @@ MOL_API mol_status mol_router_topk(int32_t dtype, const void *logits, int64_t ld
  *   counts        int32 [num_experts + 1] of mol_router_balance, or their sums over the ranks that
  *                 share the batch (the loss is then that of the whole batch: its P_e are sums too)
  *   grad_loss     float32 [1], the gradient that arrives at the loss, or NULL for 1
- *   others        as above. M = 0 enqueues nothing.
+ *   others        as above. grad_logits may be logits itself (with its stride). M = 0 enqueues nothing.
  * Errors of both: MOL_E_ARG, MOL_E_DTYPE, MOL_E_ALIGN, MOL_E_WORKSPACE, MOL_E_LIMIT (num_experts + 1 >
  * MOL_MAX_BUCKETS, topk > MOL_MAX_ROUTER_TOPK, M * topk past 32 bits).
  * ------------------------------------------------------------------------------- */
@@ -485,8 +485,8 @@ MOL_API mol_status mol_moe_gemm_q4(int32_t dtype, const void *xin, int64_t ld_x,
  *                 (ld_x a multiple of 32), with scales ld_x / 32 bytes apart
  *   W             uint8 [E, N, K / 2], 16-byte aligned;  scales uint8 [E, N, K / 32]
  *   others        as for mol_moe_gemm (rows of xin on 16-byte boundaries)
- * For decode and prefill batches; blocks of any block_m are taken. Dense blocks run fastest at block_m
- * = 128.
+ * For decode and prefill batches; blocks of any block_m are taken. From some thousand tokens on blocks of 128
+ * pairs run fastest; of 64, 32 or 16 of one expert in a row, full but for the last, are taken together.
  * Errors: MOL_E_ARG (K not a multiple of 32), MOL_E_LIMIT (one expert's weights 2 GiB or more, 2^24
  * work items or more), others as for mol_moe_gemm.
  * ------------------------------------------------------------------------------- */

@@ -15,6 +15,11 @@
 // whole-number atomics in LDS). A second launch adds the rows, 8 experts a workgroup; the last
 // workgroup to finish forms the loss. Few tokens take one workgroup and one launch. No sum depends
 // on the order in which anything arrives: results are the same bit for bit.
+//
+// Kernel times (rocprofv3): 138 tokens of 160 experts in fp32, sigmoid 5.2 + 5.1 us forward and 4.6 the gradient,
+// latency and launches throughout (0.2 MB); 16384 of 128 in bf16, softmax 6.9 + 7.0 and 9.0, of which their 4.2 MB read and
+// 8.4 moved take 0.9 and 1.7 at a copy's rate: issue of the exponentials, the reductions over lanes and waves, and the
+// second launch's wait for the first.
 #include "router_row.h"
 
 namespace mol {

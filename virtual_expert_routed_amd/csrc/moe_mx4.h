@@ -21,7 +21,7 @@
 //
 // Kernel times (rocprofv3) and what bounds them, K 2048 and N 1536 (gate_up) or K 768 and N 2048 (down), top 8 of
 // 128 experts, a copy's 4.94 TB/s:
-//   1 token, codes, gate_up                   8.4 us  13.4 MB in 2.7 us: the launch, the routing, then one load's latency after another
+//   1 token, bf16 rows, gate_up               8.4 us  13.4 MB in 2.7 us: launch, routing, one latency after another
 //   23 tokens, codes, down                   17.4 us  83 MB of weights, 97 % of the copy's rate
 //   128 tokens, zipf, bf16 rows, gate_up     42.9 us  200 MB, 95 %
 //   4096 tokens, codes, gate_up             112 us    1.8 PFLOP/s: look-ups of the L1 for W (the bytes alone: 64)

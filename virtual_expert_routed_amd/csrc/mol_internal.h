@@ -228,7 +228,9 @@ struct BalanceArgs {
   int64_t ld_grad;
 };
 
-// Rows of 16 lanes, four a wave, instead of a wave each.
+// Rows of 16 lanes, four a wave, instead of a wave each: few rows are a chain of latencies, which a lane with more
+// experts lengthens. Forward and gradient, us: 138 tokens of 160 experts 17.0 + 8.0 against 10.3 + 4.6, 16384 of 128
+// 13.9 + 9.0 against 15.9 + 8.3.
 inline bool balance_narrow(int64_t M, int32_t E) { return E <= 256 && M > 1024; }
 
 // Threads of a workgroup of the forward pass (a lane holds the scores of up to 16 experts, or of 32 and 128),
@@ -237,7 +239,8 @@ inline int balance_threads(int32_t E) { return E <= 1024 ? 1024 : 256; }
 inline int64_t balance_rows(int64_t M, int32_t E) { return balance_threads(E) / (balance_narrow(M, E) ? 16 : 64); }
 
 // Workgroups of the forward pass: one for up to four turns of its rows, which needs no second launch (a turn takes
-// 1.5 us, the second launch 5); else one for each turn, at most 256, and fewer where their partial sums would take more than 4 MiB.
+// 1.5 us, the second launch 5); else one for each turn, at most 256, and fewer where their partial
+// sums would take more than 4 MiB.
 constexpr int kBalanceGroups = 256;
 constexpr int kBalanceGradGroups = 2048;
 inline int32_t balance_groups(int64_t M, int32_t E) {

@@ -98,6 +98,13 @@ def test_every_form(x, M, E, topk, K, N, block, form, per_pair):
              pad_out=8 if per_pair else 0).check()
 
 
+@pytest.mark.parametrize("x,M,E,topk,K,N,block,form", mc.POPULAR)
+def test_popular_experts_in_several_passes(x, M, E, topk, K, N, block, form):
+    c = Case(M, E, topk, K, N, "codes" if x == "codes" else "rows", torch.bfloat16, block=block, skew=True)
+    assert int((c.ids == 0).sum()) > 3 * block
+    c.check()
+
+
 @pytest.mark.parametrize("x,dtype", [("codes", torch.bfloat16), ("rows", torch.bfloat16)], ids=["codes", "bf16"])
 @pytest.mark.parametrize("block", [16, 32, 64])
 def test_small_blocks_in_any_order(x, dtype, block):

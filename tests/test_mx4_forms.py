@@ -24,11 +24,12 @@ def test_the_cases_take_the_forms_they_name(tmp_path):
     subprocess.run(["g++", "-std=c++17", "-O1", "-w", "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include", "-I",
                     os.path.join(conftest.ROOT, "virtual_expert_routed_amd", "csrc"), str(src), "-o", str(exe)], check=True)
     asked = []
-    for x, M, E, topk, K, N, block_m, form in mc.FORMS:
+    for x, M, E, topk, K, N, block_m, form in mc.FORMS + mc.POPULAR:
         asked.append((M * topk, E, N, block_m, {"bf16": 0, "f32": 1, "codes": 2}[x]))
     r = subprocess.run([str(exe)], input="\n".join(" ".join(map(str, a)) for a in asked), text=True, capture_output=True,
                        check=True)
     got = [int(ln) for ln in r.stdout.splitlines()]
-    assert got == [c[-1] for c in mc.FORMS], [(c, g) for c, g in zip(mc.FORMS, got) if c[-1] != g]
+    cases = mc.FORMS + mc.POPULAR
+    assert got == [c[-1] for c in cases], [(c, g) for c, g in zip(cases, got) if c[-1] != g]
     assert {(c[0], c[-1]) for c in mc.FORMS} == {(x, f) for x in ("bf16", "codes", "f32") for f in (mc.NARROW, mc.WIDE)} | {
-        ("f32", mc.SPLIT)}
+        ("f32", mc.SPLIT), ("bf16", mc.SPREAD), ("codes", mc.SPREAD)}

@@ -9,8 +9,8 @@
 // exact, scale included. Products and sums are fp32, so infinities and NaN of x reach exactly the
 // sums that the formula has them in.
 //
-// A work item is a span of columns of a routing block (of the wide form; all of the block's of the narrow ones)
-// and NW times 16 FR weight rows; wave w has 16 FR of them as the A operand, straight from memory into
+// A work item is a span of columns of a routing block (of the wide, spread and split forms; all of the block's of
+// the narrow one) and NW times 16 FR weight rows; wave w has 16 FR of them as the A operand, straight from memory into
 // registers: lane l holds row l % 16 and whole blocks of 32 k's, which block of a step being free as long as
 // x agrees. x goes through LDS for all waves, as it lies in memory: direct-to-LDS loads, whose lanes choose
 // their 16 bytes of a row so that the reads of a fragment (16 columns at one place of their rows) spread over
@@ -423,23 +423,29 @@ __device__ __forceinline__ int put_pairs(MxCols<TC>& cols, int p, const MxGemmAr
 }
 
 // A few columns a block: an item is a block and 64 weight rows (16 with split k's), whose passes of up to
-// TC columns take the buffers in the shape of the columns there are.
-template <int XF, bool OBF16, int TC, int SU, int KS>
+// TC columns take the buffers in the shape of the columns there are; or, where SPREAD, one such pass.
+template <int XF, bool OBF16, int TC, int SU, int KS, bool SPREAD>
 __global__ void __launch_bounds__(256, 4) mx4_narrow_kernel(MxGemmArgs a) {
   __shared__ MxLds<XF, TC, 1, SU, 4, KS> lds;
   const int blk = fdiv((int)blockIdx.x, a.f_items);
-  const int n0 = ((int)blockIdx.x - blk * a.items) * (KS > 1 ? 16 : 64);
+  int in_blk = (int)blockIdx.x - blk * a.items, first = 0;
+  if constexpr (SPREAD) {
+    const int span = fdiv(in_blk, a.f_tiles);
+    in_blk -= span * (int)a.f_tiles.d;
+    first = span * TC;
+  }
+  const int n0 = in_blk * (KS > 1 ? 16 : 64);
   const int32_t* sorted = a.sorted + (int64_t)blk * a.BM;
   const int tid = threadIdx.x;
   const int npp = *a.npp;
   const int er = a.expert_ids[blk];
   // the first entries with the routing reads (their index stays inside the block)
-  int p = tid < TC && tid < a.BM ? sorted[tid] : a.numel;
+  int p = tid < TC && tid < a.BM - first ? sorted[first + tid] : a.numel;
   const int nb = npp < 0 ? 0 : fdiv(npp, a.f_bm);
   if (blk >= nb || (unsigned)er >= (unsigned)a.E) return;
   const int e = __builtin_amdgcn_readfirstlane(er);
-  for (int j0 = 0; j0 < a.BM; j0 += TC) {
-    if (j0 > 0) {
+  for (int j0 = first; j0 < a.BM; j0 += TC) {
+    if (j0 > first) {
       p = tid < TC && j0 + tid < a.BM ? sorted[j0 + tid] : a.numel;
       __syncthreads();  // the last pass is done with LDS
     }
@@ -456,7 +462,7 @@ __global__ void __launch_bounds__(256, 4) mx4_narrow_kernel(MxGemmArgs a) {
     } else {
       pass(std::integral_constant<int, TC>{});
     }
-    if (ncol < TC) return;
+    if (SPREAD || ncol < TC) return;
   }
 }
 
@@ -513,13 +519,15 @@ __global__ void __launch_bounds__(64 * NW, 4) mx4_wide_kernel(MxGemmArgs a) {
                                          __builtin_amdgcn_readfirstlane(er), n0, ncol);
 }
 
-template <int XF, bool OBF16, int TC, int SU, int KS>
+template <int XF, bool OBF16, int TC, int SU, int KS, bool SPREAD>
 hipError_t mx4_narrow(MxGemmArgs a, hipStream_t st) {
   static_assert(KS == 1 || (KS == 4 && 4096 * TC / 16 <= 2 * MxShape<XF, TC, 1, SU, 4, KS>::BYTES),
                 "room for the waves' sums");
-  a.items = (a.N + (KS > 1 ? 15 : 63)) / (KS > 1 ? 16 : 64);
+  const int32_t tiles = (a.N + (KS > 1 ? 15 : 63)) / (KS > 1 ? 16 : 64);
+  a.f_tiles = make_fastdiv((uint32_t)tiles);
+  a.items = SPREAD ? tiles * mx_spans(a.BM, TC) : tiles;
   a.f_items = make_fastdiv((uint32_t)a.items);
-  hipLaunchKernelGGL((mx4_narrow_kernel<XF, OBF16, TC, SU, KS>), dim3((unsigned)(a.max_blocks * a.items)),
+  hipLaunchKernelGGL((mx4_narrow_kernel<XF, OBF16, TC, SU, KS, SPREAD>), dim3((unsigned)(a.max_blocks * a.items)),
                      dim3(256), 0, st, a);
   return hipGetLastError();
 }
@@ -529,7 +537,7 @@ hipError_t mx4_wide(MxGemmArgs a, hipStream_t st) {
   using Sh = MxShape<XF, TC, FR, SU, NW, 1>;
   const int32_t tiles = (a.N + Sh::ROWS - 1) / Sh::ROWS;
   a.f_tiles = make_fastdiv((uint32_t)tiles);
-  a.items = tiles * ((a.BM + TC - 1) / TC);
+  a.items = tiles * mx_spans(a.BM, TC);
   a.merge = mx_merge(a.BM, TC);
   a.f_items = make_fastdiv((uint32_t)a.items);
   // (a range for each XCD, rounded up)

@@ -6,8 +6,11 @@ namespace {
 
 template <bool OBF16>
 hipError_t by_form(const MxGemmArgs& a, int form, hipStream_t st) {
-  return form == kMxWide ? mx4_wide<kMxRowsCodes, OBF16, 128, 2, 1, 8>(a, st)
-                         : mx4_narrow<kMxRowsCodes, OBF16, 64, 1, 1>(a, st);
+  switch (form) {
+    case kMxSpread: return mx4_narrow<kMxRowsCodes, OBF16, 64, 1, 1, true>(a, st);
+    case kMxNarrow: return mx4_narrow<kMxRowsCodes, OBF16, 64, 1, 1, false>(a, st);
+    default: return mx4_wide<kMxRowsCodes, OBF16, 128, 2, 1, 8>(a, st);
+  }
 }
 
 }  // namespace

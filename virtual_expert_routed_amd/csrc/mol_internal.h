@@ -307,10 +307,13 @@ struct MxGemmArgs {
 enum { kMxRowsBf16 = 0, kMxRowsF32 = 1, kMxRowsCodes = 2 };  // of x
 
 // The form of the product:
-//  - split: passes of 16 columns over 16 weight rows, whose k's four waves share out (fp32 rows)
-//  - narrow: passes of up to 64 columns (fp32 rows 32) over 64 weight rows
-//  - wide: 128 columns over 256 weight rows (fp32 rows 32 over 64), a work item each
-enum { kMxSplit = 0, kMxNarrow = 1, kMxWide = 2 };
+//  - split: 16 columns over 16 weight rows, whose k's four waves share out, a work item (fp32 rows)
+//  - narrow: all of a block's columns over 64 weight rows, in passes of up to 64 (fp32 rows 32)
+//  - spread: a pass of the narrow form (bf16 rows: of up to 32 columns) is a work item
+//  - wide: 128 columns over 256 weight rows (fp32 rows 32 over 64) are
+enum { kMxSplit = 0, kMxNarrow = 1, kMxWide = 2, kMxSpread = 3 };
+// Spans of up to TC columns of a block.
+inline int32_t mx_spans(int64_t BM, int TC) { return (int32_t)((BM + TC - 1) / TC); }
 // Blocks of BM pairs that hold some: at most one partly filled for each of E experts, beside the full ones.
 inline int64_t mx_filled(int64_t pairs, int64_t E, int64_t BM) { return pairs < E + pairs / BM ? pairs : E + pairs / BM; }
 // Blocks of BM pairs that an item of the wide form, of TC columns, takes together. (4096 tokens, top 8 of 128
@@ -324,6 +327,9 @@ inline int mx_merge(int64_t BM, int TC) { return BM >= 16 && BM < TC && TC % BM 
 //     and 47, 512 73 and 56.  bf16 rows, blocks of 64: 512 tokens 72 and 77, 768 98 and 85, 4096 401 and 235
 //   one expert of N 2048 (8 items a span): blocks of 64, codes: 1024 tokens 12.5 and 18.4 (72 items), 4096 32 and 29
 //     (264); of 16: 1024 23 and 18, 2048 42 and 20 (136); bf16 rows, blocks of 64: 2048 34 and 46 (136), 4096 63 and 61
+//   narrow and spread, one expert of N 2048 (32 items a block): bf16 rows, blocks of 64: 64 tokens 19.3 and 12.1, 512 20.4
+//     and 13.9; of 128: 512 37.5 and 14.8; codes, blocks of 128: 512 15.5 and 12.5. One pair a block (one token of 8 of 128
+//     experts) 8.7 and 9.5
 //   narrow and split, fp32 rows: one token of one expert (32 items) 17.3 and 10.5, of 8 of 128 experts (192) 19.3 and
 //     19.0, 256 items 12.6 and 13.4.  (bf16 rows, split against narrow: one token of one expert 11.1 and 9.5.)
 inline int mx_form(int64_t pairs, int64_t E, int64_t N, int64_t BM, int rows) {
@@ -333,13 +339,19 @@ inline int mx_form(int64_t pairs, int64_t E, int64_t N, int64_t BM, int rows) {
   const int64_t spans = mx_merge(BM, 128) > 1 ? mx_filled(pairs, E, 128) : filled * ((BM + 127) / 128);
   const int64_t taken = mx_merge(BM, 128) > 1 ? spans : filled;  // blocks, or runs of blocks taken together
   const int64_t items = spans * ((N + 255) / 256), least = rows == kMxRowsCodes && filled >= 4 * spans ? 100 : 200;
-  return (pairs > 32 * taken || filled >= 2 * taken) && items >= least ? kMxWide : kMxNarrow;
+  if ((pairs > 32 * taken || filled >= 2 * taken) && items >= least) return kMxWide;
+  const int64_t full = mx_filled(pairs, E, BM < 64 ? BM : 64);  // passes of a full block's size
+  return BM > (rows == kMxRowsCodes ? 64 : 32) && pairs > 16 * full &&
+                 full * ((N + 63) / 64) < (BM > 64 ? 2048 : 1024)
+             ? kMxSpread
+             : kMxNarrow;
 }
 // The launch for up to B routing blocks, in workgroups of 256 threads (a wide one over codes or bf16 rows has 512).
 inline int64_t mx_grid(int form, int64_t B, int64_t N, int64_t BM, int rows) {
-  if (form != kMxWide) return B * (form == kMxSplit ? (N + 15) / 16 : (N + 63) / 64);
+  if (form == kMxSplit) return B * ((N + 15) / 16) * mx_spans(BM, 16);
+  if (form != kMxWide) return B * ((N + 63) / 64) * (form == kMxNarrow ? 1 : mx_spans(BM, rows == kMxRowsCodes ? 64 : 32));
   const int TC = rows == kMxRowsF32 ? 32 : 128, ROWS = rows == kMxRowsF32 ? 64 : 256, merge = mx_merge(BM, TC);
-  const int64_t items = (N + ROWS - 1) / ROWS * ((BM + TC - 1) / TC);
+  const int64_t items = (N + ROWS - 1) / ROWS * mx_spans(BM, TC);
   return ((B + merge - 1) / merge * items + 7) / 8 * 8 * merge * (rows == kMxRowsF32 ? 1 : 2);
 }
 

@@ -8,8 +8,9 @@
 //
 // The division is by a power of two and the rounding the hardware's, so codes of given values are
 // exact. Those of the activation are the ones of its value in 64 bits: the product is formed in fp32,
-// within 2^-18.5 of itself, and lanes whose codes or scale would be others 2^-18 to either side form it
-// again in 64 bits (about one lane in a thousand).
+// within 2^-18.5 of itself and 2^-149 |up|, and lanes whose codes or scale would be others 2^-18 to either
+// side form it again in 64 bits (about one lane in a thousand), as do blocks with an up so large that the
+// second term counts: SiLU(gate) is then a number below fp32's normal ones, or 0 in fp32.
 //
 // Bound by bytes. A lane takes eight consecutive values (16 bytes of bf16), four lanes a block; a thread
 // has kVecs such vectors in flight. Kernel times (rocprofv3): 196608 rows of 2048 in fp32 (1.6 GB, to codes and
@@ -65,8 +66,8 @@ __device__ __forceinline__ uint32_t scale_of(uint32_t m) {
   return m >= 0x7f800000u ? kMxNaN : (uint32_t)max((int)(m >> 23) - 2, 0);
 }
 
-// v = SiLU(g) * u within 2^-18.5 of itself. Up to |g| = 32 the hardware's exp2 and reciprocal do: the exponent's argument
-// is rounded at 46 (2^-19.5 in all).
+// v = SiLU(g) * u within 2^-18.5 of itself, and what SiLU(g) loses below the normal numbers, up to 2^-149, times |u|. Up to
+// |g| = 32 the hardware's exp2 and reciprocal do: the exponent's argument is rounded at 46 (2^-19.5 in all).
 __device__ __forceinline__ void silu_mul8(const float (&g)[8], const float (&u)[8], float (&v)[8]) {
   float m = 0.f;
 #pragma unroll
@@ -79,6 +80,15 @@ __device__ __forceinline__ void silu_mul8(const float (&g)[8], const float (&u)[
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = silu(g[j]) * u[j];
   }
+}
+
+// Whether a lane's ups meet bits that SiLU(g) has lost: 2^-149 |u| is more than 2^-23 of the block's scale, 2^-21 of the
+// smallest value that is not 0. Gates of zero lose nothing.
+__device__ __forceinline__ bool silu_lost(const float (&g)[8], const float (&u)[8], float unit) {
+  bool lost = false;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) lost |= g[j] != 0.f && fabsf(u[j]) > unit * 0x1p126f;
+  return lost;
 }
 
 // SiLU(g) * u in 64 bits
@@ -162,8 +172,13 @@ __global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(MxArgs a) {
         hi[j] = v[j] * kMore;
       }
       const float mf = __uint_as_float(m), unit = mx_scale(s);
-      const bool other_scale = s != kMxNaN && scale_of(__float_as_uint(mf * kLess)) !=
-                                                  scale_of(__float_as_uint(mf * kMore));
+      bool other_scale = s != kMxNaN && scale_of(__float_as_uint(mf * kLess)) !=
+                                            scale_of(__float_as_uint(mf * kMore));
+      float um = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) um = fmaxf(um, fabsf(f[t][j]));
+      um = __uint_as_float(block_max(__float_as_uint(um)));
+      if (um > unit * 0x1p126f) other_scale |= block_max(silu_lost(g[t], f[t], unit)) != 0;
       w = mx_encode(lo, unit);  // (the same as v's, or formed again)
       if (other_scale || (s != kMxNaN && w != mx_encode(hi, unit)))
         codes64<BF16>(a, i, other_scale, w, s);

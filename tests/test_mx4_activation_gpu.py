@@ -70,3 +70,50 @@ def test_zeros_of_either_half(dtype):
     gate[5, 40], up[5, ::2] = -500.0, 0.0
     _, s = check(gate, up, dtype)
     assert not s[:5].any()
+
+
+def border_products(n, seed):
+    """Gates and ups in fp32 whose product in 64 bits is within 2^-20 of 2^128, on both sides of it, and some that fp32
+    rounds onto the other side."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    gate = (torch.rand(n, generator=g, device="cuda", dtype=torch.float64) * 20 + 1.5).float()
+    silu = gate.double() / (1 + torch.exp(-gate.double()))
+    steps = torch.randint(-8, 9, (n,), generator=g, device="cuda").double() * 2.0 ** -25
+    up = (2.0 ** 128 * (1 + steps) / silu).float()
+    return gate, up
+
+
+def test_products_on_either_side_of_fp32s_range():
+    """2^128 in 64 bits is the border of a NaN block, not what fp32 rounds the product to: a value below it has codes, at
+    the largest scale there is."""
+    gate, up = border_products(4096, 7)
+    value = torch.nn.functional.silu(gate.double()) * up.double()
+    below = (value < 2.0 ** 128)
+    rounds_up = below & (value >= 2.0 ** 128 * (1 - 2.0 ** -25))
+    assert int(below.sum()) > 1000 and int((~below).sum()) > 1000 and int(rounds_up.sum()) > 100
+    g, u = torch.full((4096, 64), 2.0, device="cuda"), uniform(4096, 64, -1e38, 1e38, 8)
+    places = torch.arange(4096, device="cuda") % 64
+    rows = torch.arange(4096, device="cuda")
+    g[rows, places], u[rows, places] = gate, up * torch.where(rows % 3 == 0, -1.0, 1.0)
+    _, s = check(g, u, torch.float32)
+    own = s[rows.cpu().numpy(), (places // 32).cpu().numpy()]
+    assert np.array_equal(own == 255, (~below).cpu().numpy()) and set(own.tolist()) == {252, 255}
+
+
+@BOTH
+def test_finite_inputs_past_fp32s_range_and_inputs_that_are_not_finite(dtype):
+    top, inf, nan = torch.finfo(dtype).max, float("inf"), float("nan")
+    gate, up = uniform(10, 64, 1.0, 3.0, 9), uniform(10, 64, -3.0, 3.0, 10)
+    gate[0, 3], up[0, 3] = top, top                # past the range, beside ordinary values
+    gate[1, 40], up[1, 40] = -top, top             # SiLU(-max) = -0
+    gate[2, 5], up[2, 5] = 1.0, top                # 0.73 max
+    gate[3, 5], up[3, 5] = 100.0, top
+    gate[4, 0], up[4, 0], up[4, 1] = 100.0, top, nan
+    gate[5, 0], up[5, 0], gate[5, 31] = 100.0, -top, -inf
+    gate[6, 0], up[6, 0] = inf, 0.0
+    gate[7, 0], up[7, 0] = 0.0, inf
+    gate[8], up[8] = top, top
+    gate[9], up[9] = -110.0, inf
+    _, s = check(gate, up, dtype)
+    assert (s == 255).tolist() == [[True, False], [False, False], [False, False], [True, False], [True, False], [True, False],
+                                   [True, False], [True, False], [True, True], [True, True]]

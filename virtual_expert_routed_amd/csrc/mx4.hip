@@ -10,7 +10,8 @@
 // exact. Those of the activation are the ones of its value in 64 bits: the product is formed in fp32,
 // within 2^-18.5 of itself and 2^-149 |up|, and lanes whose codes or scale would be others 2^-18 to either
 // side form it again in 64 bits (about one lane in a thousand), as do blocks with an up so large that the
-// second term counts: SiLU(gate) is then a number below fp32's normal ones, or 0 in fp32.
+// second term counts: SiLU(gate) is then a number below fp32's normal ones, or 0 in fp32. So do blocks whose
+// product leaves fp32's range, which decide in 64 bits whether a value is 2^128 or more.
 //
 // Bound by bytes. A lane takes eight consecutive values (16 bytes of bf16), four lanes a block; a thread
 // has kVecs such vectors in flight. Kernel times (rocprofv3): 196608 rows of 2048 in fp32 (1.6 GB, to codes and
@@ -91,6 +92,13 @@ __device__ __forceinline__ bool silu_lost(const float (&g)[8], const float (&u)[
   return lost;
 }
 
+__device__ __forceinline__ bool all_finite(const float (&g)[8], const float (&u)[8]) {
+  bool all = true;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) all &= fabsf(g[j]) < __builtin_inff() && fabsf(u[j]) < __builtin_inff();
+  return all;
+}
+
 // SiLU(g) * u in 64 bits
 __device__ __forceinline__ double silu_mul64(float g, float u) {
   return (double)g / (1.0 + exp(-(double)g)) * (double)u;
@@ -104,7 +112,8 @@ __device__ __forceinline__ uint32_t encode64(double v, int s) {
 }
 
 // The codes of vector i once more, from values in 64 bits, and the scale if `scale` (then in a block's four
-// lanes together). Reads its values again: kept, they would take registers from every lane.
+// lanes together; NaN, as the codes have to find it, if a value is 2^128 or more or none). Reads its values again: kept,
+// they would take registers from every lane.
 template <bool BF16>
 __device__ __forceinline__ void codes64(const MxArgs& a, int i, bool scale, uint32_t& w, uint32_t& s) {
   const int row = fdiv(i, a.f_vpr), k0 = (i - row * a.vpr) * 8;
@@ -119,10 +128,14 @@ __device__ __forceinline__ void codes64(const MxArgs& a, int i, bool scale, uint
   if (scale) {
     double d = 0.0;
 #pragma unroll 1
-    for (int j = 0; j < 8; ++j) d = fmax(d, fabs(value(j)));
+    for (int j = 0; j < 8; ++j) {
+      const double v = fabs(value(j));
+      d = v < 0x1p128 ? fmax(d, v) : 0x1p128;
+    }
     d = fmax(d, __shfl_xor(d, 1, 64));
     d = fmax(d, __shfl_xor(d, 2, 64));
-    s = (uint32_t)max(ilogb(d) + 125, 0);
+    s = d < 0x1p128 ? (uint32_t)max(ilogb(d) + 125, 0) : kMxNaN;
+    if (s == kMxNaN) return;
   }
   w = 0;
 #pragma unroll 1
@@ -172,8 +185,8 @@ __global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(MxArgs a) {
         hi[j] = v[j] * kMore;
       }
       const float mf = __uint_as_float(m), unit = mx_scale(s);
-      bool other_scale = s != kMxNaN && scale_of(__float_as_uint(mf * kLess)) !=
-                                            scale_of(__float_as_uint(mf * kMore));
+      bool other_scale = scale_of(__float_as_uint(mf * kLess)) != scale_of(__float_as_uint(mf * kMore)) ||
+                         (s == kMxNaN && block_max(!all_finite(g[t], f[t])) == 0);
       float um = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) um = fmaxf(um, fabsf(f[t][j]));

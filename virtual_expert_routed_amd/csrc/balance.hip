@@ -20,6 +20,7 @@
 // latency and launches throughout (0.2 MB); 16384 of 128 in bf16, softmax 6.9 + 7.0 and 9.0, of which their 4.2 MB read and
 // 8.4 moved take 0.9 and 1.7 at a copy's rate: issue of the exponentials, the reductions over lanes and waves, and the
 // second launch's wait for the first.
+#include "bf16_pair.h"
 #include "router_row.h"
 
 namespace mol {

@@ -24,12 +24,6 @@ __device__ __forceinline__ uint16_t f32_to_bf16_rne(float f) {
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
-// two floats to packed bf16 (to nearest even), one instruction
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-  typedef float f32x2 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2_t));
-}
-
 // acc + a.lo * b.lo + a.hi * b.hi for two packed bf16 pairs, in one v_dot2c_f32_bf16 (the
 // bf16 products are exact in fp32; no unpacking of either operand)
 __device__ __forceinline__ float dot2_bf16(uint32_t a, uint32_t b, float acc) {

@@ -37,6 +37,7 @@
 
 #include <type_traits>
 
+#include "bf16_pair.h"
 #include "mx4.h"
 
 namespace mol {

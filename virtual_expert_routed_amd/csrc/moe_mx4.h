@@ -467,6 +467,8 @@ __global__ void __launch_bounds__(256, 4) mx4_narrow_kernel(MxGemmArgs a) {
   }
 }
 
+constexpr int kMxChain = 64;  // a wave's lanes, a multiple of what an item takes together
+
 // Many columns an expert: an item is a span of TC columns of a block, or up to a.merge smaller blocks of one expert
 // that together have TC, and 16 FR NW weight rows. The items of the live blocks are a contiguous range for
 // each of the eight XCDs (workgroups go round them): neighbouring items share an expert's weights and a block's
@@ -491,22 +493,20 @@ __global__ void __launch_bounds__(64 * NW, 4) mx4_wide_kernel(MxGemmArgs a) {
   int width = a.BM;  // columns of the item's blocks
   if (a.merge > 1) {
     // A full block and the next one go together where they are one expert's: of a chain of such blocks every
-    // a.merge-th, from its first on, leads an item, and its followers leave theirs to it.
-    const int lane = threadIdx.x & 63;
+    // a.merge-th, from its first on, leads an item, and its followers leave theirs to it. Chains end before every
+    // block whose index is a multiple of kMxChain, so that one look of a wave finds a block's place in its own; it costs
+    // one item more for each such end. (Looking back to the first block of an expert grew with the square of its
+    // pairs: 65536 pairs of one, K 2048, N 1536, codes at blocks of 16, 32, 64 and 128 1724, 576, 265 and 155 us, so 208,
+    // 178, 164 and 156.)
+    const int lane = threadIdx.x & 63, at = blk & (kMxChain - 1);
     auto joins = [&](int i) __attribute__((always_inline)) {  // block i with block i + 1, 0 <= i < nb - 1
       return a.expert_ids[i] == er && a.expert_ids[i + 1] == er &&
              real_pair(a.sorted[(int64_t)i * a.BM + a.BM - 1], a.numel);
     };
-    int place = 0;
-    for (int at = blk; at > 0; at -= 64) {
-      const int i = at - 1 - lane;
-      const uint64_t ends = __builtin_amdgcn_ballot_w64(i < 0 || !joins(i));
-      place += ends ? __builtin_ctzll(ends) : 64;
-      if (ends) break;
-    }
-    if (place % a.merge) return;
+    const uint64_t begins = __builtin_amdgcn_ballot_w64(lane >= at || !joins(blk - 1 - lane));
+    if (__builtin_ctzll(begins) % a.merge) return;  // (lane 63 always votes: at < 64)
     const int i = blk + lane;
-    const uint64_t ends = __builtin_amdgcn_ballot_w64(lane >= a.merge - 1 || i >= nb - 1 || !joins(i));
+    const uint64_t ends = __builtin_amdgcn_ballot_w64(lane >= min(a.merge, kMxChain - at) - 1 || i >= nb - 1 || !joins(i));
     width += __builtin_ctzll(ends) * a.BM;  // (a.merge <= 8)
   }
   const int in_blk = item - group * a.items;

@@ -469,8 +469,8 @@ __global__ void __launch_bounds__(256, 4) mx4_narrow_kernel(MxGemmArgs a) {
 
 constexpr int kMxChain = 64;  // a wave's lanes, a multiple of what an item takes together
 
-// Many columns an expert: an item is a span of TC columns of a block, or up to a.merge smaller blocks of one expert
-// that together have TC, and 16 FR NW weight rows. The items of the live blocks are a contiguous range for
+// Many columns an expert: an item is a span of TC columns of a block, or (not of fp32 rows) up to a.merge smaller blocks of
+// one expert that together have TC, and 16 FR NW weight rows. The items of the live blocks are a contiguous range for
 // each of the eight XCDs (workgroups go round them): neighbouring items share an expert's weights and a block's
 // rows in its L2.
 template <int XF, bool OBF16, int TC, int FR, int SU, int NW>
@@ -483,7 +483,8 @@ __global__ void __launch_bounds__(64 * NW, 4) mx4_wide_kernel(MxGemmArgs a) {
   // second's: those that lead (below) lie together more often than not, and their workgroups on all compute units
   const int per_xcd = (int)((((int64_t)nb + a.merge - 1) / a.merge * a.items + 7) >> 3);
   const int local = (int)blockIdx.x >> 3;
-  const int turn = a.merge > 1 ? (int)((uint32_t)local / (uint32_t)max(per_xcd, 1)) : 0;
+  constexpr bool kMerges = XF != kMxRowsF32;
+  const int turn = kMerges && a.merge > 1 ? (int)((uint32_t)local / (uint32_t)max(per_xcd, 1)) : 0;
   const int item = ((int)blockIdx.x & 7) * per_xcd + local - turn * per_xcd;
   const int group = fdiv(item, a.f_items);
   const int blk = group * a.merge + turn;
@@ -491,7 +492,7 @@ __global__ void __launch_bounds__(64 * NW, 4) mx4_wide_kernel(MxGemmArgs a) {
   const int er = a.expert_ids[blk];
   if ((unsigned)er >= (unsigned)a.E) return;
   int width = a.BM;  // columns of the item's blocks
-  if (a.merge > 1) {
+  if (kMerges && a.merge > 1) {
     // A full block and the next one go together where they are one expert's: of a chain of such blocks every
     // a.merge-th, from its first on, leads an item, and its followers leave theirs to it. Chains end before every
     // block whose index is a multiple of kMxChain, so that one look of a wave finds a block's place in its own; it costs
@@ -539,7 +540,7 @@ hipError_t mx4_wide(MxGemmArgs a, hipStream_t st) {
   const int32_t tiles = (a.N + Sh::ROWS - 1) / Sh::ROWS;
   a.f_tiles = make_fastdiv((uint32_t)tiles);
   a.items = tiles * mx_spans(a.BM, TC);
-  a.merge = mx_merge(a.BM, TC);
+  a.merge = mx_merge(a.BM, XF);
   a.f_items = make_fastdiv((uint32_t)a.items);
   // (a range for each XCD, rounded up)
   const int64_t grid = ((int64_t)(a.max_blocks + a.merge - 1) / a.merge * a.items + 7) / 8 * 8 * a.merge;

@@ -316,10 +316,11 @@ enum { kMxSplit = 0, kMxNarrow = 1, kMxWide = 2, kMxSpread = 3 };
 inline int32_t mx_spans(int64_t BM, int TC) { return (int32_t)((BM + TC - 1) / TC); }
 // Blocks of BM pairs that hold some: at most one partly filled for each of E experts, beside the full ones.
 inline int64_t mx_filled(int64_t pairs, int64_t E, int64_t BM) { return pairs < E + pairs / BM ? pairs : E + pairs / BM; }
-// Blocks of BM pairs that an item of the wide form, of TC columns, takes together. (4096 tokens, top 8 of 128
+// Blocks of BM pairs that an item of the wide form takes together. (4096 tokens, top 8 of 128
 // experts, K 2048, N 1536, codes and bf16 rows: blocks of 64 one by one 155 and 277 us, together 119 and 235;
-// blocks of 16 447 and 596, together 135 and 253.)
-inline int mx_merge(int64_t BM, int TC) { return BM >= 16 && BM < TC && TC % BM == 0 ? (int)(TC / BM) : 1; }
+// blocks of 16 447 and 596, together 135 and 253. fp32 rows take theirs one by one: blocks of up to 32 are the narrow form's,
+// which is as fast: 32768 pairs of 128 experts at blocks of 16 and 32 1963 and 1827, at 64 and 128, wide, 1901 and 2023.)
+inline int mx_merge(int64_t BM, int rows) { return rows != kMxRowsF32 && BM >= 16 && BM < 128 && 128 % BM == 0 ? (int)(128 / BM) : 1; }
 // Wide where a pass of the narrow form would have many columns or read an expert's weights many times, and where
 // there are work items for the chip; of the narrow ones split for few items. Queued calls, us (K 2048, N 1536, experts
 // 128 top 8 unless said):
@@ -336,8 +337,8 @@ inline int mx_form(int64_t pairs, int64_t E, int64_t N, int64_t BM, int rows) {
   const int64_t filled = mx_filled(pairs, E, BM);
   if (rows == kMxRowsF32)
     return pairs > 32 * filled ? kMxWide : filled * ((N + 63) / 64) < 256 ? kMxSplit : kMxNarrow;
-  const int64_t spans = mx_merge(BM, 128) > 1 ? mx_filled(pairs, E, 128) : filled * ((BM + 127) / 128);
-  const int64_t taken = mx_merge(BM, 128) > 1 ? spans : filled;  // blocks, or runs of blocks taken together
+  const int64_t spans = mx_merge(BM, rows) > 1 ? mx_filled(pairs, E, 128) : filled * ((BM + 127) / 128);
+  const int64_t taken = mx_merge(BM, rows) > 1 ? spans : filled;  // blocks, or runs of blocks taken together
   const int64_t items = spans * ((N + 255) / 256), least = rows == kMxRowsCodes && filled >= 4 * spans ? 100 : 200;
   if ((pairs > 32 * taken || filled >= 2 * taken) && items >= least) return kMxWide;
   const int64_t full = mx_filled(pairs, E, BM < 64 ? BM : 64);  // passes of a full block's size
@@ -350,7 +351,7 @@ inline int mx_form(int64_t pairs, int64_t E, int64_t N, int64_t BM, int rows) {
 inline int64_t mx_grid(int form, int64_t B, int64_t N, int64_t BM, int rows) {
   if (form == kMxSplit) return B * ((N + 15) / 16) * mx_spans(BM, 16);
   if (form != kMxWide) return B * ((N + 63) / 64) * (form == kMxNarrow ? 1 : mx_spans(BM, rows == kMxRowsCodes ? 64 : 32));
-  const int TC = rows == kMxRowsF32 ? 32 : 128, ROWS = rows == kMxRowsF32 ? 64 : 256, merge = mx_merge(BM, TC);
+  const int TC = rows == kMxRowsF32 ? 32 : 128, ROWS = rows == kMxRowsF32 ? 64 : 256, merge = mx_merge(BM, rows);
   const int64_t items = (N + ROWS - 1) / ROWS * mx_spans(BM, TC);
   return ((B + merge - 1) / merge * items + 7) / 8 * 8 * merge * (rows == kMxRowsF32 ? 1 : 2);
 }

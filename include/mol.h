@@ -479,7 +479,9 @@ MOL_API mol_status mol_moe_gemm_q4(int32_t dtype, const void *xin, int64_t ld_x,
  * mol_moe_gemm_mx4 - mol_moe_gemm's base product over such weights:
  *   out[p, n] = round( sum_k W[t, n, k] * xin[p / row_div, k] )
  * for every pair p with a local base expert t in [0, E); other rows are untouched. Products and sums
- * are fp32, rounded once. num_experts = 1 and ids of zero give the product with a single matrix.
+ * are fp32, rounded once. num_experts = 1 and ids of zero give the product with a single matrix. Beside
+ * bf16 or fp32 rows a weight is its value in fp32: infinite from 2^128 on (some codes at s = 253 and 254);
+ * beside rows of codes any two scales multiply as powers of two.
  *   dtype         MOL_F32 or MOL_BF16 of out, and of xin without x_scales
  *   xin, x_scales x_scales NULL: rows of ld_x elements (dtype). Else rows of codes, ld_x / 2 bytes apart
  *                 (ld_x a multiple of 32), with scales ld_x / 32 bytes apart

@@ -5,9 +5,9 @@
 // base expert each).
 //
 // Codes times codes go to the scaled matrix-core product (16 x 16 x 128, both operands 4 bits, a scale
-// byte a lane); beside bf16 and fp32 rows the weights are widened to that type in registers, which is
-// exact, scale included. Products and sums are fp32, so infinities and NaN of x reach exactly the
-// sums that the formula has them in.
+// byte a lane); beside bf16 and fp32 rows the weights are widened to that type in registers, scale
+// included, which is exact below 2^128 and infinite from there on (codes at s = 253 and 254). Products and
+// sums are fp32, so infinities and NaN of x reach exactly the sums that the formula has them in.
 //
 // A work item is a span of columns of a routing block (of the wide, spread and split forms; all of the block's of
 // the narrow one) and NW times 16 FR weight rows; wave w has 16 FR of them as the A operand, straight from memory into

@@ -20,7 +20,7 @@ __device__ __forceinline__ float mx_scale(uint32_t s) {
 }
 
 // Eight codes of a dword times a scale: bf16 (exact: two bits of mantissa, and bf16's subnormals reach
-// 2^-133) or fp32. A NaN scale makes them NaN.
+// 2^-133) or fp32; infinite from 2^128 on. A NaN scale makes them NaN.
 __device__ __forceinline__ uint4 mx_bf16(uint32_t w, float scale) {
   return make_uint4(
       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0)),

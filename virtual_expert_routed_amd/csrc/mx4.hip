@@ -185,13 +185,14 @@ __global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(MxArgs a) {
         hi[j] = v[j] * kMore;
       }
       const float mf = __uint_as_float(m), unit = mx_scale(s);
-      bool other_scale = scale_of(__float_as_uint(mf * kLess)) != scale_of(__float_as_uint(mf * kMore)) ||
-                         (s == kMxNaN && block_max(!all_finite(g[t], f[t])) == 0);
+      bool other_scale = scale_of(__float_as_uint(mf * kLess)) != scale_of(__float_as_uint(mf * kMore));
       float um = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) um = fmaxf(um, fabsf(f[t][j]));
-      um = __uint_as_float(block_max(__float_as_uint(um)));
-      if (um > unit * 0x1p126f) other_scale |= block_max(silu_lost(g[t], f[t], unit)) != 0;
+      if (__builtin_amdgcn_ballot_w64(!(um <= unit * 0x1p126f))) {  // rare, and where the scale is NaN
+        if (s == kMxNaN) other_scale |= block_max(!all_finite(g[t], f[t])) == 0;
+        else other_scale |= block_max(silu_lost(g[t], f[t], unit)) != 0;
+      }
       w = mx_encode(lo, unit);  // (the same as v's, or formed again)
       if (other_scale || (s != kMxNaN && w != mx_encode(hi, unit)))
         codes64<BF16>(a, i, other_scale, w, s);

@@ -467,8 +467,8 @@ MOL_API mol_status mol_moe_gemm_q4(int32_t dtype, const void *xin, int64_t ld_x,
  *   the even code, beyond 6 to 6. A block with a NaN or an infinity gets s = 255 and codes of zero.
  *   activation    MOL_ACT_NONE: x [rows, K], the values;  MOL_ACT_SILU_MUL: x [rows, 2 K], gate
  *                 columns first, value k = SiLU(x[k]) * x[K + k] (the rows of a layer's gate_up product,
- *                 for its down product). Its codes are those of the value in 64 bits; a value beyond
- *                 fp32's range counts as infinite.
+ *                 for its down product). Its codes are those of the value in 64 bits; a value of 2^128 or
+ *                 more counts as infinite.
  *   x             rows of ld_x elements (dtype), aligned to its element
  *   q             uint8 [rows, K / 2] out, 16-byte aligned;  scales  uint8 [rows, K / 32] out
  * mol_mx4_dequantize - the values of codes and scales, x [rows, ld_x] (dtype) out: exact in both dtypes
@@ -488,9 +488,10 @@ MOL_API mol_status mol_moe_gemm_q4(int32_t dtype, const void *xin, int64_t ld_x,
  *   W             uint8 [E, N, K / 2], 16-byte aligned;  scales uint8 [E, N, K / 32]
  *   others        as for mol_moe_gemm (rows of xin on 16-byte boundaries)
  * For decode and prefill batches; blocks of any block_m are taken. From some thousand tokens on blocks of 128
- * pairs run fastest; of 64, 32 or 16 of one expert in a row, full but for the last, are taken together.
- * Errors: MOL_E_ARG (K not a multiple of 32), MOL_E_LIMIT (one expert's weights 2 GiB or more, 2^24
- * work items or more), others as for mol_moe_gemm.
+ * pairs run fastest; of 64, 32 or 16 of one expert in a row, full but for the last, are taken together (not beside
+ * fp32 rows).
+ * Errors: MOL_E_ARG (K not a multiple of 32), MOL_E_LIMIT (one expert's weights 2 GiB or more; 2^32 threads
+ * or more, which are 2^24 work items, 2^23 of many pairs of codes or bf16 rows), others as for mol_moe_gemm.
  * ------------------------------------------------------------------------------- */
 enum { MOL_ACT_NONE = 0, MOL_ACT_SILU_MUL = 1 };
 

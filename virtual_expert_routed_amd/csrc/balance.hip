@@ -16,8 +16,8 @@
 // workgroup to finish forms the loss. Few tokens take one workgroup and one launch. No sum depends
 // on the order in which anything arrives: results are the same bit for bit.
 //
-// Kernel times (rocprofv3): 138 tokens of 160 experts in fp32, sigmoid 5.2 + 5.1 us forward and 4.6 the gradient,
-// latency and launches throughout (0.2 MB); 16384 of 128 in bf16, softmax 6.9 + 7.0 and 9.0, of which their 4.2 MB read and
+// Kernel times (rocprofv3): 138 tokens of 160 experts in fp32, sigmoid 5.2 + 5.5 us forward and 4.7 the gradient,
+// latency and launches throughout (0.2 MB); 16384 of 128 in bf16, softmax 6.8 + 7.5 and 9.1, of which their 4.2 MB read and
 // 8.4 moved take 0.9 and 1.7 at a copy's rate: issue of the exponentials, the reductions over lanes and waves, and the
 // second launch's wait for the first.
 #include "bf16_pair.h"
@@ -28,8 +28,8 @@ namespace {
 
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
-// exp(x) for x <= 0 (0 below -200) within 2^-22 of itself: the hardware's exp2 of x log2(e), corrected by what that
-// product rounds away.
+// exp(x) for x <= 0 within 2^-22 of itself down to the smallest normal number (x = -87.3), within 2^-126 below it: the
+// hardware's exp2 of x log2(e), corrected by what that product rounds away.
 __device__ __forceinline__ float exp_neg(float x) {
   constexpr float kL = 1.44269502f, kLlo = 1.92596303e-8f, kLn2 = 0.693147182f;
   x = fmaxf(x, -200.f);

@@ -20,15 +20,19 @@
 // of the L1 as the codes.
 //
 // Kernel times (rocprofv3) and what bounds them, K 2048 and N 1536 (gate_up) or K 768 and N 2048 (down), top 8 of
-// 128 experts, a copy's 4.94 TB/s:
-//   1 token, bf16 rows, gate_up               8.4 us  13.4 MB in 2.7 us: launch, routing, one latency after another
-//   23 tokens, codes, down                   17.4 us  83 MB of weights, 97 % of the copy's rate
-//   128 tokens, zipf, bf16 rows, gate_up     42.9 us  200 MB, 95 %
-//   4096 tokens, codes, gate_up             112 us    1.8 PFLOP/s: look-ups of the L1 for W (the bytes alone: 64)
-//   4096 tokens, bf16 rows, down            131 us    0.79 PFLOP/s of bf16, 71 % of the library's square product
-//   16384 tokens, codes, down               275 us    1.5 PFLOP/s; a third of it the stores of 537 MB
-// W as the A operand costs 64 lines of the L1 a load (16 rows of 64 bytes apart). Both operands through LDS, three
-// stages deep, took as long (129 and 308 us for 4096 gate_up and 16384 down where this took 130 and 307),
+// 128 experts, a copy's 4.94 TB/s. First over one set of buffers, which the last-level cache holds a part of, then over three in
+// turn:
+//   1 token, bf16 rows, gate_up               8.7 and 9.3 us  13.4 MB in 2.7: launch, routing, one latency after another
+//   23 tokens, codes, down                   18 us     83 MB of weights, 94 % of the copy's rate
+//   128 tokens, zipf, bf16 rows, gate_up     47 and 56 us  200 MB, 86 and 72 %
+//   4096 tokens, codes, gate_up             114 and 134 us  1.8 PFLOP/s (the bytes alone: 64)
+//   4096 tokens, bf16 rows, down            132 and 155 us  0.78 PFLOP/s of bf16, 70 % of the library's square product
+//   16384 tokens, codes, down               272 and 340 us  1.5 PFLOP/s; a third of it the stores of 537 MB
+//   4096 tokens, fp32 rows, gate_up        1900 us    108 TFLOP/s, 71 % of the library's square product
+// Counters of one launch of the two wide ones over codes: look-ups of the L1 in 65 and 73 % of its cycles, the matrix cores
+// busy in 20 and 19 %, waves waiting half their time. W as the A operand costs 64 look-ups a load (16 rows, four
+// 16-byte places of each). Both operands through LDS, three stages deep, took as long (129 and 308 us for 4096
+// gate_up and 16384 down where this took 130 and 307),
 // so the form with fewer barriers stayed; workgroups that stay and take item after item 155 and 363; 256 columns
 // an item 138 and 306 against 113 and 275.
 //

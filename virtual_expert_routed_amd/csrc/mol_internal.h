@@ -333,6 +333,13 @@ inline int mx_merge(int64_t BM, int rows) { return rows != kMxRowsF32 && BM >= 1
 //     experts) 8.7 and 9.5
 //   narrow and split, fp32 rows: one token of one expert (32 items) 17.3 and 10.5, of 8 of 128 experts (192) 19.3 and
 //     19.0, 256 items 12.6 and 13.4.  (bf16 rows, split against narrow: one token of one expert 11.1 and 9.5.)
+//   narrow and wide, fp32 rows: 1024 pairs of 8 experts at blocks of 64 and 128 99 and 87, 184 and 108; 4096 of one at 64 and
+//     128 245 and 234, 252 and 230, at 32 243 and 239; 32768 of 128 experts 1852 and 1904, 1913 and 2028, at 32 1826 and 1832
+// K is on neither side of the rule. At K 768 and 6144 (one expert of N 2048 and 64 to 4096 pairs; 128 experts, 23 to 2048
+// tokens; blocks of 16, 64 and 128; codes and bf16 rows) the form taken is within 10 % of the fastest of narrow, spread and wide, but
+// for one expert at blocks of 16: 1024 pairs of codes narrow 14.5 and wide 11.9 at K 768, 57 and 49 at 6144, 2048 bf16
+// pairs 26.7 and 20.9 at K 768, 148 and 130 at 6144; 512 tokens of bf16 rows over 128 experts, K 768, blocks of 128, 38 and
+// 34; 768 tokens of codes at blocks of 64 wide 34 and narrow 30 at K 768, 51 and 45 at 2048.
 inline int mx_form(int64_t pairs, int64_t E, int64_t N, int64_t BM, int rows) {
   const int64_t filled = mx_filled(pairs, E, BM);
   if (rows == kMxRowsF32)

@@ -15,9 +15,9 @@
 //
 // Bound by bytes. A lane takes eight consecutive values (16 bytes of bf16), four lanes a block; a thread
 // has kVecs such vectors in flight. Kernel times (rocprofv3): 196608 rows of 2048 in fp32 (1.6 GB, to codes and
-// back) 339 and 328 us, 5.4 and 5.6 TB/s; the activation of 32768 bf16 rows of 2 x 768 28 us (4.0 TB/s: eight
-// exponentials, reciprocals and two encodings a lane beside the bytes), back to bf16 10 us (6.3 TB/s); 23 rows of
-// 2048 3 us each way, a launch.
+// back) 340 and 328 us, 5.4 and 5.6 TB/s; the activation of 32768 bf16 rows of 2 x 768 27 us over the same rows again
+// (4.2 TB/s: eight exponentials, reciprocals and two encodings a lane beside the bytes) and 33 us over three sets in turn,
+// which the last-level cache does not hold; back to bf16 10 us (6.3 TB/s); 23 rows of 2048 3 us each way, a launch.
 #include "mx4.h"
 #include "skinny.h"
 

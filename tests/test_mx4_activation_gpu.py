@@ -117,3 +117,28 @@ def test_finite_inputs_past_fp32s_range_and_inputs_that_are_not_finite(dtype):
     _, s = check(gate, up, dtype)
     assert (s == 255).tolist() == [[True, False], [False, False], [False, False], [True, False], [True, False], [True, False],
                                    [True, False], [True, False], [True, True], [True, True]]
+
+
+@BOTH
+@pytest.mark.parametrize("seed", [11, 12, 13])
+def test_blocks_of_every_size_of_gates_and_ups(dtype, seed):
+    """Gates of a block next to zero, ordinary, far below or far above it, ups of any exponent, both with a spread of their
+    own; some zeros of either."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rows, blocks = 1500, 4
+
+    def rand(*shape):
+        return torch.rand(*shape, generator=g, device="cuda", dtype=torch.float64)
+
+    sign = torch.where(rand(rows, blocks, 32) < 0.5, -1.0, 1.0)
+    kind = torch.randint(0, 5, (rows, blocks, 1), generator=g, device="cuda")
+    near = torch.exp2(-150 + 60 * rand(rows, blocks, 1) + 6 * rand(rows, blocks, 32)) * sign
+    below = -80 - 170 * rand(rows, blocks, 1) - 8 * rand(rows, blocks, 32)
+    far = torch.exp2(5 + 100 * rand(rows, blocks, 1) + 2 * rand(rows, blocks, 32)) * sign
+    ordinary = 6 * rand(rows, blocks, 32) - 3
+    gate = torch.where(kind == 0, near, torch.where(kind == 1, below, torch.where(kind == 2, far, ordinary)))
+    up = torch.exp2(-145 + 262 * rand(rows, blocks, 1) + 10 * rand(rows, blocks, 32)) * torch.where(rand(rows, blocks, 32) < 0.5, -1.0, 1.0)
+    gate[rand(rows, blocks, 32) < 0.02] = 0.0
+    up[rand(rows, blocks, 32) < 0.02] = 0.0
+    _, s = check(gate.view(rows, 128).float(), up.view(rows, 128).float(), dtype)
+    assert 0 < (s == 255).sum() < s.size // 4 and len(np.unique(s)) > 200
